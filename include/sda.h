@@ -431,6 +431,56 @@ sda_status sda_qk_norm_rope_swa_store_fp8(const void* q, const void* kv, const v
                                           void* kv_fp8, float* kv_scale, int32_t* status,
                                           void* stream);
 
+/*
+ * Attention of a chunk of new tokens of every sequence over its cached
+ * positions, found through a block table (prefill behind a cached prefix,
+ * drafted tokens, or one new token per sequence).
+ *
+ * Sequence b has m_b = q_indptr[b + 1] - q_indptr[b] new tokens and n_b =
+ * kv_len[b] cached positions, the new tokens' own rows being the last m_b of
+ * them (stored before this call).  Position j's pool row, key and value of
+ * every head, is base + block_table[b][j / k_per_block] * k_per_block +
+ * j % k_per_block (base: the first pool row of the block region, swa_pages of
+ * the other entry points; k_per_block = 1: a table of single slots).  Token i
+ * stands at position p = n_b - m_b + i and sees every j <= p with
+ *   window == 0  or  j > p - window  or  j < first
+ * (a sliding window of `window` positions, itself included, and `first`
+ * first positions that stay visible).  Per row (token, head h), over the
+ * positions it sees:
+ *   x_j = softmax_scale <q, kv_j>,  lse = log(e^attn_sink[h] + sum_j e^x_j)
+ *   out = sum_j e^(x_j - lse) kv_j
+ * A row that sees nothing (n_b < m_b, or n_b = 0) gets out = +0 and lse =
+ * attn_sink[h]; with attn_sink[h] = +inf out = +0 and lse = +inf.  Infinities
+ * and NaN in positions that a row does not see leave the row as it is.
+ *
+ * Arguments (device pointers):
+ *   q           [T, H, D] bf16, 16-byte aligned; D in {64, 128, 256, 512},
+ *               1 <= H <= 256, T * H < 2^31 - 64
+ *   unified_kv  [total_pages, D] bf16, 16-byte aligned
+ *   block_table [B, max_blocks] int32: entries of blocks behind
+ *               kv_len are never read
+ *   q_indptr    [B + 1] int32, non-decreasing inside [0, T]; rows of q, out
+ *               and lse outside [q_indptr[0], q_indptr[B]) are not written
+ *   kv_len      [B] int32 in [0, max_blocks * k_per_block]
+ *   attn_sink   [H] fp32 sink logits (-inf: no sink)
+ *   out         [T, H, D] bf16, 16-byte aligned, overlapping neither q nor the
+ *               pool; lse [T, H] fp32
+ * The device error word (sda_decode_error_flag on the workspace): 2 = q_indptr
+ * or kv_len broke the contract (nothing computed); 3 = a table entry pointed
+ * outside the pool (that row counts as zeros, outputs that see it are
+ * unspecified); 1 = a pipeline wait timed out.  Three launches, no
+ * allocation, graph-capturable; calls that may run at the same time need a
+ * workspace each.
+ */
+sda_status sda_chunk_attention_workspace_size(int B, int T, int H, int D, size_t* bytes);
+
+sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t total_pages,
+                               const int32_t* block_table, int max_blocks, int k_per_block,
+                               int64_t base, const int32_t* q_indptr, const int32_t* kv_len,
+                               const float* attn_sink, float softmax_scale, int window, int first,
+                               int B, int T, int H, int D, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,11 +19,13 @@ import ctypes
 import torch
 
 from . import _lib
+from .paged import chunk_attention, chunk_attention_workspace_size
 
 __all__ = ["decode", "workspace_size", "build_indices", "validate_indices", "decode_error_flag",
            "decode_kernel", "decode_fp8", "workspace_size_fp8", "qk_norm_rope_swa_store", "topk_slots", "build_decode",
            "build_decode_host", "build_decode_host_workspace_size",
-           "decode_host", "set_timing_events", "decode_noalloc", "library_path"]
+           "decode_host", "set_timing_events", "decode_noalloc", "library_path",
+           "chunk_attention", "chunk_attention_workspace_size"]
 
 library_path = _lib.LIB_PATH
 

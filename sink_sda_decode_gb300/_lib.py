@@ -60,6 +60,11 @@ SIGNATURES = {
     "sda_qk_norm_rope_swa_store_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32,
                                               _i32, _i32, _i32, _f32, _i32, _i64, _i64, _vp, _vp,
                                               _vp, _vp, _vp]),
+    "sda_chunk_attention_workspace_size": (_i32, [_i32, _i32, _i32, _i32,
+                                                  ctypes.POINTER(ctypes.c_size_t)]),
+    "sda_chunk_attention": (_i32, [_vp, _vp, _i64, _vp, _i32, _i32, _i64, _vp, _vp, _vp, _f32, _i32,
+                                   _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_size_t,
+                                   _vp]),
 }
 
 

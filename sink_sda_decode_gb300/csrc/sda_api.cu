@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "sda_chunk.cuh"
 #include "sda_copy.cuh"
 #include "sda_internal.cuh"
 #include "sda_scatter.cuh"
@@ -28,11 +29,6 @@ constexpr unsigned long long kDefaultWaitTimeoutNs = 2000000000ull;
 thread_local cudaEvent_t g_ev_before = nullptr;
 thread_local cudaEvent_t g_ev_after = nullptr;
 
-void note_cuda_error(cudaError_t e, const char* where) {
-  std::snprintf(g_last_error, sizeof g_last_error, "%s: %s (%s)", where, cudaGetErrorName(e),
-                cudaGetErrorString(e));
-}
-
 constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
@@ -43,6 +39,11 @@ struct DeviceInfo {
 DeviceInfo g_dev[kMaxDevices];
 
 }  // namespace
+
+void note_cuda_error(cudaError_t e, const char* where) {
+  std::snprintf(g_last_error, sizeof g_last_error, "%s: %s (%s)", where, cudaGetErrorName(e),
+                cudaGetErrorString(e));
+}
 
 // SM count of the current device, queried once per device; also sets the
 // tensor-core kernels' shared-memory attributes on that device.
@@ -56,6 +57,7 @@ cudaError_t device_caps(DeviceCaps* caps) {
     d.err = cudaDeviceGetAttribute(&d.caps.num_sms, cudaDevAttrMultiProcessorCount, dev);
     for (int nh : {16, 32, 64})
       if (d.err == cudaSuccess) d.err = umma_prepare(nh);
+    if (d.err == cudaSuccess) d.err = chunk_prepare();
   });
   *caps = d.caps;
   return d.err;
@@ -929,6 +931,88 @@ sda_status sda_qk_norm_rope_swa_store_fp8(const void* q, const void* kv, const v
                       state_slot, N, H, D, rope_dim, eps, win, swa_pages, total_pages, q_out,
                       nullptr, static_cast<uint8_t*>(kv_fp8), kv_scale, status, stream,
                       "sda_qk_norm_rope_swa_store_fp8");
+}
+
+// The checks that the paged-cache operators share; what the kernels trust.
+static sda_status chunk_geometry_ok(const ChunkGeom& g) {
+  if (g.B < 0 || g.T < 0 || g.k_per_block <= 0 || g.max_blocks < 0 || g.window < 0 || g.first < 0)
+    return SDA_ERR_INVALID_ARG;
+  if (g.total_pages <= 0 || g.total_pages > 0x7fffffffll || g.base < 0 || g.base > g.total_pages)
+    return SDA_ERR_INVALID_ARG;
+  if (!shape_supported(g.H, g.D)) return SDA_ERR_UNSUPPORTED;
+  // rows are counted in 32 bits, 64 of them past the end being addressable
+  if (static_cast<int64_t>(g.T) * g.H > 0x7fffffffll - 64 || g.B > (1 << 24))
+    return SDA_ERR_INVALID_ARG;
+  return SDA_OK;
+}
+
+static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+sda_status sda_chunk_attention_workspace_size(int B, int T, int H, int D, size_t* bytes) {
+  if (!bytes) return SDA_ERR_INVALID_ARG;
+  ChunkGeom g = {};
+  g.B = B, g.T = T, g.H = H, g.D = D, g.k_per_block = 1, g.total_pages = 1;
+  const sda_status s = chunk_geometry_ok(g);
+  if (s != SDA_OK) return s;
+  DeviceCaps caps;
+  const cudaError_t e = device_caps(&caps);
+  if (e != cudaSuccess) {
+    note_cuda_error(e, "sda_chunk_attention_workspace_size");
+    return SDA_ERR_CUDA;
+  }
+  *bytes = chunk_layout(B, T, H, D, caps.num_sms).total;
+  return SDA_OK;
+}
+
+sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t total_pages,
+                               const int32_t* block_table, int max_blocks, int k_per_block,
+                               int64_t base, const int32_t* q_indptr, const int32_t* kv_len,
+                               const float* attn_sink, float softmax_scale, int window, int first,
+                               int B, int T, int H, int D, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const ChunkGeom g{q_indptr, kv_len,      block_table, B,      T,    H, D, max_blocks,
+                    k_per_block, base, total_pages, window, first};
+  const sda_status s = chunk_geometry_ok(g);
+  if (s != SDA_OK) return s;
+  if (B == 0 || T == 0) return SDA_OK;
+  if (!q || !unified_kv || !q_indptr || !kv_len || !attn_sink || !out || !lse || !workspace)
+    return SDA_ERR_INVALID_ARG;
+  if (max_blocks > 0 && !block_table) return SDA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, unified_kv, static_cast<const void*>(out)})
+    if (!aligned(ptr, 16)) return SDA_ERR_INVALID_ARG;
+  for (const void* ptr : {static_cast<const void*>(q_indptr), static_cast<const void*>(kv_len),
+                          static_cast<const void*>(block_table), static_cast<const void*>(attn_sink),
+                          static_cast<const void*>(lse)})
+    if (!aligned(ptr, 4)) return SDA_ERR_INVALID_ARG;
+  // a unit's out is written while other units still read q and the pool
+  const size_t rows = static_cast<size_t>(T) * H;
+  if (overlaps(q, rows * D * 2, out, rows * D * 2) ||
+      overlaps(unified_kv, static_cast<size_t>(total_pages) * D * 2, out, rows * D * 2))
+    return SDA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return SDA_ERR_WORKSPACE;
+  DeviceCaps caps;
+  cudaError_t e = device_caps(&caps);
+  if (e != cudaSuccess) {
+    note_cuda_error(e, "sda_chunk_attention");
+    return SDA_ERR_CUDA;
+  }
+  const ChunkLayout L = chunk_layout(B, T, H, D, caps.num_sms);
+  if (workspace_bytes < L.total) return SDA_ERR_WORKSPACE;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  e = launch_chunk_plan(g, L, workspace, st);
+  if (e == cudaSuccess && g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_before, st);
+  if (e == cudaSuccess)
+    e = launch_chunk_attn(q, unified_kv, g, attn_sink, softmax_scale, out, lse, L, workspace, st);
+  if (e == cudaSuccess && g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_after, st);
+  if (e == cudaSuccess) e = launch_chunk_combine(attn_sink, g, out, lse, L, workspace, st);
+  if (e != cudaSuccess) {
+    note_cuda_error(e, "sda_chunk_attention");
+    return SDA_ERR_CUDA;
+  }
+  return SDA_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,85 @@
+// sda_chunk.cuh -- geometry shared by the paged-cache operators: which cached
+// positions a token of a chunk sees, the work units of the chunk attention,
+// and the launchers.
+//
+// Sequence b has m_b = q_indptr[b + 1] - q_indptr[b] new tokens and
+// n_b = kv_len[b] cached positions, of which the new tokens' own rows are the
+// last m_b.  Its token i stands at position p = n_b - m_b + i and sees the
+// positions j <= p with (window == 0 or j > p - window or j < first).
+// Position j's row is pool row base + block_table[b][j / K] * K + j % K.
+#pragma once
+
+#include <cstddef>
+
+#include "sda_internal.cuh"
+
+namespace sda {
+
+struct ChunkGeom {
+  const int32_t* q_indptr;     // [B + 1]
+  const int32_t* kv_len;       // [B]
+  const int32_t* block_table;  // [B, max_blocks]
+  int B, T, H, D;
+  int max_blocks, k_per_block;
+  int64_t base, total_pages;
+  int window, first;
+};
+
+// All heads share the cached rows, so the (token, head) rows of a sequence
+// are one matrix of m_b * H rows of q, and a work unit is up to R consecutive
+// rows of it: one tile of queries, whatever H.
+struct alignas(16) ChunkUnit {
+  int row0;     // first row of q (token * H + head)
+  int nrows;    // rows of this unit, 1..R
+  int b;        // sequence
+  int pos0;     // position of row 0's token (negative if n_b < m_b)
+  int h0;       // head of row 0; row i: token pos0 + (h0 + i) / H, head (h0 + i) % H
+  int lo;       // positions below lo are visible only if they are below `first`
+  int hi;       // positions from hi on are visible to no row
+  int nf;       // KV tiles of the first positions (those below lo's tile)
+  int ntiles;   // KV tiles of 64 positions: tiles 0..nf-1, then from lo / 64 on (>= 1)
+  int cum;      // KV tiles of all earlier units
+  int pad0, pad1;
+};
+static_assert(sizeof(ChunkUnit) == 48, "three 16-byte words");
+
+constexpr int kChunkTile = 64;  // positions per KV tile
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The position that logical tile i of a unit starts at.
+__host__ __device__ inline int chunk_tile_start(int i, int nf, int lo) {
+  return (i < nf ? i : lo / kChunkTile + i - nf) * kChunkTile;
+}
+
+// Header of the workspace.
+struct ChunkHeader {
+  int n_units;
+  int n_tiles;  // KV tiles of all units
+  int per;      // tiles per CTA: CTA k owns tiles [k * per, min((k + 1) * per, n_tiles))
+  int ctas;     // CTAs with tiles
+  int error;    // 1 = a wait timed out, 2 = bad lengths (nothing computed), 3 = bad table entry
+  int pad[59];
+};
+static_assert(sizeof(ChunkHeader) == 256, "header is 256 bytes");
+static_assert(offsetof(ChunkHeader, error) == offsetof(WsHeader, error),
+              "sda_decode_error_flag reads either header");
+
+struct ChunkLayout {
+  size_t units_off, seq_off, cta_off, ml_off, o_off, total;
+  int u_max, grid, R;
+};
+// The layout for B sequences, T tokens: R rows per unit is a function of them.
+ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms);
+
+cudaError_t chunk_prepare();  // one-time kernel attributes on the current device
+cudaError_t launch_chunk_plan(const ChunkGeom& g, const ChunkLayout& L, void* ws, cudaStream_t st);
+cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
+                              const float* attn_sink, float scale, void* out, float* lse,
+                              const ChunkLayout& L, void* ws, cudaStream_t st);
+cudaError_t launch_chunk_combine(const float* attn_sink, const ChunkGeom& g, void* out, float* lse,
+                                 const ChunkLayout& L, void* ws, cudaStream_t st);
+
+// sda_api.cu: the text that sda_last_cuda_error returns.
+void note_cuda_error(cudaError_t e, const char* where);
+
+}  // namespace sda

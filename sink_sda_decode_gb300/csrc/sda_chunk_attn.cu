@@ -1,0 +1,798 @@
+// sda_chunk_attn.cu -- attention of a chunk of new tokens of every sequence
+// over its cached positions, found through a block table (tcgen05 / TMEM).
+//
+// For every row (token i of sequence b, head h), over the positions j the
+// token sees (sda_chunk.cuh):
+//   x_j = scale <q, kv_j>,  lse = log(e^sink_h + sum_j e^(x_j)),
+//   out = sum_j e^(x_j - lse) kv_j
+// as an online softmax in the log2 domain.  A cached row is key and value of
+// every head, so R consecutive (token, head) rows of q form one tile of
+// queries whatever H is, and each KV tile of 64 positions is read once per
+// tile of queries.
+//
+// One persistent CTA per SM owns a contiguous range of KV tiles (the plan,
+// sda_chunk_plan.cu).  Roles:
+//   warps 0..7    softmax and epilogue; thread 0 issues the PV MMAs
+//   warps 8..23   KV rows: each warp copies 4 rows of every tile with 16-byte
+//                 cp.async into a 128-byte-swizzled stage
+//   warps 24, 26  QK MMAs, one half of D each (D <= 128: warp 24 alone); warp
+//                 24 loads q by TMA
+// S = Q K^T (M = 64 rows, N = 64 positions) and O^T += V^T P^T (M = 128 of D,
+// N = R rows, K = 64 positions) read the same shared tile, K-major as K and
+// MN-major as V.
+#include <cuda_bf16.h>
+
+#include "sda_chunk.cuh"
+#include "sda_pipe.cuh"
+
+namespace sda {
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = kChunkTile;          // 64 positions per KV tile
+constexpr int kPanel = kTile * 128;        // bytes of one 64-column panel of a KV tile
+constexpr int kSmWarps = 8;
+constexpr int kSmThreads = kSmWarps * 32;
+constexpr int kLoadWarp0 = 8;
+constexpr int kLoadWarps = 16;
+constexpr int kMmaWarp = 24;
+constexpr int kMmaWarpB = 26;
+constexpr int kThreads = 896;
+// Registers: the launch gives 72 a thread (65536 / 896, rounded down to 8);
+// the softmax warps grow, the others shrink.
+constexpr int kLaunchRegs = 72;
+constexpr int kSmRegs = 104, kLoadRegs = 56, kMmaRegs = 56;
+static_assert(kSmThreads * kSmRegs + kLoadWarps * 32 * kLoadRegs + 128 * kMmaRegs <=
+                  kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr int kMaxStages = 5;
+constexpr float kHeadroom = 8.0f;  // log2: the running reference is raised when a score exceeds it by this
+
+enum Bar : int {
+  kQFull = 0,
+  kQEmpty,
+  kKvFull0,                              // + 2 * stage + half
+  kPvDone0 = kKvFull0 + 2 * kMaxStages,  // + 2 * stage + half
+  kSFull0 = kPvDone0 + 2 * kMaxStages,
+  kSEmpty0 = kSFull0 + 2,
+  kDrainA = kSEmpty0 + 2,
+  kDrainB,
+  kDrainPv,
+  kBars
+};
+
+template <int R, int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kBlocks = (D + 127) / 128;    // 128-row blocks of O^T
+  static constexpr int kHalves = D >= 256 ? 2 : 1;   // a stage is filled and freed in halves of D
+  static constexpr int kPanelsH = kPanels / kHalves, kBlocksH = kBlocks / kHalves;
+  static constexpr int kStage = kPanels * kPanel;
+  static constexpr int kStages = D == 512 ? (R == 16 ? 3 : 2) : (D == 256 ? 4 : 5);
+  static constexpr int kPanelQ = R * 128;
+  static constexpr int kPBytes = R * 128;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKV = kPanels * kPanelQ;
+  static constexpr int kOffP = kOffKV + kStages * kStage;
+  // output staging: area 0 is the two P buffers, area 1 follows
+  static constexpr int kOffStage2 = kOffP + 2 * kPBytes;
+  static constexpr int kOffBar = kOffStage2 + R * 256;
+  static constexpr int kOffMisc = kOffBar + 256;
+  static constexpr int kOffLSum = kOffMisc + 16;        // float [2][64]
+  static constexpr int kOffAlpha = kOffLSum;            // aliases the first half (used inside a unit)
+  static constexpr int kOffFac = kOffLSum + 4 * 64;     // aliases the second half
+  static constexpr int kOffHMax = kOffLSum + 4 * 128;   // float [2 tiles][2][64]
+  // The QK MMA reads 64 rows of a q panel and the PV MMA 128 columns of D
+  // whatever R and D are: what lies behind (other panels and stages, valid
+  // shared memory) lands in TMEM lanes that nothing reads.
+  static constexpr int kReach = kOffKV + kStages * kStage + kPanel;
+  static constexpr int kUsed = kOffHMax + 4 * 256;
+  static constexpr int kSmem = (kUsed > kReach ? kUsed : kReach) + 1024;
+  static constexpr int kSbCol = 128 + kBlocks * R;  // S of the second half, after O^T
+  static constexpr int kNeedCols = kSbCol + (kHalves == 2 ? 128 : 0);
+  static constexpr int kTmemCols = kNeedCols <= 256 ? 256 : 512;
+  static constexpr int kOCol = 128;
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(64, 64, false, false);
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, R, true, false);
+  static_assert(kNeedCols <= 512, "TMEM columns");
+  static_assert(kOffKV % 1024 == 0 && kOffP % 1024 == 0 && kPBytes % 1024 == 0, "swizzle atoms");
+  static_assert((kPanels - 1) * kPanelQ + 64 * 128 <= kOffBar, "padded QK operand inside smem");
+  static_assert(kBars * 8 <= 256, "mbarrier area");
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+struct Params {
+  const __nv_bfloat16* kv;
+  const float* attn_sink;
+  __nv_bfloat16* out;
+  float* lse;
+  ChunkHeader* hdr;
+  const ChunkUnit* units;
+  const int* cta_unit;
+  float2* part_ml;
+  float* part_o;
+  ChunkGeom g;
+  float qk_scale_log2;
+  uint64_t wait_timeout_ns;
+};
+
+// Walks the CTA's tiles in order; every role walks the same ones.
+struct Cursor {
+  const ChunkUnit* units;
+  int u;           // unit
+  int i;           // logical tile within the unit
+  int left;        // tiles left to this CTA, this one included
+  bool first;      // first tile of this CTA's piece of the unit
+  int b, lo, hi, nf, ntiles;
+  __device__ __forceinline__ void load() {
+    const int4 a = __ldcg(reinterpret_cast<const int4*>(units + u) + 1);
+    ntiles = __ldcg(&units[u].ntiles);
+    b = __ldcg(&units[u].b);
+    lo = a.y;
+    hi = a.z;
+    nf = a.w;
+  }
+  __device__ __forceinline__ void init(const ChunkUnit* us, int u0, int t0, int n) {
+    units = us;
+    u = u0;
+    left = n;
+    first = true;
+    if (left > 0) {
+      load();
+      i = t0 - __ldcg(&units[u].cum);
+    }
+  }
+  __device__ __forceinline__ bool last() const { return left == 1 || i == ntiles - 1; }
+  __device__ __forceinline__ void next() {
+    first = false;
+    --left;
+    if (++i == ntiles && left > 0) {
+      ++u;
+      i = 0;
+      first = true;
+      load();
+    }
+  }
+};
+
+template <int R, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
+  using C = Cfg<R, D>;
+  constexpr int KS = C::kStages;
+  constexpr int HV = C::kHalves;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t sQ = sbase + C::kOffQ, sKV = sbase + C::kOffKV, sP = sbase + C::kOffP;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
+  auto kv_full = [&](int s, int h) { return bar(kKvFull0 + 2 * s + h); };
+  auto pv_done = [&](int s, int h) { return bar(kPvDone0 + 2 * s + h); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(bar(kQFull), 1);
+    mbar_init(bar(kQEmpty), HV);
+    for (int s = 0; s < KS; ++s) {
+      for (int h = 0; h < HV; ++h) {
+        mbar_init(kv_full(s, h), kLoadWarps);
+        mbar_init(pv_done(s, h), 1);
+      }
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kSFull0 + s), HV);
+      mbar_init(bar(kSEmpty0 + s), kSmWarps);
+    }
+    mbar_init(bar(kDrainA), 1);
+    mbar_init(bar(kDrainB), 1);
+    mbar_init(bar(kDrainPv), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmap_q);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // everything above overlaps the plan; global memory only below
+  pdl_trigger();
+  const int per = p.hdr->per, n_tiles = p.hdr->n_tiles;
+  const long long t0l = (long long)blockIdx.x * per;
+  const int t0 = (int)min(t0l, (long long)n_tiles);
+  const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // this CTA's tiles
+  const int u0 = p.cta_unit[blockIdx.x];
+  const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
+
+  if (warp >= kLoadWarp0 && warp < kLoadWarp0 + kLoadWarps) {
+    // ===================================================== KV rows
+    setmaxnreg_dec<kLoadRegs>();
+    constexpr int kRows = kTile / kLoadWarps;          // 4 rows per warp and tile
+    constexpr int kCh = D / 8 / HV;                    // 16-byte chunks of a row's half
+    constexpr int kRowsPer = 32 / kCh;                 // rows per warp-wide copy
+    const int v = warp - kLoadWarp0;
+    const uint4* kv4 = reinterpret_cast<const uint4*>(p.kv);
+    // lanes 0..3: the pool row of position 4v + lane of the cursor's tile; -1:
+    // a position that no row of the unit sees (it is not read: zeros).
+    auto slot_of = [&](const Cursor& c) {
+      if (lane >= kRows) return -1;
+      const int j = chunk_tile_start(c.i, c.nf, c.lo) + v * kRows + lane;
+      if (j >= c.hi || (j < c.lo && j >= p.g.first)) return -1;
+      const int blk = __ldg(p.g.block_table + (size_t)c.b * p.g.max_blocks + j / p.g.k_per_block);
+      const long long s = p.g.base + (long long)blk * p.g.k_per_block + j % p.g.k_per_block;
+      if (blk < 0 || s >= p.g.total_pages) {
+        atomicExch(&p.hdr->error, 3);
+        return -1;
+      }
+      return (int)s;
+    };
+    auto prefetch = [&](int slot) {
+      if (slot >= 0) bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + (size_t)slot * D * 2, D * 2);
+    };
+    Cursor c;  // runs two tiles ahead of the copies
+    c.init(p.units, u0, t0, nt);
+    int sl0 = -1, sl1 = -1;
+    if (c.left > 0) {
+      sl0 = slot_of(c);
+      c.next();
+    }
+    if (c.left > 0) {
+      sl1 = slot_of(c);
+      prefetch(sl1);
+      c.next();
+    }
+    bool ok = true;
+    for (int g = 0; g < nt && ok; ++g) {
+      const int s = g % KS;
+      int sl2 = -1;
+      if (c.left > 0) {
+        sl2 = slot_of(c);
+        c.next();
+      }
+      const uint32_t stage = sKV + s * C::kStage;
+      int issued = 0;
+#pragma unroll
+      for (int h = 0; h < HV; ++h) {
+        if (g >= KS) {
+          if (lane == 0) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+        }
+        const int ch = h * kCh + lane % kCh;  // 16-byte chunk of the row: panel ch / 8
+#pragma unroll
+        for (int r0 = 0; r0 < kRows; r0 += kRowsPer) {
+          const int r = r0 + lane / kCh;
+          const int slot = __shfl_sync(0xffffffffu, sl0, r);
+          const int r8 = 4 * (v & 1) + r;
+          const uint32_t dst = stage + (ch >> 3) * kPanel + (v >> 1) * 1024 + r8 * 128 +
+                               (((ch & 7) ^ r8) << 4);
+          const uint4* src = slot >= 0 ? kv4 + (size_t)slot * (D / 8) + ch : kv4;
+          cp_async16(dst, src, slot >= 0 ? 16u : 0u);
+        }
+        cp_async_commit();
+        ++issued;
+      }
+      if (HV == 2 && issued == HV) {
+        cp_async_wait_group<1>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_full(s, 0));
+      }
+      cp_async_wait_group<0>();
+      if (issued == HV) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_full(s, HV - 1));
+      }
+      prefetch(sl2);
+      sl0 = sl1;
+      sl1 = sl2;
+    }
+  } else if (warp >= kMmaWarp) {
+    // ===================================================== QK MMAs
+    setmaxnreg_dec<kMmaRegs>();
+    const int qh = warp == kMmaWarpB ? 1 : 0;  // half of D
+    if (lane == 0 && (warp == kMmaWarp || (HV == 2 && warp == kMmaWarpB))) {
+      Cursor c;
+      c.init(p.units, u0, t0, nt);
+      int q_loads = 0;
+      bool ok = true;
+      auto load_q = [&]() {
+        mbar_arrive_expect_tx(bar(kQFull), C::kPanels * C::kPanelQ);
+        const int row = __ldcg(&p.units[c.u].row0);
+#pragma unroll
+        for (int x = 0; x < C::kPanels; ++x)
+          tma_load_2d(sQ + x * C::kPanelQ, &tmap_q, x * 64, row, bar(kQFull));
+        ++q_loads;
+      };
+      if (qh == 0 && c.left > 0) load_q();
+      int nu = 0;  // pieces seen
+      for (int g = 0; g < nt && ok; ++g) {
+        const int s = g & 1, ks = g % KS;
+        if (g >= 2) ok = pipe_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
+        if (ok && c.first) ok = pipe_wait(bar(kQFull), nu & 1, wc);
+        if (ok) ok = pipe_wait(kv_full(ks, qh), (g / KS) & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a0 = sdesc_sw128(sQ, 16, 1024);
+        const uint64_t b0 = sdesc_sw128(sKV + ks * C::kStage, 16, 1024);
+        const uint32_t acc = tmem + (qh ? C::kSbCol : 0) + s * 64;
+#pragma unroll
+        for (int x = 0; x < C::kPanelsH; ++x) {
+          const int pn = qh * C::kPanelsH + x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_bf16(acc, sdesc_advance(a0, pn * C::kPanelQ + k * 32),
+                     sdesc_advance(b0, pn * kPanel + k * 32), C::kIdescQK, (x || k) ? 1u : 0u);
+        }
+        mma_commit(bar(kSFull0 + s));
+        const bool last = c.last();
+        if (last) mma_commit(bar(kQEmpty));
+        c.next();
+        if (last) {
+          if (qh == 0 && c.left > 0) {  // q of the next unit, once both halves have read this one's
+            ok = pipe_wait(bar(kQEmpty), nu & 1, wc);
+            if (!ok) break;
+            load_q();
+          }
+          ++nu;
+        }
+      }
+      mma_commit(bar(qh ? kDrainB : kDrainA));
+      pipe_drain(bar(qh ? kDrainB : kDrainA), 0, wc);
+      if (q_loads > 0) pipe_drain(bar(kQFull), (q_loads - 1) & 1, wc);
+    }
+    __syncwarp();
+  } else {
+    // ===================================================== softmax, PV, epilogue
+    // Warp w reads TMEM lane quadrant q4 = w % 4 and positions [32hc, 32hc + 32)
+    // of each tile, hc = w / 4: thread t holds rows hA = 16 q4 + t / 4 and
+    // hB = hA + 8 at the 8 positions 32hc + 8rep + 2(t % 4) + {0, 1}.
+    setmaxnreg_inc<kSmRegs>();
+    const int q4 = warp & 3, hc = warp >> 2, st = threadIdx.x, tq = lane & 3;
+    const int hA = q4 * 16 + (lane >> 2), hB = hA + 8;
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    float* s_alpha = reinterpret_cast<float*>(smem + C::kOffAlpha);
+    float* s_fac = reinterpret_cast<float*>(smem + C::kOffFac);
+    float* s_lsum = reinterpret_cast<float*>(smem + C::kOffLSum);
+    float* s_hmax = reinterpret_cast<float*>(smem + C::kOffHMax);
+    const float sc = p.qk_scale_log2;
+    const int H = p.g.H, window = p.g.window, nfirst = p.g.first;
+    const bool held = hA < R;  // this warp's rows exist in P (uniform over the warp)
+    // Control flow is the same in the eight warps (it depends on the plan and
+    // on block-wide votes), so every named barrier is reached by all of them
+    // even after a wait timed out.
+    int g = 0;
+    for (int u = u0; g < nt; ++u) {
+      const ChunkUnit un = p.units[u];
+      const int i0 = g == 0 ? t0 - un.cum : 0;
+      const int i1 = min(un.ntiles, i0 + nt - g);
+      const bool whole = i0 == 0 && i1 == un.ntiles;
+      const bool vA = hA < un.nrows, vB = hB < un.nrows;
+      const int posA = un.pos0 + (un.h0 + hA) / H, posB = un.pos0 + (un.h0 + hB) / H;
+      const int p_hi = un.pos0 + (un.h0 + un.nrows - 1) / H;
+      const float sinkA = whole && vA ? __ldg(p.attn_sink + (un.h0 + hA) % H) : 0.f;
+      const float sinkB = whole && vB ? __ldg(p.attn_sink + (un.h0 + hB) % H) : 0.f;
+      float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;  // l: this thread's share
+      for (int i = i0; i < i1; ++i, ++g) {
+        const int s = g & 1;
+        const int j0 = chunk_tile_start(i, un.nf, un.lo);
+        // whether every row of the unit sees the whole tile
+        const bool full = j0 + kTile - 1 <= un.pos0 &&
+                          (window == 0 || j0 > p_hi - window || j0 + kTile <= nfirst);
+        pipe_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
+        tc_fence_after();
+        float x[16];
+        {
+          uint32_t sa[16];
+          tmem_ld_16x256b_x4(tmem + lane_base + s * 64 + 32 * hc, sa);
+          if constexpr (HV == 2) {
+            uint32_t sb[16];
+            tmem_ld_16x256b_x4(tmem + lane_base + C::kSbCol + s * 64 + 32 * hc, sb);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(sa[e]) + __uint_as_float(sb[e]);
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(sa[e]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSEmpty0 + s));
+        uint32_t see = 0xffffu;  // bit e: row and position of element e see each other
+        bool poison = false;     // a score that is masked and not finite
+        if (!full) {
+          see = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = j0 + 32 * hc + 8 * (e >> 2) + 2 * tq + (e & 1);
+            const int pos = (e & 3) < 2 ? posA : posB;
+            const bool ok = j <= pos && (window == 0 || j > pos - window || j < nfirst);
+            see |= ok ? 1u << e : 0u;
+            poison |= !ok && !(fabsf(x[e]) < INFINITY);
+          }
+          // A cached row with an infinity or NaN that some row of this tile
+          // does not see: its weight there is 0, but 0 x inf = NaN in the MMA.
+          // Such rows are cleared in shared memory (the rows that do see it
+          // have a NaN weight already), after the QK MMAs have read them.
+          if (named_bar_or(1, kSmThreads, poison)) {
+            uint8_t* stage = smem + C::kOffKV + (g % KS) * C::kStage;
+            const int r = st >> 2, part = st & 3;  // 4 threads per cached row
+            uint32_t bad = 0;
+            for (int ch = part; ch < D / 8; ch += 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(
+                  stage + (ch >> 3) * kPanel + (r >> 3) * 1024 + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                bad |= (ws[e] & 0x7f80u) == 0x7f80u || (ws[e] & 0x7f800000u) == 0x7f800000u;
+            }
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+            if (bad) {
+              for (int ch = part; ch < D / 8; ch += 4)
+                *reinterpret_cast<uint4*>(stage + (ch >> 3) * kPanel + (r >> 3) * 1024 +
+                                          (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();  // read by the PV MMA, issued after a later barrier
+          }
+        }
+        // P buffer s is free once the PV of tile g - 2 is done
+        if (g >= 2) {
+          if (lane == 0) pipe_wait(pv_done((g - 2) % KS, HV - 1), ((g - 2) / KS) & 1, wc);
+          __syncwarp();
+        }
+        // p = 2^(x scale - m) in bf16 into rows hA, hB of P (K-major, 128-byte
+        // swizzle) with two stmatrix.x4.  The MMA multiplies the rounded p, the
+        // denominator sums the unrounded ones: each weight is off by at most
+        // 2^-9 of itself, less than the output's own rounding, and lse is exact.
+        const uint32_t prow = sP + s * C::kPBytes + (2 * q4) * 1024 + (lane & 7) * 128 +
+                              ((((4 * hc) + (lane >> 3)) ^ (lane & 7)) << 4);
+        float sumA, sumB;
+        auto weights = [&]() {
+          bool over = false;
+          sumA = sumB = 0.f;
+          uint32_t pa[4], pb[4];
+#pragma unroll
+          for (int rep = 0; rep < 4; ++rep) {
+            float e[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool ok = (see >> (4 * rep + k)) & 1u;
+              const float arg = fmaf(x[4 * rep + k], sc, -((k < 2) ? mA : mB));
+              over = over || (ok && ((k < 2) ? vA : vB) && arg > kHeadroom);
+              e[k] = ok ? ex2_approx(arg) : 0.f;
+            }
+            sumA += e[0] + e[1];
+            sumB += e[2] + e[3];
+            const __nv_bfloat162 a = __floats2bfloat162_rn(e[0], e[1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(e[2], e[3]);
+            pa[rep] = *reinterpret_cast<const uint32_t*>(&a);
+            pb[rep] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          if (held) {
+            stmatrix_x4(prow, pa[0], pa[1], pa[2], pa[3]);
+            stmatrix_x4(prow + 1024, pb[0], pb[1], pb[2], pb[3]);
+          }
+          return over;
+        };
+        // The first tile of a piece sets m to its exact row maxima; a later one
+        // is weighted against the current m, and only if a score exceeds it by
+        // the headroom do the warps raise m and rescale O^T (p stays below 2^8).
+        bool exact = i == i0;
+        if (!exact) {
+          const bool over = weights();
+          fence_proxy_async_smem();
+          exact = named_bar_or(1, kSmThreads, over);
+        }
+        if (exact) {
+          float eA = -INFINITY, eB = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if ((see >> e) & 1u) {
+              if ((e & 3) < 2) eA = fmaxf(eA, x[e] * sc);
+              else eB = fmaxf(eB, x[e] * sc);
+            }
+          }
+#pragma unroll
+          for (int o = 1; o <= 2; o <<= 1) {
+            eA = fmaxf(eA, __shfl_xor_sync(0xffffffffu, eA, o));
+            eB = fmaxf(eB, __shfl_xor_sync(0xffffffffu, eB, o));
+          }
+          {  // the other half of the tile: warp w ^ 4
+            float* hm = s_hmax + (g & 1) * 128;
+            if (tq == 0) {
+              hm[hc * 64 + hA] = eA;
+              hm[hc * 64 + hB] = eB;
+            }
+            named_bar_sync(2 + q4, 64);
+            eA = fmaxf(eA, hm[(hc ^ 1) * 64 + hA]);
+            eB = fmaxf(eB, hm[(hc ^ 1) * 64 + hB]);
+          }
+          float alphaA = 1.f, alphaB = 1.f;
+          if (eA > mA + kHeadroom || (mA == -INFINITY && eA > mA)) {
+            alphaA = ex2_approx(mA - eA);  // 0 when m was -inf
+            lA *= alphaA;
+            mA = eA;
+          }
+          if (eB > mB + kHeadroom || (mB == -INFINITY && eB > mB)) {
+            alphaB = ex2_approx(mB - eB);
+            lB *= alphaB;
+            mB = eB;
+          }
+          weights();
+          fence_proxy_async_smem();
+          if (i > i0) {
+            if (tq == 0 && hc == 0) {
+              s_alpha[hA] = alphaA;
+              s_alpha[hB] = alphaB;
+            }
+            named_bar_sync(1, kSmThreads);
+            // O^T must be quiescent: wait for the PV of tile g - 1
+            if (lane == 0) pipe_wait(pv_done((g - 1) % KS, HV - 1), ((g - 1) / KS) & 1, wc);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int b = hc; b < C::kBlocks; b += 2) {
+#pragma unroll
+              for (int c = 0; c < R / 16; ++c) {
+                uint32_t ov[16];
+                const uint32_t ta = tmem + lane_base + C::kOCol + b * R + c * 16;
+                tmem_ld16(ta, ov);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  ov[e] = __float_as_uint(__uint_as_float(ov[e]) * s_alpha[c * 16 + e]);
+                tmem_st16(ta, ov);
+              }
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          named_bar_sync(1, kSmThreads);
+        }
+        lA += sumA;
+        lB += sumB;
+        if (threadIdx.x == 0) {
+          tc_fence_after();
+          const int ks = g % KS;
+          const uint64_t a0 = sdesc_sw128(sKV + ks * C::kStage, kPanel, 1024);
+          const uint64_t b0 = sdesc_sw128(sP + s * C::kPBytes, 16, 1024);
+#pragma unroll
+          for (int b = 0; b < C::kBlocks; ++b) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16(tmem + C::kOCol + b * R, sdesc_advance(a0, 2 * b * kPanel + k * 2048),
+                       sdesc_advance(b0, k * 32), C::kIdescPV, (i == i0 && k == 0) ? 0u : 1u);
+            if ((b + 1) % C::kBlocksH == 0) mma_commit(pv_done(ks, b / C::kBlocksH));
+          }
+        }
+        __syncwarp();
+      }
+      // ---------------------------------------------- end of the piece
+      lA += __shfl_xor_sync(0xffffffffu, lA, 1);
+      lA += __shfl_xor_sync(0xffffffffu, lA, 2);
+      lB += __shfl_xor_sync(0xffffffffu, lB, 1);
+      lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+      // (the last tile's barrier lies behind every read of s_alpha, which s_lsum aliases)
+      if (tq == 0) {
+        s_lsum[hc * 64 + hA] = lA;
+        s_lsum[hc * 64 + hB] = lB;
+      }
+      if (lane == 0) pipe_wait(pv_done((g - 1) % KS, HV - 1), ((g - 1) / KS) & 1, wc);
+      __syncwarp();
+      tc_fence_after();
+      named_bar_sync(1, kSmThreads);
+      const int slot = 2 * (int)blockIdx.x + (i0 == 0 ? 1 : 0);
+      if (tq == 0 && hc == 0) {
+#pragma unroll
+        for (int w2 = 0; w2 < 2; ++w2) {
+          const int r = w2 ? hB : hA;
+          if (r >= R) continue;
+          const float m = w2 ? mB : mA;
+          const float l = s_lsum[r] + s_lsum[64 + r];  // read before fac[r] overwrites s_lsum[64 + r]
+          float f = 0.f;
+          if (whole) {
+            if (w2 ? vB : vA) {
+              const float ms = (w2 ? sinkB : sinkA) * kLog2e;
+              const float M = fmaxf(m, ms);
+              float lse = M * kLn2;
+              if (M != -INFINITY && ms != INFINITY) {
+                const float a = m == -INFINITY ? 0.f : ex2_approx(m - M);
+                const float den = fmaf(l, a, ex2_approx(ms - M));
+                f = a / den;
+                lse = (M + log2f(den)) * kLn2;
+              }
+              p.lse[un.row0 + r] = lse;
+            }
+          } else {
+            p.part_ml[(size_t)slot * R + r] = make_float2(m, l);
+          }
+          s_fac[r] = f;
+        }
+      }
+      named_bar_sync(1, kSmThreads);
+      if (whole) {
+        // warps 4hc .. 4hc + 3 write blocks hc, hc + 2 of O^T through staging
+        // area hc: scaled, packed to bf16 and transposed with stmatrix into two
+        // boxes of R rows x 64 columns, then row by row to out
+        uint8_t* stg = smem + (hc ? C::kOffStage2 : C::kOffP);
+        constexpr int kRc = R < 32 ? R : 32;
+#pragma unroll 1
+        for (int b = hc; b < C::kBlocks; b += 2) {
+#pragma unroll
+          for (int r0 = 0; r0 < R; r0 += kRc) {
+            float fac[kRc / 4];
+#pragma unroll
+            for (int rep = 0; rep < kRc / 8; ++rep) {
+              fac[2 * rep] = s_fac[r0 + 8 * rep + 2 * tq];
+              fac[2 * rep + 1] = s_fac[r0 + 8 * rep + 2 * tq + 1];
+            }
+            uint32_t rr[2][kRc / 2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t ta =
+                  tmem + ((uint32_t)(q4 * 32 + 16 * half) << 16) + C::kOCol + b * R + r0;
+              if constexpr (kRc == 32) tmem_ld_16x256b_x4(ta, rr[half]);
+              else tmem_ld_16x256b_x2(ta, rr[half]);
+            }
+            tmem_wait_ld();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t pk[kRc / 4];
+#pragma unroll
+              for (int rep = 0; rep < kRc / 8; ++rep) {
+#pragma unroll
+                for (int dg = 0; dg < 2; ++dg) {
+                  // "+ 0.f" turns -0 into +0 when the factor is 0 (sink = +inf)
+                  const __nv_bfloat162 v2 = __floats2bfloat162_rn(
+                      __uint_as_float(rr[half][4 * rep + 2 * dg]) * fac[2 * rep] + 0.f,
+                      __uint_as_float(rr[half][4 * rep + 2 * dg + 1]) * fac[2 * rep + 1] + 0.f);
+                  pk[2 * rep + dg] = *reinterpret_cast<const uint32_t*>(&v2);
+                }
+              }
+              const int mt = lane >> 3, jr = lane & 7;
+              const int dl = q4 * 32 + 16 * half + 8 * (mt & 1);
+              const int box = dl >> 6, chunk = (dl & 63) >> 3;
+#pragma unroll
+              for (int rep0 = 0; rep0 < kRc / 8; rep0 += 2) {
+                const int r = r0 + 8 * (rep0 + (mt >> 1)) + jr;
+                stmatrix_x4_trans(smem_addr(stg) + box * (R * 128) + r * 128 + ((chunk ^ (r & 7)) << 4),
+                                  pk[2 * rep0], pk[2 * rep0 + 1], pk[2 * rep0 + 2], pk[2 * rep0 + 3]);
+              }
+            }
+          }
+          named_bar_sync(6 + hc, 128);
+          constexpr int kW = D < 128 ? D / 8 : 16;  // 16-byte chunks of a row of this block
+          for (int e = st & 127; e < un.nrows * kW; e += 128) {
+            const int r = e / kW, ch = e % kW;
+            const uint4 w = *reinterpret_cast<const uint4*>(stg + (ch >> 3) * (R * 128) + r * 128 +
+                                                            (((ch & 7) ^ (r & 7)) << 4));
+            *reinterpret_cast<uint4*>(p.out + (size_t)(un.row0 + r) * D + b * 128 + ch * 8) = w;
+          }
+          named_bar_sync(6 + hc, 128);  // the area may be rewritten
+        }
+      } else {
+#pragma unroll 1
+        for (int b = hc; b < C::kBlocks; b += 2) {
+          const int d = b * 128 + q4 * 32 + lane;
+#pragma unroll
+          for (int c = 0; c < R / 16; ++c) {
+            uint32_t ov[16];
+            tmem_ld16(tmem + lane_base + C::kOCol + b * R + c * 16, ov);
+            tmem_wait_ld();
+            float* o = p.part_o + ((size_t)slot * R + c * 16) * D + d;
+            if (d < D) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[(size_t)e * D] = __uint_as_float(ov[e]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(1, kSmThreads);
+    }
+    if (threadIdx.x == 0) {
+      mma_commit(bar(kDrainPv));
+      pipe_drain(bar(kDrainPv), 0, wc);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <typename F>
+cudaError_t for_shape(int R, int D, F&& f) {
+#define SDA_CASE(RV, DV) \
+  if (R == RV && D == DV) return f(chunk_attn_kernel<RV, DV>, (size_t)Cfg<RV, DV>::kSmem);
+  SDA_CASE(16, 64) SDA_CASE(16, 128) SDA_CASE(16, 256) SDA_CASE(16, 512)
+  SDA_CASE(64, 64) SDA_CASE(64, 128) SDA_CASE(64, 256) SDA_CASE(64, 512)
+#undef SDA_CASE
+  return cudaErrorInvalidValue;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+}  // namespace
+
+bool pipe_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
+                 uint32_t box_rows) {
+  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+  const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// setmaxnreg.inc waits until the other warps have released registers: a build
+// whose launch allocation is smaller than the split assumes is never launched.
+cudaError_t chunk_prepare() {
+  for (int R : {16, 64}) {
+    for (int D : {64, 128, 256, 512}) {
+      const cudaError_t e = for_shape(R, D, [&](auto kernel, size_t smem) {
+        cudaError_t r =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncAttributes a;
+        if (r == cudaSuccess) r = cudaFuncGetAttributes(&a, kernel);
+        if (r == cudaSuccess && (a.numRegs < kLaunchRegs || a.maxThreadsPerBlock < kThreads))
+          r = cudaErrorInvalidConfiguration;
+        return r;
+      });
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
+                              const float* attn_sink, float scale, void* out, float* lse,
+                              const ChunkLayout& L, void* ws, cudaStream_t st) {
+  CUtensorMap tq;
+  if (!pipe_map_2d(&tq, q, g.D, (uint64_t)g.T * g.H, 64, L.R)) return cudaErrorInvalidValue;
+  char* base = static_cast<char*>(ws);
+  Params p;
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.attn_sink = attn_sink;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.hdr = reinterpret_cast<ChunkHeader*>(base);
+  p.units = reinterpret_cast<const ChunkUnit*>(base + L.units_off);
+  p.cta_unit = reinterpret_cast<const int*>(base + L.cta_off);
+  p.part_ml = reinterpret_cast<float2*>(base + L.ml_off);
+  p.part_o = reinterpret_cast<float*>(base + L.o_off);
+  p.g = g;
+  p.qk_scale_log2 = scale * kLog2e;
+  p.wait_timeout_ns = current_wait_fault().timeout_ns;
+  return for_shape(L.R, g.D, [&](auto kernel, size_t smem) {
+    return launch_pdl(kernel, dim3(L.grid), dim3(kThreads), smem, st, tq, p);
+  });
+}
+
+}  // namespace sda

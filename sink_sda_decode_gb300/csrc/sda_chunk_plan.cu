@@ -1,0 +1,293 @@
+// sda_chunk_plan.cu -- work plan of the chunk attention, and the merge of
+// units that the plan cut.
+//
+// The plan runs on the device because the lengths live there and the call
+// must stay capturable.  The units' KV tiles form one sequence, which is cut
+// into equal ranges, one per CTA ("split-L"): CTA k owns the tiles
+// [k * per, (k + 1) * per).  A unit that a range boundary cuts becomes
+// pieces, each of which leaves an unnormalised (m, l, acc); the combine
+// kernel merges them.
+#include <cuda_bf16.h>
+
+#include "sda_chunk.cuh"
+
+namespace sda {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kSmemUnits = 8192;  // units whose tile offsets are also kept in shared memory
+constexpr int kSmemSeqs = 2048;   // sequences whose unit offsets are kept in shared memory
+
+__device__ long long scan_exclusive(long long v, long long* warp_sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    const long long w = warp_sums[lane];
+    long long s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s - w;
+    if (lane == 31) *total = s;
+  }
+  __syncthreads();
+  const long long r = warp_sums[warp] + x - v;
+  __syncthreads();  // warp_sums is rewritten by the next call (*total after its first barrier)
+  return r;
+}
+
+// Last index i in [0, n) with a[i] <= x; a non-decreasing, a[0] <= x.
+__device__ __forceinline__ int last_le(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
+    const ChunkGeom g, int R, int grid, int u_max, ChunkHeader* __restrict__ hdr,
+    ChunkUnit* __restrict__ units, int* __restrict__ seq_unit, int* __restrict__ cta_unit) {
+  __shared__ long long warp_sums[32];
+  __shared__ long long s_total;
+  __shared__ int s_cum[kSmemUnits];
+  __shared__ int s_seq[kSmemSeqs + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  // units of every sequence; lengths that make no sense stop the plan
+  int bad = 0;
+  long long U = 0;
+  const long long cap = (long long)g.max_blocks * g.k_per_block;
+  for (int b0 = 0; b0 < g.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    long long nu = 0;
+    if (b < g.B) {
+      const int q0 = g.q_indptr[b], q1 = g.q_indptr[b + 1], n = g.kv_len[b];
+      if (q0 < 0 || q1 < q0 || q1 > g.T || n < 0 || n > cap) bad = 1;
+      else nu = ((long long)(q1 - q0) * g.H + R - 1) / R;
+    }
+    long long tot;
+    const long long ex = scan_exclusive(nu, warp_sums, &s_total);
+    tot = s_total;
+    if (b < g.B) {
+      const int v = (int)min(U + ex, (long long)u_max);
+      if (b <= kSmemSeqs) s_seq[b] = v;
+      seq_unit[b] = v;
+    }
+    U += tot;
+    __syncthreads();
+  }
+  if (U > u_max) bad = 1;
+  bad = __syncthreads_or(bad);
+  const int nu = bad ? 0 : (int)U;
+  const int* seq = g.B <= kSmemSeqs ? s_seq : seq_unit;
+  long long tt = 0;
+  for (int u0 = 0; u0 < nu; u0 += kPlanThreads) {
+    const int u = u0 + tid;
+    ChunkUnit d = {};
+    if (u < nu) {
+      // the last sequence that starts at or before u (sequences without tokens share a start)
+      const int b = last_le(seq, g.B, u);
+      const int q0 = g.q_indptr[b], m = g.q_indptr[b + 1] - q0, n = g.kv_len[b];
+      const long long r0 = (long long)(u - seq[b]) * R;  // row in the sequence's m * H rows
+      const long long rows = (long long)m * g.H - r0;
+      d.row0 = (int)((long long)q0 * g.H + r0);
+      d.nrows = (int)min((long long)R, rows);
+      d.b = b;
+      d.pos0 = n - m + (int)(r0 / g.H);
+      d.h0 = (int)(r0 % g.H);
+      const int p_hi = d.pos0 + (d.h0 + d.nrows - 1) / g.H;
+      d.hi = max(p_hi + 1, 0);
+      d.lo = g.window > 0 ? max(0, (int)max((long long)d.pos0 - g.window + 1, 0ll)) : 0;
+      if (d.hi == 0) d.lo = 0;
+      const int lot = d.lo / kChunkTile;
+      d.nf = (min(g.first, lot * kChunkTile) + kChunkTile - 1) / kChunkTile;
+      d.ntiles = d.nf + (d.hi + kChunkTile - 1) / kChunkTile - lot;
+      if (d.ntiles < 1) d.ntiles = 1;  // rows that see nothing: one tile of masked positions
+    }
+    const long long ex = scan_exclusive(d.ntiles, warp_sums, &s_total);
+    const long long tot = s_total;
+    if (u < nu) {
+      d.cum = (int)min(tt + ex, 0x7fffffffll);
+      units[u] = d;
+      if (u < kSmemUnits) s_cum[u] = d.cum;
+    }
+    tt += tot;
+    __syncthreads();
+  }
+  if (tt > 0x7fffffffll) bad = 1, tt = 0;  // uniform: every thread has the same sum
+  const int TT = bad ? 0 : (int)tt;
+  const int per = TT > 0 ? (int)((TT + (long long)grid - 1) / grid) : 1;
+  for (int k = tid; k <= grid; k += kPlanThreads) {
+    const long long t = (long long)k * per;
+    int u = nu;
+    if (t < TT) {
+      if (nu <= kSmemUnits) {
+        u = last_le(s_cum, nu, (int)t);
+      } else {
+        int lo = 0, hi = nu;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (units[mid].cum <= t) lo = mid;
+          else hi = mid;
+        }
+        u = lo;
+      }
+    }
+    cta_unit[k] = u;
+  }
+  if (tid == 0) {
+    hdr->n_units = nu;
+    hdr->n_tiles = TT;
+    hdr->per = per;
+    hdr->ctas = (TT + per - 1) / per;
+    hdr->error = bad ? 2 : 0;
+  }
+}
+
+// Merge of the pieces of cut units.  Block (x = k - 1, y): boundary k of the
+// tile ranges; it acts if boundary k is the first to cut its unit, and its
+// warps take that unit's rows y * kWarps + warp.  Piece 0 lies in slot
+// 2 (k - 1) + 1 (the unit starts in CTA k - 1's range), piece i in slot
+// 2 (k - 1 + i).
+constexpr int kCombineWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
+    const float* __restrict__ attn_sink, int H, int R, __nv_bfloat16* __restrict__ out,
+    float* __restrict__ lse, const ChunkHeader* __restrict__ hdr,
+    const ChunkUnit* __restrict__ units, const int* __restrict__ cta_unit,
+    const float2* __restrict__ part_ml, const float* __restrict__ part_o) {
+  pdl_wait();
+  pdl_trigger();
+  const int k = blockIdx.x + 1;
+  if (k >= hdr->ctas) return;
+  const int per = hdr->per;
+  const int u = cta_unit[k];
+  const int cum = units[u].cum;
+  const long long t0 = (long long)k * per;
+  if (cum >= t0 || cum < t0 - per) return;  // not cut here, or cut by an earlier boundary already
+  const int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= units[u].nrows) return;
+  const long long end = (long long)cum + units[u].ntiles;
+  const int np = 1 + (int)((end - t0 + per - 1) / per);
+  auto slot = [&](int i) { return i == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + i); };
+  const int h = (units[u].h0 + row) % H;
+  const float ms = attn_sink[h] * kLog2e;
+  float mk = -INFINITY;
+  for (int i = lane; i < np; i += 32) mk = fmaxf(mk, part_ml[(size_t)slot(i) * R + row].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+  const float M = fmaxf(ms, mk);
+  const bool dead = ms == INFINITY || M == -INFINITY;
+  float den = 0.f;
+  for (int i = lane; i < np; i += 32) {
+    const float2 ml = part_ml[(size_t)slot(i) * R + row];
+    // (a piece whose rows are all masked has m = -inf, l = 0)
+    den += dead || ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - M);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (!dead) den += ex2_approx(ms - M);
+  constexpr int kPer = D / 32 < 4 ? 2 : 4;     // consecutive values per lane and group
+  constexpr int kGroups = D / (32 * kPer);
+  float acc[kGroups][kPer] = {};
+  for (int i = 0; i < np && !dead; ++i) {
+    const float m = part_ml[(size_t)slot(i) * R + row].x;
+    const float w = ex2_approx(m - M);
+    const float* o = part_o + ((size_t)slot(i) * R + row) * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kGroups; ++e) {
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) acc[e][x] += w * o[e * 32 * kPer + x];
+    }
+  }
+  const float inv = dead ? 0.f : 1.f / den;
+  const size_t orow = (size_t)units[u].row0 + row;
+#pragma unroll
+  for (int e = 0; e < kGroups; ++e) {
+#pragma unroll
+    for (int x = 0; x < kPer; x += 2) {
+      // "+ 0.f" turns -0 into +0 (a factor of 0 when the sink is +inf)
+      const __nv_bfloat162 v =
+          __floats2bfloat162_rn(acc[e][x] * inv + 0.f, acc[e][x + 1] * inv + 0.f);
+      *reinterpret_cast<__nv_bfloat162*>(out + orow * D + e * 32 * kPer + lane * kPer + x) = v;
+    }
+  }
+  if (lane == 0) lse[orow] = dead ? M * kLn2 : (M + log2f(den)) * kLn2;
+}
+
+}  // namespace
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms) {
+  ChunkLayout L;
+  const int64_t rows = (int64_t)T * H;
+  // 16-row units where a sequence has at most 16 rows on average (a step of
+  // few heads): q then takes a quarter of the shared memory and a third KV
+  // stage fits, and the rows' masks and stores are not padded to 64.
+  L.R = rows <= (int64_t)16 * B ? 16 : 64;
+  L.u_max = (int)((rows + L.R - 1) / L.R + B);
+  L.grid = num_sms < kMaxPlanGrid ? num_sms : kMaxPlanGrid;
+  size_t off = sizeof(ChunkHeader);
+  L.units_off = off;
+  off = align256(off + (size_t)L.u_max * sizeof(ChunkUnit));
+  L.seq_off = off;
+  off = align256(off + (size_t)(B + 1) * 4);
+  L.cta_off = off;
+  off = align256(off + (size_t)(L.grid + 1) * 4);
+  L.ml_off = off;
+  off = align256(off + (size_t)2 * L.grid * L.R * 8);
+  L.o_off = off;
+  off = align256(off + (size_t)2 * L.grid * L.R * D * 4);
+  L.total = off;
+  return L;
+}
+
+cudaError_t launch_chunk_plan(const ChunkGeom& g, const ChunkLayout& L, void* ws, cudaStream_t st) {
+  char* base = static_cast<char*>(ws);
+  return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, g, L.R, L.grid, L.u_max,
+                    reinterpret_cast<ChunkHeader*>(base),
+                    reinterpret_cast<ChunkUnit*>(base + L.units_off),
+                    reinterpret_cast<int*>(base + L.seq_off),
+                    reinterpret_cast<int*>(base + L.cta_off));
+}
+
+cudaError_t launch_chunk_combine(const float* attn_sink, const ChunkGeom& g, void* out, float* lse,
+                                 const ChunkLayout& L, void* ws, cudaStream_t st) {
+  char* base = static_cast<char*>(ws);
+  if (L.grid < 2) return cudaSuccess;
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(L.grid - 1, L.R / kCombineWarps), dim3(kCombineWarps * 32), 0,
+                      st, attn_sink, g.H, L.R, static_cast<__nv_bfloat16*>(out), lse,
+                      reinterpret_cast<const ChunkHeader*>(base),
+                      reinterpret_cast<const ChunkUnit*>(base + L.units_off),
+                      reinterpret_cast<const int*>(base + L.cta_off),
+                      reinterpret_cast<const float2*>(base + L.ml_off),
+                      reinterpret_cast<const float*>(base + L.o_off));
+  };
+  switch (g.D) {
+    case 64: return go(chunk_combine_kernel<64>);
+    case 128: return go(chunk_combine_kernel<128>);
+    case 256: return go(chunk_combine_kernel<256>);
+    case 512: return go(chunk_combine_kernel<512>);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace sda

@@ -1,0 +1,109 @@
+"""Operators on a paged cache: attention of a chunk of new tokens.
+
+A sequence's cached positions are found through a block table: position j of
+sequence b lies in pool row
+
+    base + block_table[b, j // k_per_block] * k_per_block + j % k_per_block
+
+(`base` is the first pool row of the block region; k_per_block = 1 makes the
+table one of single slots).  With m_b new tokens and n_b = kv_len[b] cached
+positions, the new tokens' own rows the last m_b of them, token i stands at
+p = n_b - m_b + i and sees the positions j <= p with window == 0, or
+j > p - window, or j < first.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+
+
+def _int32(v, name: str, low: int = 0) -> int:
+    v = int(v)
+    if not low <= v < 2 ** 31:
+        raise ValueError(f"{name} must be in [{low}, 2^31), got {v}")
+    return v
+
+
+def _tables(q, unified_kv, block_table, q_indptr, kv_len):
+    """Checks the tensors that the paged operators share; returns (B, T, H, D)."""
+    from . import _req
+    _req(q, "q", torch.bfloat16, 3)
+    dev = q.device
+    _req(unified_kv, "unified_kv", torch.bfloat16, 2, dev)
+    _req(block_table, "block_table", torch.int32, 2, dev)
+    _req(q_indptr, "q_indptr", torch.int32, 1, dev)
+    _req(kv_len, "kv_len", torch.int32, 1, dev)
+    T, H, D = q.shape
+    B = kv_len.numel()
+    if unified_kv.shape[1] != D:
+        raise ValueError("unified_kv row length must equal q's head dim")
+    if block_table.shape[0] != B or q_indptr.numel() != B + 1:
+        raise ValueError("block_table must have a row and q_indptr an interval per entry of kv_len")
+    return B, T, H, D
+
+
+def chunk_attention_workspace_size(B: int, T: int, H: int, D: int) -> int:
+    """Bytes of workspace chunk_attention() needs on the current CUDA device
+    for B sequences and T tokens in all."""
+    lib = _lib.load()
+    n = ctypes.c_size_t(0)
+    _lib.check(lib.sda_chunk_attention_workspace_size(_int32(B, "B"), _int32(T, "T"), _int32(H, "H"),
+                                                      _int32(D, "D"), ctypes.byref(n)),
+               "sda_chunk_attention_workspace_size")
+    return int(n.value)
+
+
+def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torch.Tensor,
+                    q_indptr: torch.Tensor, kv_len: torch.Tensor, attn_sink: torch.Tensor,
+                    softmax_scale: float, *, k_per_block: int, base: int = 0, window: int = 0,
+                    first: int = 0, out: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None):
+    """Causal attention of every sequence's new tokens over its cached positions.
+
+    q [T, H, D] bf16, the sequences' tokens one after the other; unified_kv
+    [P, D] bf16 (a row is key and value); block_table [B, max_blocks] int32;
+    q_indptr [B + 1] int32 (sequence b's tokens: q_indptr[b] .. q_indptr[b + 1]);
+    kv_len [B] int32, cached positions including the new tokens' own; attn_sink
+    [H] fp32 sink logits.  Returns (out [T, H, D] bf16, lse [T, H] fp32, the log
+    of the softmax denominator, sink included).  A row that sees nothing gets
+    out = 0 and lse = the sink; rows outside [q_indptr[0], q_indptr[B]) are not
+    written.  H up to 256, D in {64, 128, 256, 512}.
+
+    Asynchronous on `stream`.  With out, lse and `workspace` (uint8, at least
+    chunk_attention_workspace_size(...) bytes) given the call allocates nothing
+    and can be captured into a CUDA graph; calls that may overlap on the GPU
+    need a workspace each.  decode_error_flag(workspace) reads its error word
+    (2: lengths outside the contract, nothing computed; 3: a table entry
+    outside the pool).
+    """
+    from . import _req, _stream_ptr, _workspace_for
+    lib = _lib.load()
+    B, T, H, D = _tables(q, unified_kv, block_table, q_indptr, kv_len)
+    dev = q.device
+    _req(attn_sink, "attn_sink", torch.float32, 1, dev)
+    if attn_sink.numel() != H:
+        raise ValueError("attn_sink must have H entries")
+    if out is None:
+        out = torch.empty_like(q)
+    _req(out, "out", torch.bfloat16, 3, dev)
+    if lse is None:
+        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+    _req(lse, "lse", torch.float32, 2, dev)
+    if out.shape != q.shape or lse.shape != (T, H):
+        raise ValueError("out must have q's shape and lse be [T, H]")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = _workspace_for(chunk_attention_workspace_size(B, T, H, D), dev, stream)
+        _req(workspace, "workspace", torch.uint8, 1, dev)
+        rc = lib.sda_chunk_attention(
+            q.data_ptr(), unified_kv.data_ptr(), unified_kv.shape[0], block_table.data_ptr(),
+            block_table.shape[1], _int32(k_per_block, "k_per_block", 1), int(base),
+            q_indptr.data_ptr(), kv_len.data_ptr(), attn_sink.data_ptr(), float(softmax_scale),
+            _int32(window, "window"), _int32(first, "first"), B, T, H, D, out.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+    _lib.check(rc, "sda_chunk_attention")
+    return out, lse
