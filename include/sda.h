@@ -481,6 +481,58 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
                                int B, int T, int H, int D, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/*
+ * Attention mass: the weight that every cached position received from a
+ * chunk's tokens, summed over tokens and heads, added to what it had.  With
+ * the geometry and arguments of sda_chunk_attention and its lse:
+ *   out[b][j] = decay * prev[b][j] + sum over the rows (token, head) of
+ *               sequence b that see j of e^(softmax_scale <q, kv_j> - lse)
+ * for j < kv_len[b], and 0 from kv_len[b] on.  A row with lse = +inf (a sink
+ * of +inf) adds nothing.  The sums run in a fixed order: same inputs, same
+ * bits.
+ *   lse   [T, H] fp32
+ *   prev  [B, S] fp32, S = max_blocks * k_per_block, or NULL for zeros
+ *   out   [B, S] fp32; may be prev itself, must not partly overlap it
+ * T may be 0 (q and lse may then be NULL): out = decay * prev.  Error word and
+ * workspace as sda_chunk_attention (word 2: lengths outside the contract, out
+ * without any weight added).  The timing hook brackets all of its launches.
+ */
+sda_status sda_attention_mass_workspace_size(int B, int max_blocks, int k_per_block, size_t* bytes);
+
+sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t total_pages,
+                              const int32_t* block_table, int max_blocks, int k_per_block,
+                              int64_t base, const int32_t* q_indptr, const int32_t* kv_len,
+                              const float* lse, float softmax_scale, int window, int first,
+                              const float* prev, float decay, int B, int T, int H, int D,
+                              float* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction from caches held as tables of single slots (a block table with
+ * k_per_block = 1): which positions of each sequence to keep by accumulated
+ * weight.  Sequence b with n = kv_len[b] <= budget keeps everything.
+ * Otherwise it keeps its first `first` and last `recent` positions and, of
+ * those between, the budget - first - recent with the largest score (-0 equal
+ * to +0, NaN below -inf, equal scores by increasing position), in their order:
+ *   out_scores, out_table [B, out_stride]: the kept positions' scores and
+ *               slots, behind them 0 and -1
+ *   out_len     [B] min(n, budget)
+ *   freed_slots, freed_indptr [B + 1]: the other positions' slots, sequence by
+ *               sequence in increasing position; behind freed_indptr[B]: -1
+ * Arguments (device pointers): scores [B, stride] fp32, slot_table [B, stride]
+ * int32 (entries behind kv_len are not read), kv_len [B] int32 in [0, stride]
+ * (outside: counts as 0, status bit 1); 0 <= first + recent <= budget;
+ * out_stride >= min(stride, budget); freed_capacity >= B * max(stride -
+ * budget, 0), at most 2^31 - 1.  out_scores / out_table / out_len may be
+ * scores / slot_table / kv_len themselves (with out_stride = stride) and must
+ * not otherwise overlap what is read.  *status (device int32, overwritten):
+ * bits 1 (bad length), 8 (a NaN competed).  Graph-capturable, no workspace.
+ */
+sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64_t stride,
+                           const int32_t* kv_len, int B, int budget, int first, int recent,
+                           float* out_scores, int32_t* out_table, int64_t out_stride,
+                           int32_t* out_len, int32_t* freed_slots, int64_t freed_capacity,
+                           int32_t* freed_indptr, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

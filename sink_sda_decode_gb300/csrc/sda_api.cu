@@ -13,6 +13,7 @@
 
 #include "sda_chunk.cuh"
 #include "sda_copy.cuh"
+#include "sda_evict.cuh"
 #include "sda_internal.cuh"
 #include "sda_scatter.cuh"
 
@@ -58,6 +59,7 @@ cudaError_t device_caps(DeviceCaps* caps) {
     for (int nh : {16, 32, 64})
       if (d.err == cudaSuccess) d.err = umma_prepare(nh);
     if (d.err == cudaSuccess) d.err = chunk_prepare();
+    if (d.err == cudaSuccess) d.err = mass_prepare();
   });
   *caps = d.caps;
   return d.err;
@@ -1010,6 +1012,121 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
   if (e == cudaSuccess) e = launch_chunk_combine(attn_sink, g, out, lse, L, workspace, st);
   if (e != cudaSuccess) {
     note_cuda_error(e, "sda_chunk_attention");
+    return SDA_ERR_CUDA;
+  }
+  return SDA_OK;
+}
+
+// The mass's score rows span the whole table: S = max_blocks * k_per_block.
+static sda_status mass_geometry_ok(const ChunkGeom& g) {
+  const sda_status s = chunk_geometry_ok(g);
+  if (s != SDA_OK) return s;
+  const int64_t S = static_cast<int64_t>(g.max_blocks) * g.k_per_block;
+  if (S > 0x7fffffffll || (S / 128 + 1) * g.B > (1 << 26)) return SDA_ERR_INVALID_ARG;
+  return SDA_OK;
+}
+
+sda_status sda_attention_mass_workspace_size(int B, int max_blocks, int k_per_block, size_t* bytes) {
+  if (!bytes) return SDA_ERR_INVALID_ARG;
+  ChunkGeom g = {};
+  g.B = B, g.H = 1, g.D = 64, g.max_blocks = max_blocks, g.k_per_block = k_per_block;
+  g.total_pages = 1;
+  const sda_status s = mass_geometry_ok(g);
+  if (s != SDA_OK) return s;
+  DeviceCaps caps;
+  const cudaError_t e = device_caps(&caps);
+  if (e != cudaSuccess) {
+    note_cuda_error(e, "sda_attention_mass_workspace_size");
+    return SDA_ERR_CUDA;
+  }
+  *bytes = mass_layout(B, static_cast<int64_t>(max_blocks) * k_per_block, caps.num_sms).total;
+  return SDA_OK;
+}
+
+sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t total_pages,
+                              const int32_t* block_table, int max_blocks, int k_per_block,
+                              int64_t base, const int32_t* q_indptr, const int32_t* kv_len,
+                              const float* lse, float softmax_scale, int window, int first,
+                              const float* prev, float decay, int B, int T, int H, int D,
+                              float* out, void* workspace, size_t workspace_bytes, void* stream) {
+  const ChunkGeom g{q_indptr, kv_len,      block_table, B,      T,    H, D, max_blocks,
+                    k_per_block, base, total_pages, window, first};
+  const sda_status s = mass_geometry_ok(g);
+  if (s != SDA_OK) return s;
+  const int64_t S = static_cast<int64_t>(max_blocks) * k_per_block;
+  if (B == 0 || S == 0) return SDA_OK;
+  if (!unified_kv || !block_table || !q_indptr || !kv_len || !out || !workspace)
+    return SDA_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !lse)) return SDA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(unified_kv, 16)) return SDA_ERR_INVALID_ARG;
+  for (const void* ptr : {static_cast<const void*>(q_indptr), static_cast<const void*>(kv_len),
+                          static_cast<const void*>(block_table), static_cast<const void*>(lse),
+                          static_cast<const void*>(prev), static_cast<const void*>(out)})
+    if (!aligned(ptr, 4)) return SDA_ERR_INVALID_ARG;
+  // out is prev itself or apart from everything that is read
+  const size_t nb = static_cast<size_t>(B) * S * 4;
+  if (prev && prev != out && overlaps(prev, nb, out, nb)) return SDA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return SDA_ERR_WORKSPACE;
+  DeviceCaps caps;
+  cudaError_t e = device_caps(&caps);
+  if (e != cudaSuccess) {
+    note_cuda_error(e, "sda_attention_mass");
+    return SDA_ERR_CUDA;
+  }
+  const MassLayout L = mass_layout(B, S, caps.num_sms);
+  if (workspace_bytes < L.total) return SDA_ERR_WORKSPACE;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_before, st);
+  if (e == cudaSuccess)
+    e = launch_mass(q, unified_kv, g, lse, softmax_scale, prev, decay, out, L, workspace, st);
+  if (e == cudaSuccess && g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_after, st);
+  if (e != cudaSuccess) {
+    note_cuda_error(e, "sda_attention_mass");
+    return SDA_ERR_CUDA;
+  }
+  return SDA_OK;
+}
+
+sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64_t stride,
+                           const int32_t* kv_len, int B, int budget, int first, int recent,
+                           float* out_scores, int32_t* out_table, int64_t out_stride,
+                           int32_t* out_len, int32_t* freed_slots, int64_t freed_capacity,
+                           int32_t* freed_indptr, int32_t* status, void* stream) {
+  if (B < 0 || stride < 0 || stride > 0x7fffffffll || budget < 0 || first < 0 || recent < 0 ||
+      out_stride < 0 || out_stride > 0x7fffffffll || freed_capacity < 0)
+    return SDA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(first) + recent > budget) return SDA_ERR_INVALID_ARG;
+  const int64_t most = stride > budget ? stride - budget : 0;  // slots a sequence can free
+  if (out_stride < (stride < budget ? stride : budget)) return SDA_ERR_INVALID_ARG;
+  if (most * B > 0x7fffffffll || freed_capacity < most * B) return SDA_ERR_INVALID_ARG;
+  if (!freed_indptr || !status || (freed_capacity > 0 && !freed_slots)) return SDA_ERR_INVALID_ARG;
+  if (B > 0 && (!kv_len || !out_len)) return SDA_ERR_INVALID_ARG;
+  if (B > 0 && stride > 0 && (!scores || !slot_table)) return SDA_ERR_INVALID_ARG;
+  if (B > 0 && out_stride > 0 && (!out_scores || !out_table)) return SDA_ERR_INVALID_ARG;
+  const void* words[] = {scores, slot_table, kv_len, out_scores, out_table, out_len, freed_slots,
+                         freed_indptr, status};
+  for (const void* ptr : words)
+    if (!aligned(ptr, 4)) return SDA_ERR_INVALID_ARG;
+  // in place (same array, same row length) or apart
+  const size_t in = static_cast<size_t>(B) * stride * 4, on = static_cast<size_t>(B) * out_stride * 4;
+  const bool same = stride == out_stride;
+  if (!(same && scores == out_scores) && overlaps(scores, in, out_scores, on))
+    return SDA_ERR_INVALID_ARG;
+  if (!(same && slot_table == out_table) && overlaps(slot_table, in, out_table, on))
+    return SDA_ERR_INVALID_ARG;
+  const size_t bn = static_cast<size_t>(B) * 4;
+  if (out_len != kv_len && overlaps(kv_len, bn, out_len, bn)) return SDA_ERR_INVALID_ARG;
+  const EvictArgs a{scores,  slot_table,  stride,         kv_len,       B,     budget, first, recent,
+                    out_scores, out_table, out_stride, out_len, freed_slots, freed_capacity,
+                    freed_indptr, status};
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  DeviceCaps caps;
+  cudaError_t e = device_caps(&caps);
+  if (e == cudaSuccess && g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_before, st);
+  if (e == cudaSuccess) e = launch_evict(a, st);
+  if (e == cudaSuccess && g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_after, st);
+  if (e != cudaSuccess) {
+    note_cuda_error(e, "sda_evict_slots");
     return SDA_ERR_CUDA;
   }
   return SDA_OK;

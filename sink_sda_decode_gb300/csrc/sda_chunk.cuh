@@ -79,7 +79,61 @@ cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
 cudaError_t launch_chunk_combine(const float* attn_sink, const ChunkGeom& g, void* out, float* lse,
                                  const ChunkLayout& L, void* ws, cudaStream_t st);
 
+inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Attention mass.
+struct MassLayout {
+  size_t units_off, seq_off, cta_off, part_off, total;
+  int u_max, grid;
+};
+MassLayout mass_layout(int B, int64_t S, int num_sms);
+cudaError_t mass_prepare();
+cudaError_t launch_mass(const void* q, const void* kv, const ChunkGeom& g, const float* lse,
+                        float scale, const float* prev, float decay, float* out,
+                        const MassLayout& L, void* ws, cudaStream_t st);
+
 // sda_api.cu: the text that sda_last_cuda_error returns.
 void note_cuda_error(cudaError_t e, const char* where);
+
+#ifdef __CUDACC__
+// Exclusive scan over a block of 1024 threads; *total (shared) holds the sum.
+__device__ inline long long scan_exclusive(long long v, long long* warp_sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    const long long w = warp_sums[lane];
+    long long s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s - w;
+    if (lane == 31) *total = s;
+  }
+  __syncthreads();
+  const long long r = warp_sums[warp] + x - v;
+  __syncthreads();  // warp_sums is rewritten by the next call (*total after its first barrier)
+  return r;
+}
+
+// Last index i in [0, n) with a[i] <= x; a non-decreasing, a[0] <= x.
+__device__ __forceinline__ int last_le(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+#endif
 
 }  // namespace sda

@@ -19,44 +19,6 @@ constexpr int kPlanThreads = 1024;
 constexpr int kSmemUnits = 8192;  // units whose tile offsets are also kept in shared memory
 constexpr int kSmemSeqs = 2048;   // sequences whose unit offsets are kept in shared memory
 
-__device__ long long scan_exclusive(long long v, long long* warp_sums, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    const long long w = warp_sums[lane];
-    long long s = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s - w;
-    if (lane == 31) *total = s;
-  }
-  __syncthreads();
-  const long long r = warp_sums[warp] + x - v;
-  __syncthreads();  // warp_sums is rewritten by the next call (*total after its first barrier)
-  return r;
-}
-
-// Last index i in [0, n) with a[i] <= x; a non-decreasing, a[0] <= x.
-__device__ __forceinline__ int last_le(const int* a, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
     const ChunkGeom g, int R, int grid, int u_max, ChunkHeader* __restrict__ hdr,
     ChunkUnit* __restrict__ units, int* __restrict__ seq_unit, int* __restrict__ cta_unit) {
@@ -232,8 +194,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
 }
 
 }  // namespace
-
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms) {
   ChunkLayout L;

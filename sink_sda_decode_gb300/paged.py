@@ -1,4 +1,5 @@
-"""Operators on a paged cache: attention of a chunk of new tokens.
+"""Operators on a paged cache: attention of a chunk of new tokens, the weight
+that every cached position received, and eviction by that weight.
 
 A sequence's cached positions are found through a block table: position j of
 sequence b lies in pool row
@@ -14,6 +15,7 @@ j > p - window, or j < first.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -107,3 +109,127 @@ def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torc
             lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
     _lib.check(rc, "sda_chunk_attention")
     return out, lse
+
+
+def attention_mass_workspace_size(B: int, max_blocks: int, k_per_block: int) -> int:
+    """Bytes of workspace attention_mass() needs on the current CUDA device."""
+    lib = _lib.load()
+    n = ctypes.c_size_t(0)
+    _lib.check(lib.sda_attention_mass_workspace_size(_int32(B, "B"), _int32(max_blocks, "max_blocks"),
+                                                     _int32(k_per_block, "k_per_block", 1),
+                                                     ctypes.byref(n)),
+               "sda_attention_mass_workspace_size")
+    return int(n.value)
+
+
+def attention_mass(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torch.Tensor,
+                   q_indptr: torch.Tensor, kv_len: torch.Tensor, lse: torch.Tensor,
+                   softmax_scale: float, *, k_per_block: int, base: int = 0, window: int = 0,
+                   first: int = 0, scores: torch.Tensor | None = None, decay: float = 1.0,
+                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The attention weight every cached position received from the tokens in q.
+
+    The arguments and their meaning are chunk_attention()'s, whose `lse` [T, H]
+    this takes.  Returns out [B, S] fp32, S = max_blocks * k_per_block:
+
+        out[b, j] = decay * scores[b, j] + sum of softmax weights of position j
+                    over the tokens and heads of sequence b that see it
+
+    for j < kv_len[b] and 0 behind it.  `scores` [B, S] fp32 (None: zeros) may be
+    given as `out` too.  To rank positions by the last few tokens only, pass
+    those tokens (and their lse): they still stand at the end of the cache.
+    Deterministic.  Asynchronous on `stream`; with `out` and `workspace` (uint8,
+    attention_mass_workspace_size(...) bytes) given, the call can be captured.
+    """
+    from . import _req, _stream_ptr, _workspace_for
+    lib = _lib.load()
+    B, T, H, D = _tables(q, unified_kv, block_table, q_indptr, kv_len)
+    dev = q.device
+    S = block_table.shape[1] * _int32(k_per_block, "k_per_block", 1)
+    _req(lse, "lse", torch.float32, 2, dev)
+    if lse.shape != (T, H):
+        raise ValueError("lse must be [T, H]")
+    if out is None:
+        out = torch.empty(B, S, dtype=torch.float32, device=dev)
+    for name, t in (("scores", scores), ("out", out)):
+        if t is not None:
+            _req(t, name, torch.float32, 2, dev)
+            if t.shape != (B, S):
+                raise ValueError(f"{name} must be [B, max_blocks * k_per_block]")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = _workspace_for(
+                attention_mass_workspace_size(B, block_table.shape[1], k_per_block), dev, stream)
+        _req(workspace, "workspace", torch.uint8, 1, dev)
+        rc = lib.sda_attention_mass(
+            q.data_ptr(), unified_kv.data_ptr(), unified_kv.shape[0], block_table.data_ptr(),
+            block_table.shape[1], int(k_per_block), int(base), q_indptr.data_ptr(),
+            kv_len.data_ptr(), lse.data_ptr(), float(softmax_scale), _int32(window, "window"),
+            _int32(first, "first"), None if scores is None else scores.data_ptr(), float(decay), B,
+            T, H, D, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+    _lib.check(rc, "sda_attention_mass")
+    return out
+
+
+class Evicted(NamedTuple):
+    """What evict_slots() returns."""
+    scores: torch.Tensor        # [B, W] fp32, kept positions' scores, then 0
+    slot_table: torch.Tensor    # [B, W] int32, kept positions' slots, then -1
+    kv_len: torch.Tensor        # [B] int32
+    freed_slots: torch.Tensor   # int32, sequence by sequence, then -1
+    freed_indptr: torch.Tensor  # [B + 1] int32
+    status: torch.Tensor        # [1] int32: bits 1 (a bad length), 8 (a NaN competed)
+
+
+def evict_slots(scores: torch.Tensor, slot_table: torch.Tensor, kv_len: torch.Tensor, budget: int, *,
+                first: int = 0, recent: int = 0, out: Evicted | None = None,
+                stream: torch.cuda.Stream | None = None) -> Evicted:
+    """Cut every sequence's cache down to `budget` positions by score.
+
+    scores [B, S] fp32 and slot_table [B, S] int32 (a block table with
+    k_per_block = 1), kv_len [B] int32.  A sequence of more than `budget`
+    positions keeps its first `first`, its last `recent` and the best-scored
+    others, in their order; equal scores keep the lower position, NaN goes
+    first.  Returns an Evicted with tables of min(S, budget) columns.  `out`
+    (an Evicted of preallocated tensors) keeps the call free of allocations; its
+    scores, slot_table and kv_len may be the inputs themselves, which is the
+    update in place.  Asynchronous on `stream`.
+    """
+    from . import _req, _stream_ptr
+    lib = _lib.load()
+    _req(scores, "scores", torch.float32, 2)
+    dev = scores.device
+    _req(slot_table, "slot_table", torch.int32, 2, dev)
+    _req(kv_len, "kv_len", torch.int32, 1, dev)
+    B, S = scores.shape
+    if slot_table.shape != (B, S) or kv_len.numel() != B:
+        raise ValueError("scores and slot_table must be [B, S] and kv_len [B]")
+    budget = _int32(budget, "budget")
+    freed = B * max(S - budget, 0)
+    if out is None:
+        W = min(S, budget)
+        i32 = dict(dtype=torch.int32, device=dev)
+        out = Evicted(torch.empty(B, W, dtype=torch.float32, device=dev), torch.empty(B, W, **i32),
+                      torch.empty(B, **i32), torch.empty(freed, **i32), torch.empty(B + 1, **i32),
+                      torch.empty(1, **i32))
+    else:
+        _req(out.scores, "out.scores", torch.float32, 2, dev)
+        for name in ("slot_table", "kv_len", "freed_slots", "freed_indptr", "status"):
+            _req(getattr(out, name), f"out.{name}", torch.int32, 2 if name == "slot_table" else 1, dev)
+        if out.scores.shape != out.slot_table.shape or out.scores.shape[0] != B:
+            raise ValueError("out.scores and out.slot_table must be [B, W]")
+        if out.kv_len.numel() != B or out.freed_indptr.numel() != B + 1 or out.status.numel() != 1:
+            raise ValueError("out.kv_len must be [B], out.freed_indptr [B + 1] and out.status [1]")
+        if out.scores.shape[1] < min(S, budget) or out.freed_slots.numel() < freed:
+            raise ValueError("out's tables need min(S, budget) columns and freed_slots "
+                             "B * max(S - budget, 0) entries")
+    with torch.cuda.device(dev):
+        rc = lib.sda_evict_slots(
+            scores.data_ptr(), slot_table.data_ptr(), S, kv_len.data_ptr(), B, budget,
+            _int32(first, "first"), _int32(recent, "recent"), out.scores.data_ptr(),
+            out.slot_table.data_ptr(), out.scores.shape[1], out.kv_len.data_ptr(),
+            out.freed_slots.data_ptr(), out.freed_slots.numel(), out.freed_indptr.data_ptr(),
+            out.status.data_ptr(), _stream_ptr(stream))
+    _lib.check(rc, "sda_evict_slots")
+    return out

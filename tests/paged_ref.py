@@ -107,3 +107,54 @@ class Case:
         return sda.chunk_attention(self.q, self.pool, self.table, self.q_indptr, self.kv_len,
                                    self.sink, self.scale, k_per_block=self.K, base=self.base,
                                    window=self.window, first=self.first, **kw)
+
+
+def mass(c, lse, prev=None, decay=1.0):
+    """out [B, S] and how far each entry may be off.  An fp32 sum of N terms in a
+    fixed order, in groups, is off by at most (N + 2) * 2^-24 of the sum of sizes."""
+    S = c.table.shape[1] * c.K
+    out = torch.zeros(c.B, S, dtype=torch.float64)
+    if prev is not None:
+        out += decay * prev.cpu().double()
+    for b in range(c.B):
+        out[b, c.n[b]:] = 0
+    tol = out.abs() * 2.0 ** -22
+    for b in range(c.B):
+        s = slice(c.q_indptr_l[b], c.q_indptr_l[b + 1])
+        if s.stop == s.start or c.n[b] == 0:
+            continue
+        x, _, see, delta = logits(c, b)
+        z = lse.cpu().double()[s][..., None]
+        w = torch.where(see & (z != float("inf")), torch.exp(x - z), torch.zeros_like(x))
+        N = x.shape[0] * x.shape[1]
+        out[b, :c.n[b]] += w.sum(dim=(0, 1))
+        # the argument of 2^x is rounded to 2^-24 of its size, its result to about 2^-21
+        arg = torch.where(see, x.abs() + z.abs(), torch.zeros_like(x)).nan_to_num(posinf=0.0)
+        rel = delta[..., None] + arg * 2.0 ** -22 + 2.0 ** -21 + (N + 2) * 2.0 ** -24
+        tol[b, :c.n[b]] += torch.where(w > 0, w * rel, w).sum(dim=(0, 1)) + 2.0 ** -120 * N
+    return out, tol
+
+
+def evict(scores, slots, lens, budget, first, recent, W):
+    """The definition, sequence by sequence, with Python's own sort."""
+    B, S = scores.shape
+    s, t = scores.cpu().numpy(), slots.cpu().numpy()
+    os, ot = np.zeros((B, W), np.float32), np.full((B, W), -1, np.int32)
+    ol, freed, ptr, status = [], [], [0], 0
+    for b in range(B):
+        n = int(lens[b])
+        if n < 0 or n > S:
+            n, status = 0, status | 1
+        kept = list(range(n))
+        if n > budget:
+            mid = list(range(first, n - recent))
+            if any(np.isnan(s[b, j]) for j in mid):
+                status |= 8
+            mid.sort(key=lambda j: (np.isnan(s[b, j]), 0.0 if np.isnan(s[b, j]) else -float(s[b, j]), j))
+            kept = sorted(list(range(first)) + mid[:budget - first - recent] + list(range(n - recent, n)))
+        os[b, :len(kept)], ot[b, :len(kept)] = s[b, kept], t[b, kept]
+        gone = sorted(set(range(n)) - set(kept))
+        freed += [int(t[b, j]) for j in gone]
+        ptr.append(len(freed))
+        ol.append(len(kept))
+    return os, ot, ol, freed, ptr, status
