@@ -86,6 +86,8 @@ class SdaError(RuntimeError):
 def load():
     """Load libsda.so (built by ``python -m sink_sda_decode_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

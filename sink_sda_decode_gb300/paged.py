@@ -14,12 +14,50 @@ j > p - window, or j < first.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
 
 from . import _lib
+
+
+def _need(t, name: str, dtype, ndim: int, dev=None):
+    """_req() with the checks of a good tensor in one expression: these run on
+    every step of a decode loop."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_cuda
+            and t.is_contiguous() and (dev is None or t.device == dev)):
+        from . import _req
+        _req(t, name, dtype, ndim, dev)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev):
+    """Makes dev the current device, at no cost where it is already."""
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _stream_of(dev, stream) -> int:
+    return (stream.cuda_stream if stream is not None
+            else torch._C._cuda_getCurrentRawStream(dev.index))
+
+
+def _workspace(nbytes, dev, stream) -> torch.Tensor:
+    """A workspace that torch's allocator knows is in use on `stream`."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if isinstance(stream, torch.cuda.Stream):
+        ws.record_stream(stream)
+    return ws
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(device: int, size, *args) -> int:
+    """A workspace size depends on the device's SM count and these sizes only."""
+    return size(*args)
 
 
 def _int32(v, name: str, low: int = 0) -> int:
@@ -31,13 +69,12 @@ def _int32(v, name: str, low: int = 0) -> int:
 
 def _tables(q, unified_kv, block_table, q_indptr, kv_len):
     """Checks the tensors that the paged operators share; returns (B, T, H, D)."""
-    from . import _req
-    _req(q, "q", torch.bfloat16, 3)
+    _need(q, "q", torch.bfloat16, 3)
     dev = q.device
-    _req(unified_kv, "unified_kv", torch.bfloat16, 2, dev)
-    _req(block_table, "block_table", torch.int32, 2, dev)
-    _req(q_indptr, "q_indptr", torch.int32, 1, dev)
-    _req(kv_len, "kv_len", torch.int32, 1, dev)
+    _need(unified_kv, "unified_kv", torch.bfloat16, 2, dev)
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    _need(q_indptr, "q_indptr", torch.int32, 1, dev)
+    _need(kv_len, "kv_len", torch.int32, 1, dev)
     T, H, D = q.shape
     B = kv_len.numel()
     if unified_kv.shape[1] != D:
@@ -82,31 +119,36 @@ def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torc
     (2: lengths outside the contract, nothing computed; 3: a table entry
     outside the pool).
     """
-    from . import _req, _stream_ptr, _workspace_for
     lib = _lib.load()
     B, T, H, D = _tables(q, unified_kv, block_table, q_indptr, kv_len)
     dev = q.device
-    _req(attn_sink, "attn_sink", torch.float32, 1, dev)
+    _need(attn_sink, "attn_sink", torch.float32, 1, dev)
     if attn_sink.numel() != H:
         raise ValueError("attn_sink must have H entries")
     if out is None:
         out = torch.empty_like(q)
-    _req(out, "out", torch.bfloat16, 3, dev)
+    else:
+        _need(out, "out", torch.bfloat16, 3, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
     if lse is None:
         lse = torch.empty(T, H, dtype=torch.float32, device=dev)
-    _req(lse, "lse", torch.float32, 2, dev)
-    if out.shape != q.shape or lse.shape != (T, H):
-        raise ValueError("out must have q's shape and lse be [T, H]")
-    with torch.cuda.device(dev):
+    else:
+        _need(lse, "lse", torch.float32, 2, dev)
+        if lse.shape != (T, H):
+            raise ValueError("lse must be [T, H]")
+    with _on(dev):
         if workspace is None:
-            workspace = _workspace_for(chunk_attention_workspace_size(B, T, H, D), dev, stream)
-        _req(workspace, "workspace", torch.uint8, 1, dev)
+            workspace = _workspace(
+                _workspace_bytes(dev.index, chunk_attention_workspace_size, B, T, H, D), dev, stream)
+        else:
+            _need(workspace, "workspace", torch.uint8, 1, dev)
         rc = lib.sda_chunk_attention(
             q.data_ptr(), unified_kv.data_ptr(), unified_kv.shape[0], block_table.data_ptr(),
             block_table.shape[1], _int32(k_per_block, "k_per_block", 1), int(base),
             q_indptr.data_ptr(), kv_len.data_ptr(), attn_sink.data_ptr(), float(softmax_scale),
             _int32(window, "window"), _int32(first, "first"), B, T, H, D, out.data_ptr(),
-            lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+            lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(dev, stream))
     _lib.check(rc, "sda_chunk_attention")
     return out, lse
 
@@ -142,32 +184,33 @@ def attention_mass(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torch
     Deterministic.  Asynchronous on `stream`; with `out` and `workspace` (uint8,
     attention_mass_workspace_size(...) bytes) given, the call can be captured.
     """
-    from . import _req, _stream_ptr, _workspace_for
     lib = _lib.load()
     B, T, H, D = _tables(q, unified_kv, block_table, q_indptr, kv_len)
     dev = q.device
     S = block_table.shape[1] * _int32(k_per_block, "k_per_block", 1)
-    _req(lse, "lse", torch.float32, 2, dev)
+    _need(lse, "lse", torch.float32, 2, dev)
     if lse.shape != (T, H):
         raise ValueError("lse must be [T, H]")
-    if out is None:
-        out = torch.empty(B, S, dtype=torch.float32, device=dev)
     for name, t in (("scores", scores), ("out", out)):
         if t is not None:
-            _req(t, name, torch.float32, 2, dev)
+            _need(t, name, torch.float32, 2, dev)
             if t.shape != (B, S):
                 raise ValueError(f"{name} must be [B, max_blocks * k_per_block]")
-    with torch.cuda.device(dev):
+    if out is None:
+        out = torch.empty(B, S, dtype=torch.float32, device=dev)
+    with _on(dev):
         if workspace is None:
-            workspace = _workspace_for(
-                attention_mass_workspace_size(B, block_table.shape[1], k_per_block), dev, stream)
-        _req(workspace, "workspace", torch.uint8, 1, dev)
+            workspace = _workspace(
+                _workspace_bytes(dev.index, attention_mass_workspace_size, B, block_table.shape[1],
+                                 k_per_block), dev, stream)
+        else:
+            _need(workspace, "workspace", torch.uint8, 1, dev)
         rc = lib.sda_attention_mass(
             q.data_ptr(), unified_kv.data_ptr(), unified_kv.shape[0], block_table.data_ptr(),
             block_table.shape[1], int(k_per_block), int(base), q_indptr.data_ptr(),
             kv_len.data_ptr(), lse.data_ptr(), float(softmax_scale), _int32(window, "window"),
             _int32(first, "first"), None if scores is None else scores.data_ptr(), float(decay), B,
-            T, H, D, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+            T, H, D, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(dev, stream))
     _lib.check(rc, "sda_attention_mass")
     return out
 
@@ -196,12 +239,11 @@ def evict_slots(scores: torch.Tensor, slot_table: torch.Tensor, kv_len: torch.Te
     scores, slot_table and kv_len may be the inputs themselves, which is the
     update in place.  Asynchronous on `stream`.
     """
-    from . import _req, _stream_ptr
     lib = _lib.load()
-    _req(scores, "scores", torch.float32, 2)
+    _need(scores, "scores", torch.float32, 2)
     dev = scores.device
-    _req(slot_table, "slot_table", torch.int32, 2, dev)
-    _req(kv_len, "kv_len", torch.int32, 1, dev)
+    _need(slot_table, "slot_table", torch.int32, 2, dev)
+    _need(kv_len, "kv_len", torch.int32, 1, dev)
     B, S = scores.shape
     if slot_table.shape != (B, S) or kv_len.numel() != B:
         raise ValueError("scores and slot_table must be [B, S] and kv_len [B]")
@@ -209,14 +251,17 @@ def evict_slots(scores: torch.Tensor, slot_table: torch.Tensor, kv_len: torch.Te
     freed = B * max(S - budget, 0)
     if out is None:
         W = min(S, budget)
-        i32 = dict(dtype=torch.int32, device=dev)
-        out = Evicted(torch.empty(B, W, dtype=torch.float32, device=dev), torch.empty(B, W, **i32),
-                      torch.empty(B, **i32), torch.empty(freed, **i32), torch.empty(B + 1, **i32),
-                      torch.empty(1, **i32))
+        i32 = torch.int32
+        out = Evicted(torch.empty(B, W, dtype=torch.float32, device=dev),
+                      torch.empty(B, W, dtype=i32, device=dev),
+                      torch.empty(B, dtype=i32, device=dev),
+                      torch.empty(freed, dtype=i32, device=dev),
+                      torch.empty(B + 1, dtype=i32, device=dev),
+                      torch.empty(1, dtype=i32, device=dev))
     else:
-        _req(out.scores, "out.scores", torch.float32, 2, dev)
+        _need(out.scores, "out.scores", torch.float32, 2, dev)
         for name in ("slot_table", "kv_len", "freed_slots", "freed_indptr", "status"):
-            _req(getattr(out, name), f"out.{name}", torch.int32, 2 if name == "slot_table" else 1, dev)
+            _need(getattr(out, name), f"out.{name}", torch.int32, 2 if name == "slot_table" else 1, dev)
         if out.scores.shape != out.slot_table.shape or out.scores.shape[0] != B:
             raise ValueError("out.scores and out.slot_table must be [B, W]")
         if out.kv_len.numel() != B or out.freed_indptr.numel() != B + 1 or out.status.numel() != 1:
@@ -224,12 +269,12 @@ def evict_slots(scores: torch.Tensor, slot_table: torch.Tensor, kv_len: torch.Te
         if out.scores.shape[1] < min(S, budget) or out.freed_slots.numel() < freed:
             raise ValueError("out's tables need min(S, budget) columns and freed_slots "
                              "B * max(S - budget, 0) entries")
-    with torch.cuda.device(dev):
+    with _on(dev):
         rc = lib.sda_evict_slots(
             scores.data_ptr(), slot_table.data_ptr(), S, kv_len.data_ptr(), B, budget,
             _int32(first, "first"), _int32(recent, "recent"), out.scores.data_ptr(),
             out.slot_table.data_ptr(), out.scores.shape[1], out.kv_len.data_ptr(),
             out.freed_slots.data_ptr(), out.freed_slots.numel(), out.freed_indptr.data_ptr(),
-            out.status.data_ptr(), _stream_ptr(stream))
+            out.status.data_ptr(), _stream_of(dev, stream))
     _lib.check(rc, "sda_evict_slots")
     return out
