@@ -37,18 +37,17 @@ struct alignas(16) ChunkUnit {
   int lo;       // positions below lo are visible only if they are below `first`
   int hi;       // positions from hi on are visible to no row
   int nf;       // KV tiles of the first positions (those below lo's tile)
-  int ntiles;   // KV tiles of 64 positions: tiles 0..nf-1, then from lo / 64 on (>= 1)
+  int ntiles;   // KV tiles: tiles 0..nf-1, then from the one that holds lo on (>= 1)
   int cum;      // KV tiles of all earlier units
   int pad0, pad1;
 };
 static_assert(sizeof(ChunkUnit) == 48, "three 16-byte words");
 
-constexpr int kChunkTile = 64;  // positions per KV tile
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The position that logical tile i of a unit starts at.
-__host__ __device__ inline int chunk_tile_start(int i, int nf, int lo) {
-  return (i < nf ? i : lo / kChunkTile + i - nf) * kChunkTile;
+// The position that logical tile i of a unit starts at, with tiles of `tile` positions.
+__host__ __device__ inline int chunk_tile_start(int i, int nf, int lo, int tile) {
+  return (i < nf ? i : lo / tile + i - nf) * tile;
 }
 
 // Header of the workspace.
@@ -66,8 +65,14 @@ static_assert(offsetof(ChunkHeader, error) == offsetof(WsHeader, error),
 
 struct ChunkLayout {
   size_t units_off, seq_off, cta_off, ml_off, o_off, total;
-  int u_max, grid, R;
+  int u_max, grid, R, tile;
 };
+// Positions per KV tile (a multiple of 16).  With 64 rows of q at D = 512 two
+// stages of 64 positions fit beside q, or three of 48: the tensor pipe needs
+// 7 % more cycles a position with 48 (it reads q more often), but a tile's load,
+// scores, softmax and PV take longer than two tiles' MMAs, and three in flight
+// keep the pipe busier (attend of a 2048-token chunk over 8192 positions).
+constexpr int chunk_tile(int R, int D) { return R == 64 && D == 512 ? 48 : 64; }
 // The layout for B sequences, T tokens: R rows per unit is a function of them.
 ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms);
 

@@ -12,14 +12,16 @@
 //
 // One persistent CTA per SM owns a contiguous range of KV tiles (the plan,
 // sda_chunk_plan.cu).  Roles:
-//   warps 0..7    softmax and epilogue; thread 0 issues the PV MMAs
-//   warps 8..23   KV rows: each warp copies 4 rows of every tile with 16-byte
-//                 cp.async into a 128-byte-swizzled stage
-//   warps 24, 26  QK MMAs, one half of D each (D <= 128: warp 24 alone); warp
-//                 24 loads q by TMA
-// S = Q K^T (M = 64 rows, N = 64 positions) and O^T += V^T P^T (M = 128 of D,
-// N = R rows, K = 64 positions) read the same shared tile, K-major as K and
-// MN-major as V.
+//   warps 0..7   softmax and epilogue
+//   warp 8       QK MMAs and the q loads (TMA)
+//   warp 9       PV MMAs
+//   warp 10      KV tiles by TMA where blocks hold whole groups of 8 rows
+//   warps 12..   (gather kernel, other block sizes) 8 warps copy the tile's rows
+//                one by one with 16-byte cp.async
+// S = Q K^T (M = 64 rows, N = a tile of positions) and O^T += V^T P^T (M = 128
+// of D, N = R rows, K = the positions) read the same shared tile, K-major as K
+// and MN-major as V.  A tile lies as groups of 8 rows, each group D / 64
+// swizzle atoms of 1 KB.
 #include <cuda_bf16.h>
 
 #include "sda_chunk.cuh"
@@ -31,55 +33,49 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTile = kChunkTile;          // 64 positions per KV tile
-constexpr int kPanel = kTile * 128;        // bytes of one 64-column panel of a KV tile
 constexpr int kSmWarps = 8;
 constexpr int kSmThreads = kSmWarps * 32;
-constexpr int kLoadWarp0 = 8;
-constexpr int kLoadWarps = 16;
-constexpr int kMmaWarp = 24;
-constexpr int kMmaWarpB = 26;
-constexpr int kThreads = 896;
-// Registers: the launch gives 72 a thread (65536 / 896, rounded down to 8);
-// the softmax warps grow, the others shrink.
-constexpr int kLaunchRegs = 72;
-constexpr int kSmRegs = 104, kLoadRegs = 56, kMmaRegs = 56;
-static_assert(kSmThreads * kSmRegs + kLoadWarps * 32 * kLoadRegs + 128 * kMmaRegs <=
-                  kThreads * kLaunchRegs,
+constexpr int kQkWarp = 8, kPvWarp = 9, kTmaWarp = 10;
+constexpr int kLoadWarp0 = 12, kLoadWarps = 8;  // gather kernel only
+constexpr int kMaxStages = 6;
+// Gather kernel: 640 threads launch with 96 registers each; the softmax warps
+// grow to 128 and the loaders shrink to 64 (the MMA warpgroup keeps 96).
+constexpr int kGatherThreads = 640, kGatherRegs = 96;
+static_assert(kSmThreads * 128 + kLoadWarps * 32 * 64 + 128 * 96 <= kGatherThreads * kGatherRegs,
               "register split exceeds the launch allocation");
-constexpr int kMaxStages = 5;
 constexpr float kHeadroom = 8.0f;  // log2: the running reference is raised when a score exceeds it by this
 
 enum Bar : int {
   kQFull = 0,
   kQEmpty,
-  kKvFull0,                              // + 2 * stage + half
-  kPvDone0 = kKvFull0 + 2 * kMaxStages,  // + 2 * stage + half
-  kSFull0 = kPvDone0 + 2 * kMaxStages,
+  kSFull0,
   kSEmpty0 = kSFull0 + 2,
-  kDrainA = kSEmpty0 + 2,
-  kDrainB,
+  kPReady0 = kSEmpty0 + 2,
+  kDrainQk = kPReady0 + 2,
   kDrainPv,
-  kBars
+  kKvFull0,                              // + 2 * stage + half of D
+  kPvDone0 = kKvFull0 + 2 * kMaxStages,  // + 2 * stage + half of D
+  kBars = kPvDone0 + 2 * kMaxStages
 };
 
 template <int R, int D>
 struct Cfg {
+  static constexpr int kTile = chunk_tile(R, D);
   static constexpr int kPanels = D / 64;
   static constexpr int kBlocks = (D + 127) / 128;    // 128-row blocks of O^T
   static constexpr int kHalves = D >= 256 ? 2 : 1;   // a stage is filled and freed in halves of D
   static constexpr int kPanelsH = kPanels / kHalves, kBlocksH = kBlocks / kHalves;
-  static constexpr int kStage = kPanels * kPanel;
-  static constexpr int kStages = D == 512 ? (R == 16 ? 3 : 2) : (D == 256 ? 4 : 5);
+  static constexpr int kGroup = kPanels * 1024;      // bytes of 8 rows
+  static constexpr int kGroups = kTile / 8;
+  static constexpr int kStage = kGroups * kGroup;
+  static constexpr int kStages = D == 512 ? 3 : (D == 256 ? 5 : 6);
   static constexpr int kPanelQ = R * 128;
   static constexpr int kPBytes = R * 128;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = kPanels * kPanelQ;
-  static constexpr int kOffP = kOffKV + kStages * kStage;
-  // output staging: area 0 is the two P buffers, area 1 follows
-  static constexpr int kOffStage2 = kOffP + 2 * kPBytes;
-  static constexpr int kOffBar = kOffStage2 + R * 256;
-  static constexpr int kOffMisc = kOffBar + 256;
+  static constexpr int kOffP = kOffKV + kStages * kStage;  // two P buffers; the epilogue's staging
+  static constexpr int kOffBar = kOffP + 2 * kPBytes;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kOffLSum = kOffMisc + 16;        // float [2][64]
   static constexpr int kOffAlpha = kOffLSum;            // aliases the first half (used inside a unit)
   static constexpr int kOffFac = kOffLSum + 4 * 64;     // aliases the second half
@@ -87,19 +83,17 @@ struct Cfg {
   // The QK MMA reads 64 rows of a q panel and the PV MMA 128 columns of D
   // whatever R and D are: what lies behind (other panels and stages, valid
   // shared memory) lands in TMEM lanes that nothing reads.
-  static constexpr int kReach = kOffKV + kStages * kStage + kPanel;
   static constexpr int kUsed = kOffHMax + 4 * 256;
-  static constexpr int kSmem = (kUsed > kReach ? kUsed : kReach) + 1024;
-  static constexpr int kSbCol = 128 + kBlocks * R;  // S of the second half, after O^T
-  static constexpr int kNeedCols = kSbCol + (kHalves == 2 ? 128 : 0);
-  static constexpr int kTmemCols = kNeedCols <= 256 ? 256 : 512;
+  static constexpr int kSmem = kUsed + 1024;
   static constexpr int kOCol = 128;
-  static constexpr uint32_t kIdescQK = idesc_bf16_f32(64, 64, false, false);
+  static constexpr int kTmemCols = kOCol + kBlocks * R <= 256 ? 256 : 512;
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(64, kTile, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, R, true, false);
-  static_assert(kNeedCols <= 512, "TMEM columns");
+  static_assert(kOCol + kBlocks * R <= 512, "TMEM columns");
   static_assert(kOffKV % 1024 == 0 && kOffP % 1024 == 0 && kPBytes % 1024 == 0, "swizzle atoms");
   static_assert((kPanels - 1) * kPanelQ + 64 * 128 <= kOffBar, "padded QK operand inside smem");
-  static_assert(kBars * 8 <= 256, "mbarrier area");
+  static_assert(D >= 128 || 2 * kPBytes >= 1024, "padded PV operand inside smem");
+  static_assert(kTile % 16 == 0 && kTile <= 64, "MMA shapes");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -157,12 +151,14 @@ struct Cursor {
   }
 };
 
-template <int R, int D>
-__global__ void __launch_bounds__(kThreads, 1)
-chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
+template <int R, int D, bool TMA>
+__global__ void __launch_bounds__(TMA ? 384 : kGatherThreads, 1)
+chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                  const __grid_constant__ CUtensorMap tmap_kv, const Params p) {
   using C = Cfg<R, D>;
   constexpr int KS = C::kStages;
   constexpr int HV = C::kHalves;
+  constexpr int kTile = C::kTile;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -174,28 +170,29 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
   auto kv_full = [&](int s, int h) { return bar(kKvFull0 + 2 * s + h); };
   auto pv_done = [&](int s, int h) { return bar(kPvDone0 + 2 * s + h); };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar(kQFull), 1);
-    mbar_init(bar(kQEmpty), HV);
+    mbar_init(bar(kQEmpty), 1);
     for (int s = 0; s < KS; ++s) {
       for (int h = 0; h < HV; ++h) {
-        mbar_init(kv_full(s, h), kLoadWarps);
+        mbar_init(kv_full(s, h), TMA ? 1 : kLoadWarps);
         mbar_init(pv_done(s, h), 1);
       }
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(kSFull0 + s), HV);
+      mbar_init(bar(kSFull0 + s), 1);
       mbar_init(bar(kSEmpty0 + s), kSmWarps);
+      mbar_init(bar(kPReady0 + s), 1);
     }
-    mbar_init(bar(kDrainA), 1);
-    mbar_init(bar(kDrainB), 1);
+    mbar_init(bar(kDrainQk), 1);
     mbar_init(bar(kDrainPv), 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmap_q);
+    if (TMA) tma_prefetch_desc(&tmap_kv);
   }
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
@@ -205,34 +202,99 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // everything above overlaps the plan; global memory only below
   pdl_trigger();
-  const int per = p.hdr->per, n_tiles = p.hdr->n_tiles;
+  const int per = __ldcg(&p.hdr->per), n_tiles = __ldcg(&p.hdr->n_tiles);
   const long long t0l = (long long)blockIdx.x * per;
   const int t0 = (int)min(t0l, (long long)n_tiles);
   const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // this CTA's tiles
-  const int u0 = p.cta_unit[blockIdx.x];
+  const int u0 = __ldcg(p.cta_unit + blockIdx.x);
   const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
 
-  if (warp >= kLoadWarp0 && warp < kLoadWarp0 + kLoadWarps) {
-    // ===================================================== KV rows
-    setmaxnreg_dec<kLoadRegs>();
-    constexpr int kRows = kTile / kLoadWarps;          // 4 rows per warp and tile
+  // Pool row of position j of the cursor's unit; -1: no row of the unit sees
+  // it (it is not read: zeros).
+  auto row_of = [&](const Cursor& c, int j) {
+    if (j >= c.hi || (j < c.lo && j >= p.g.first)) return -1;
+    const int blk = __ldg(p.g.block_table + (size_t)c.b * p.g.max_blocks + j / p.g.k_per_block);
+    const long long s = p.g.base + (long long)blk * p.g.k_per_block + j % p.g.k_per_block;
+    if (blk < 0 || s >= p.g.total_pages) {
+      atomicExch(&p.hdr->error, 3);
+      return -1;
+    }
+    return (int)s;
+  };
+
+  if (TMA && warp == kTmaWarp) {
+    // ===================================================== KV tiles by TMA
+    // A group of 8 positions lies in one block (both start at multiples of 8)
+    // and so in 8 pool rows in a row: lane i < kGroups loads group i of every
+    // tile, each half of D as soon as the PV MMAs that last read it are done,
+    // and brings its group of the tile two ahead into L2.  A group that no row
+    // sees is read from behind the pool, which fills it with zeros.
+    auto first_row = [&](const Cursor& c) {
+      if (lane >= C::kGroups) return -1;
+      const int j = chunk_tile_start(c.i, c.nf, c.lo, kTile) + lane * 8;
+      // the group's first position that is seen, if any, tells its block
+      int x = j;
+      if (x < c.lo && x >= p.g.first) x = c.lo;
+      if (x >= j + 8) return -1;
+      const int r = row_of(c, x);
+      return r < 0 ? -1 : r - (x - j);
+    };
+    auto prefetch = [&](int row) {
+      if (row >= 0)
+        bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + (size_t)row * D * 2,
+                         (uint32_t)min((long long)8, (long long)p.g.total_pages - row) * D * 2);
+    };
+    Cursor c;  // runs two tiles ahead of the copies
+    c.init(p.units, u0, t0, nt);
+    int r0 = -1, r1 = -1;
+    if (c.left > 0) {
+      r0 = first_row(c);
+      c.next();
+    }
+    if (c.left > 0) {
+      r1 = first_row(c);
+      c.next();
+    }
+    prefetch(r1);
+    bool ok = true;
+    int loads = 0;
+    for (int g = 0; g < nt && ok; ++g) {
+      const int s = g % KS;
+      int r2 = -1;
+      if (c.left > 0) {
+        r2 = first_row(c);
+        c.next();
+      }
+      const int y = r0 >= 0 ? r0 : (int)p.g.total_pages;
+#pragma unroll
+      for (int h = 0; h < HV; ++h) {
+        if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(kv_full(s, h), C::kStage / HV);
+        __syncwarp();
+        if (lane < C::kGroups)
+          tma_load_3d(sKV + s * C::kStage + lane * C::kGroup + h * C::kPanelsH * 1024, &tmap_kv, 0, y,
+                      h * C::kPanelsH, kv_full(s, h));
+        ++loads;
+      }
+      prefetch(r2);
+      r0 = r1;
+      r1 = r2;
+    }
+    // copies in flight land before the CTA's memory goes away (the last KS stages)
+    for (int x = max(0, loads - KS * HV); x < loads; ++x)
+      pipe_drain(kv_full((x / HV) % KS, x % HV), (x / HV / KS) & 1, wc);
+  } else if (!TMA && warp >= kLoadWarp0) {
+    // ===================================================== KV rows one by one
+    setmaxnreg_dec<64>();
+    constexpr int kRows = kTile / kLoadWarps;          // 6 or 8 rows per warp and tile
     constexpr int kCh = D / 8 / HV;                    // 16-byte chunks of a row's half
     constexpr int kRowsPer = 32 / kCh;                 // rows per warp-wide copy
     const int v = warp - kLoadWarp0;
     const uint4* kv4 = reinterpret_cast<const uint4*>(p.kv);
-    // lanes 0..3: the pool row of position 4v + lane of the cursor's tile; -1:
-    // a position that no row of the unit sees (it is not read: zeros).
-    auto slot_of = [&](const Cursor& c) {
-      if (lane >= kRows) return -1;
-      const int j = chunk_tile_start(c.i, c.nf, c.lo) + v * kRows + lane;
-      if (j >= c.hi || (j < c.lo && j >= p.g.first)) return -1;
-      const int blk = __ldg(p.g.block_table + (size_t)c.b * p.g.max_blocks + j / p.g.k_per_block);
-      const long long s = p.g.base + (long long)blk * p.g.k_per_block + j % p.g.k_per_block;
-      if (blk < 0 || s >= p.g.total_pages) {
-        atomicExch(&p.hdr->error, 3);
-        return -1;
-      }
-      return (int)s;
+    auto slot_of = [&](const Cursor& c) {  // lanes 0 .. kRows - 1: rows kRows v + lane
+      return lane < kRows ? row_of(c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + v * kRows + lane) : -1;
     };
     auto prefetch = [&](int slot) {
       if (slot >= 0) bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + (size_t)slot * D * 2, D * 2);
@@ -261,21 +323,19 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
       int issued = 0;
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        if (g >= KS) {
-          if (lane == 0) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-        }
+        if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         const int ch = h * kCh + lane % kCh;  // 16-byte chunk of the row: panel ch / 8
 #pragma unroll
-        for (int r0 = 0; r0 < kRows; r0 += kRowsPer) {
-          const int r = r0 + lane / kCh;
-          const int slot = __shfl_sync(0xffffffffu, sl0, r);
-          const int r8 = 4 * (v & 1) + r;
-          const uint32_t dst = stage + (ch >> 3) * kPanel + (v >> 1) * 1024 + r8 * 128 +
-                               (((ch & 7) ^ r8) << 4);
+        for (int x = 0; x < kRows; x += kRowsPer) {
+          const int rl = x + lane / kCh;  // (past the warp's rows where kRowsPer does not divide them)
+          const int slot = __shfl_sync(0xffffffffu, sl0, rl & 31);
+          const int r = v * kRows + rl;
+          const uint32_t dst = stage + (r >> 3) * C::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 +
+                               (((ch & 7) ^ (r & 7)) << 4);
           const uint4* src = slot >= 0 ? kv4 + (size_t)slot * (D / 8) + ch : kv4;
-          cp_async16(dst, src, slot >= 0 ? 16u : 0u);
+          if (rl < kRows) cp_async16(dst, src, slot >= 0 ? 16u : 0u);
         }
         cp_async_commit();
         ++issued;
@@ -296,67 +356,106 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
       sl0 = sl1;
       sl1 = sl2;
     }
-  } else if (warp >= kMmaWarp) {
+  } else if (warp == kQkWarp) {
     // ===================================================== QK MMAs
-    setmaxnreg_dec<kMmaRegs>();
-    const int qh = warp == kMmaWarpB ? 1 : 0;  // half of D
-    if (lane == 0 && (warp == kMmaWarp || (HV == 2 && warp == kMmaWarpB))) {
-      Cursor c;
-      c.init(p.units, u0, t0, nt);
-      int q_loads = 0;
-      bool ok = true;
-      auto load_q = [&]() {
+    Cursor c;
+    c.init(p.units, u0, t0, nt);
+    int pieces = 0, q_loads = 0;
+    bool ok = true;
+    auto load_q = [&]() {
+      const int row = __ldcg(&p.units[c.u].row0);
+      if (elect_one()) {
         mbar_arrive_expect_tx(bar(kQFull), C::kPanels * C::kPanelQ);
-        const int row = __ldcg(&p.units[c.u].row0);
 #pragma unroll
         for (int x = 0; x < C::kPanels; ++x)
           tma_load_2d(sQ + x * C::kPanelQ, &tmap_q, x * 64, row, bar(kQFull));
-        ++q_loads;
-      };
-      if (qh == 0 && c.left > 0) load_q();
-      int nu = 0;  // pieces seen
-      for (int g = 0; g < nt && ok; ++g) {
-        const int s = g & 1, ks = g % KS;
-        if (g >= 2) ok = pipe_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
-        if (ok && c.first) ok = pipe_wait(bar(kQFull), nu & 1, wc);
-        if (ok) ok = pipe_wait(kv_full(ks, qh), (g / KS) & 1, wc);
+      }
+      __syncwarp();
+      ++q_loads;
+    };
+    if (c.left > 0) load_q();
+    const uint64_t a0 = sdesc_sw128(sQ, 16, 1024);
+    for (int g = 0; g < nt; ++g) {
+      const int s = g & 1, ks = g % KS;
+      if (g >= 2) ok = pipe_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
+      if (ok && c.first) ok = pipe_wait(bar(kQFull), pieces & 1, wc);
+      const uint64_t b0 = sdesc_sw128(sKV + ks * C::kStage, 16, C::kGroup);
+      const bool last = c.last();
+#pragma unroll
+      for (int h = 0; h < HV; ++h) {
+        if (ok) ok = pipe_wait(kv_full(ks, h), (g / KS) & 1, wc);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t a0 = sdesc_sw128(sQ, 16, 1024);
-        const uint64_t b0 = sdesc_sw128(sKV + ks * C::kStage, 16, 1024);
-        const uint32_t acc = tmem + (qh ? C::kSbCol : 0) + s * 64;
+        if (elect_one()) {
 #pragma unroll
-        for (int x = 0; x < C::kPanelsH; ++x) {
-          const int pn = qh * C::kPanelsH + x;
+          for (int x = 0; x < C::kPanelsH; ++x) {
+            const int pn = h * C::kPanelsH + x;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16(acc, sdesc_advance(a0, pn * C::kPanelQ + k * 32),
-                     sdesc_advance(b0, pn * kPanel + k * 32), C::kIdescQK, (x || k) ? 1u : 0u);
-        }
-        mma_commit(bar(kSFull0 + s));
-        const bool last = c.last();
-        if (last) mma_commit(bar(kQEmpty));
-        c.next();
-        if (last) {
-          if (qh == 0 && c.left > 0) {  // q of the next unit, once both halves have read this one's
-            ok = pipe_wait(bar(kQEmpty), nu & 1, wc);
-            if (!ok) break;
-            load_q();
+            for (int k = 0; k < 4; ++k)
+              mma_bf16(tmem + s * 64, sdesc_advance(a0, pn * C::kPanelQ + k * 32),
+                       sdesc_advance(b0, pn * 1024 + k * 32), C::kIdescQK, (pn || k) ? 1u : 0u);
           }
-          ++nu;
+          if (h == HV - 1) {
+            mma_commit(bar(kSFull0 + s));
+            if (last) mma_commit(bar(kQEmpty));
+          }
         }
+        __syncwarp();
       }
-      mma_commit(bar(qh ? kDrainB : kDrainA));
-      pipe_drain(bar(qh ? kDrainB : kDrainA), 0, wc);
+      if (!ok) break;
+      c.next();
+      if (last) {
+        if (c.left > 0) {  // q of the next unit, once this unit's MMAs have read q
+          ok = __all_sync(0xffffffffu, pipe_wait(bar(kQEmpty), pieces & 1, wc));
+          if (!ok) break;
+          load_q();
+        }
+        ++pieces;
+      }
+    }
+    if (elect_one()) {
+      mma_commit(bar(kDrainQk));
+      pipe_drain(bar(kDrainQk), 0, wc);
       if (q_loads > 0) pipe_drain(bar(kQFull), (q_loads - 1) & 1, wc);
     }
     __syncwarp();
-  } else {
-    // ===================================================== softmax, PV, epilogue
-    // Warp w reads TMEM lane quadrant q4 = w % 4 and positions [32hc, 32hc + 32)
-    // of each tile, hc = w / 4: thread t holds rows hA = 16 q4 + t / 4 and
-    // hB = hA + 8 at the 8 positions 32hc + 8rep + 2(t % 4) + {0, 1}.
-    setmaxnreg_inc<kSmRegs>();
+  } else if (warp == kPvWarp) {
+    // ===================================================== PV MMAs
+    Cursor c;
+    c.init(p.units, u0, t0, nt);
+    for (int g = 0; g < nt; ++g) {
+      const int s = g & 1, ks = g % KS;
+      if (!__all_sync(0xffffffffu, pipe_wait(bar(kPReady0 + s), (g >> 1) & 1, wc))) break;
+      tc_fence_after();
+      const uint64_t a0 = sdesc_sw128(sKV + ks * C::kStage, 1024, C::kGroup);
+      const uint64_t b0 = sdesc_sw128(sP + s * C::kPBytes, 16, 1024);
+      const uint32_t add = c.first ? 0u : 1u;
+      if (elect_one()) {
+#pragma unroll
+        for (int b = 0; b < C::kBlocks; ++b) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_bf16(tmem + C::kOCol + b * R, sdesc_advance(a0, 2 * b * 1024 + k * 2 * C::kGroup),
+                     sdesc_advance(b0, k * 32), C::kIdescPV, k ? 1u : add);
+          if ((b + 1) % C::kBlocksH == 0) mma_commit(pv_done(ks, b / C::kBlocksH));
+        }
+      }
+      __syncwarp();
+      c.next();
+    }
+    if (elect_one()) {
+      mma_commit(bar(kDrainPv));
+      pipe_drain(bar(kDrainPv), 0, wc);
+    }
+    __syncwarp();
+  } else if (warp < kSmWarps) {
+    // ===================================================== softmax and epilogue
+    if constexpr (!TMA) setmaxnreg_inc<128>();
+    // Warp w reads TMEM lane quadrant q4 = w % 4 and half hc = w / 4 of each
+    // tile's positions: thread t holds rows hA = 16 q4 + t / 4 and hB = hA + 8 at
+    // the positions kHalf hc + 8 rep + 2 (t % 4) + {0, 1}.
+    constexpr int kHalf = kTile / 2, kReps = kHalf / 8, kE = 4 * kReps;
     const int q4 = warp & 3, hc = warp >> 2, st = threadIdx.x, tq = lane & 3;
     const int hA = q4 * 16 + (lane >> 2), hB = hA + 8;
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
@@ -384,27 +483,30 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
       float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;  // l: this thread's share
       for (int i = i0; i < i1; ++i, ++g) {
         const int s = g & 1;
-        const int j0 = chunk_tile_start(i, un.nf, un.lo);
+        const int j0 = chunk_tile_start(i, un.nf, un.lo, kTile);
         // whether every row of the unit sees the whole tile
         const bool full = j0 + kTile - 1 <= un.pos0 &&
                           (window == 0 || j0 > p_hi - window || j0 + kTile <= nfirst);
         pipe_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
         tc_fence_after();
-        float x[16];
+        float x[kE];
         {
-          uint32_t sa[16];
-          tmem_ld_16x256b_x4(tmem + lane_base + s * 64 + 32 * hc, sa);
-          if constexpr (HV == 2) {
-            uint32_t sb[16];
-            tmem_ld_16x256b_x4(tmem + lane_base + C::kSbCol + s * 64 + 32 * hc, sb);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(sa[e]) + __uint_as_float(sb[e]);
+          const uint32_t ta = tmem + lane_base + s * 64 + kHalf * hc;
+          uint32_t v[kE];
+          if constexpr (kReps == 4) {
+            tmem_ld_16x256b_x4(ta, v);
           } else {
+            static_assert(kReps == 3, "24 positions");
+            uint32_t v2[8], v1[4];
+            tmem_ld_16x256b_x2(ta, v2);
+            tmem_ld_16x256b_x1(ta + 16, v1);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(sa[e]);
+            for (int e = 0; e < kE; ++e) v[e] = e < 8 ? v2[e] : v1[e - 8];
           }
+          if constexpr (kReps == 4) tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < kE; ++e) x[e] = __uint_as_float(v[e]);
         }
         tc_fence_before();
         __syncwarp();
@@ -414,8 +516,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
         if (!full) {
           see = 0;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = j0 + 32 * hc + 8 * (e >> 2) + 2 * tq + (e & 1);
+          for (int e = 0; e < kE; ++e) {
+            const int j = j0 + kHalf * hc + 8 * (e >> 2) + 2 * tq + (e & 1);
             const int pos = (e & 3) < 2 ? posA : posB;
             const bool ok = j <= pos && (window == 0 || j > pos - window || j < nfirst);
             see |= ok ? 1u << e : 0u;
@@ -428,10 +530,11 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
           if (named_bar_or(1, kSmThreads, poison)) {
             uint8_t* stage = smem + C::kOffKV + (g % KS) * C::kStage;
             const int r = st >> 2, part = st & 3;  // 4 threads per cached row
+            uint8_t* atom = stage + (r >> 3) * C::kGroup + (r & 7) * 128;
             uint32_t bad = 0;
-            for (int ch = part; ch < D / 8; ch += 4) {
-              const uint4 w = *reinterpret_cast<const uint4*>(
-                  stage + (ch >> 3) * kPanel + (r >> 3) * 1024 + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+            for (int ch = part; ch < D / 8 && r < kTile; ch += 4) {
+              const uint4 w =
+                  *reinterpret_cast<const uint4*>(atom + (ch >> 3) * 1024 + (((ch & 7) ^ (r & 7)) << 4));
               const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -439,12 +542,9 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
             }
             bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
             bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
-            if (bad) {
-              for (int ch = part; ch < D / 8; ch += 4)
-                *reinterpret_cast<uint4*>(stage + (ch >> 3) * kPanel + (r >> 3) * 1024 +
-                                          (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(0, 0, 0, 0);
-            }
+            for (int ch = part; bad && ch < D / 8; ch += 4)
+              *reinterpret_cast<uint4*>(atom + (ch >> 3) * 1024 + (((ch & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();  // read by the PV MMA, issued after a later barrier
           }
         }
@@ -457,15 +557,17 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
         // swizzle) with two stmatrix.x4.  The MMA multiplies the rounded p, the
         // denominator sums the unrounded ones: each weight is off by at most
         // 2^-9 of itself, less than the output's own rounding, and lse is exact.
-        const uint32_t prow = sP + s * C::kPBytes + (2 * q4) * 1024 + (lane & 7) * 128 +
-                              ((((4 * hc) + (lane >> 3)) ^ (lane & 7)) << 4);
+        const uint32_t prow = sP + s * C::kPBytes + (2 * q4) * 1024 + (lane & 7) * 128;
+        auto pchunk = [&](int c) {  // this lane's address of a matrix of stmatrix: chunk c of its row
+          return prow + (uint32_t)(((kReps * hc + c) ^ (lane & 7)) << 4);
+        };
         float sumA, sumB;
         auto weights = [&]() {
           bool over = false;
           sumA = sumB = 0.f;
-          uint32_t pa[4], pb[4];
+          uint32_t pa[kReps], pb[kReps];
 #pragma unroll
-          for (int rep = 0; rep < 4; ++rep) {
+          for (int rep = 0; rep < kReps; ++rep) {
             float e[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -482,8 +584,15 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
             pb[rep] = *reinterpret_cast<const uint32_t*>(&b);
           }
           if (held) {
-            stmatrix_x4(prow, pa[0], pa[1], pa[2], pa[3]);
-            stmatrix_x4(prow + 1024, pb[0], pb[1], pb[2], pb[3]);
+            if constexpr (kReps == 4) {
+              stmatrix_x4(pchunk(lane >> 3), pa[0], pa[1], pa[2], pa[3]);
+              stmatrix_x4(pchunk(lane >> 3) + 1024, pb[0], pb[1], pb[2], pb[3]);
+            } else {
+              stmatrix_x2(pchunk((lane >> 3) & 1), pa[0], pa[1]);
+              stmatrix_x1(pchunk(2), pa[2]);
+              stmatrix_x2(pchunk((lane >> 3) & 1) + 1024, pb[0], pb[1]);
+              stmatrix_x1(pchunk(2) + 1024, pb[2]);
+            }
           }
           return over;
         };
@@ -499,7 +608,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
         if (exact) {
           float eA = -INFINITY, eB = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < kE; ++e) {
             if ((see >> e) & 1u) {
               if ((e & 3) < 2) eA = fmaxf(eA, x[e] * sc);
               else eB = fmaxf(eB, x[e] * sc);
@@ -543,9 +652,9 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
             if (lane == 0) pipe_wait(pv_done((g - 1) % KS, HV - 1), ((g - 1) / KS) & 1, wc);
             __syncwarp();
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int b = hc; b < C::kBlocks; b += 2) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < R / 16; ++c) {
                 uint32_t ov[16];
                 const uint32_t ta = tmem + lane_base + C::kOCol + b * R + c * 16;
@@ -564,21 +673,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
         }
         lA += sumA;
         lB += sumB;
-        if (threadIdx.x == 0) {
-          tc_fence_after();
-          const int ks = g % KS;
-          const uint64_t a0 = sdesc_sw128(sKV + ks * C::kStage, kPanel, 1024);
-          const uint64_t b0 = sdesc_sw128(sP + s * C::kPBytes, 16, 1024);
-#pragma unroll
-          for (int b = 0; b < C::kBlocks; ++b) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16(tmem + C::kOCol + b * R, sdesc_advance(a0, 2 * b * kPanel + k * 2048),
-                       sdesc_advance(b0, k * 32), C::kIdescPV, (i == i0 && k == 0) ? 0u : 1u);
-            if ((b + 1) % C::kBlocksH == 0) mma_commit(pv_done(ks, b / C::kBlocksH));
-          }
-        }
-        __syncwarp();
+        // the last barrier (the vote, or the exact path's) has seen every warp's P
+        if (st == 0) mbar_arrive(bar(kPReady0 + s));
       }
       // ---------------------------------------------- end of the piece
       lA += __shfl_xor_sync(0xffffffffu, lA, 1);
@@ -624,21 +720,22 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
       }
       named_bar_sync(1, kSmThreads);
       if (whole) {
-        // warps 4hc .. 4hc + 3 write blocks hc, hc + 2 of O^T through staging
-        // area hc: scaled, packed to bf16 and transposed with stmatrix into two
-        // boxes of R rows x 64 columns, then row by row to out
-        uint8_t* stg = smem + (hc ? C::kOffStage2 : C::kOffP);
-        constexpr int kRc = R < 32 ? R : 32;
+        // block by block of O^T through the P buffers: scaled, packed to bf16 and
+        // transposed with stmatrix into two boxes of R rows x 64 columns, then row
+        // by row to out.  Warp w takes 32 rows of D (q4) and half hc of the rows.
+        uint8_t* stg = smem + C::kOffP;
+        constexpr int kRc = R == 16 ? 16 : 32;
+        const bool mine = R > 16 || hc == 0;
+        const int r0 = R > 16 ? hc * kRc : 0;
+        float fac[kRc / 4];
+#pragma unroll
+        for (int rep = 0; rep < kRc / 8; ++rep) {
+          fac[2 * rep] = s_fac[r0 + 8 * rep + 2 * tq];
+          fac[2 * rep + 1] = s_fac[r0 + 8 * rep + 2 * tq + 1];
+        }
 #pragma unroll 1
-        for (int b = hc; b < C::kBlocks; b += 2) {
-#pragma unroll
-          for (int r0 = 0; r0 < R; r0 += kRc) {
-            float fac[kRc / 4];
-#pragma unroll
-            for (int rep = 0; rep < kRc / 8; ++rep) {
-              fac[2 * rep] = s_fac[r0 + 8 * rep + 2 * tq];
-              fac[2 * rep + 1] = s_fac[r0 + 8 * rep + 2 * tq + 1];
-            }
+        for (int b = 0; b < C::kBlocks; ++b) {
+          if (mine) {
             uint32_t rr[2][kRc / 2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -673,21 +770,21 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
               }
             }
           }
-          named_bar_sync(6 + hc, 128);
+          named_bar_sync(1, kSmThreads);
           constexpr int kW = D < 128 ? D / 8 : 16;  // 16-byte chunks of a row of this block
-          for (int e = st & 127; e < un.nrows * kW; e += 128) {
+          for (int e = st; e < un.nrows * kW; e += kSmThreads) {
             const int r = e / kW, ch = e % kW;
             const uint4 w = *reinterpret_cast<const uint4*>(stg + (ch >> 3) * (R * 128) + r * 128 +
                                                             (((ch & 7) ^ (r & 7)) << 4));
             *reinterpret_cast<uint4*>(p.out + (size_t)(un.row0 + r) * D + b * 128 + ch * 8) = w;
           }
-          named_bar_sync(6 + hc, 128);  // the area may be rewritten
+          named_bar_sync(1, kSmThreads);  // the area may be rewritten
         }
       } else {
 #pragma unroll 1
         for (int b = hc; b < C::kBlocks; b += 2) {
           const int d = b * 128 + q4 * 32 + lane;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < R / 16; ++c) {
             uint32_t ov[16];
             tmem_ld16(tmem + lane_base + C::kOCol + b * R + c * 16, ov);
@@ -703,22 +800,20 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
       tc_fence_before();
       named_bar_sync(1, kSmThreads);
     }
-    if (threadIdx.x == 0) {
-      mma_commit(bar(kDrainPv));
-      pipe_drain(bar(kDrainPv), 0, wc);
-    }
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == kQkWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <typename F>
-cudaError_t for_shape(int R, int D, F&& f) {
-#define SDA_CASE(RV, DV) \
-  if (R == RV && D == DV) return f(chunk_attn_kernel<RV, DV>, (size_t)Cfg<RV, DV>::kSmem);
+cudaError_t for_shape(int R, int D, bool tma, F&& f) {
+#define SDA_CASE(RV, DV)                                                                      \
+  if (R == RV && D == DV)                                                                     \
+    return tma ? f(chunk_attn_kernel<RV, DV, true>, (size_t)Cfg<RV, DV>::kSmem, dim3(384))    \
+               : f(chunk_attn_kernel<RV, DV, false>, (size_t)Cfg<RV, DV>::kSmem, dim3(kGatherThreads));
   SDA_CASE(16, 64) SDA_CASE(16, 128) SDA_CASE(16, 256) SDA_CASE(16, 512)
   SDA_CASE(64, 64) SDA_CASE(64, 128) SDA_CASE(64, 256) SDA_CASE(64, 512)
 #undef SDA_CASE
@@ -732,8 +827,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 
 }  // namespace
 
-bool pipe_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
-                 uint32_t box_rows) {
+static EncodeTiledFn encode_fn() {
   static const EncodeTiledFn fn = []() -> EncodeTiledFn {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -743,12 +837,28 @@ bool pipe_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
       return nullptr;
     return reinterpret_cast<EncodeTiledFn>(f);
   }();
-  if (!fn) return false;
+  return fn;
+}
+
+bool pipe_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
+                 uint32_t box_rows) {
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
   const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_fn() &&
+         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool pipe_map_pool(CUtensorMap* m, const void* base, uint64_t D, uint64_t rows, uint32_t panels) {
+  const cuuint64_t dims[3] = {64, rows, D / 64}, strides[2] = {D * 2, 128};
+  const cuuint32_t box[3] = {64, 8, panels}, estr[3] = {1, 1, 1};
+  return encode_fn() &&
+         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // setmaxnreg.inc waits until the other warps have released registers: a build
@@ -756,16 +866,17 @@ bool pipe_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
 cudaError_t chunk_prepare() {
   for (int R : {16, 64}) {
     for (int D : {64, 128, 256, 512}) {
-      const cudaError_t e = for_shape(R, D, [&](auto kernel, size_t smem) {
-        cudaError_t r =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        cudaFuncAttributes a;
-        if (r == cudaSuccess) r = cudaFuncGetAttributes(&a, kernel);
-        if (r == cudaSuccess && (a.numRegs < kLaunchRegs || a.maxThreadsPerBlock < kThreads))
-          r = cudaErrorInvalidConfiguration;
-        return r;
-      });
-      if (e != cudaSuccess) return e;
+      for (bool tma : {false, true}) {
+        const cudaError_t e = for_shape(R, D, tma, [&](auto kernel, size_t smem, dim3) {
+          cudaError_t r =
+              cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+          cudaFuncAttributes a;
+          if (r == cudaSuccess) r = cudaFuncGetAttributes(&a, kernel);
+          if (r == cudaSuccess && !tma && a.numRegs < kGatherRegs) r = cudaErrorInvalidConfiguration;
+          return r;
+        });
+        if (e != cudaSuccess) return e;
+      }
     }
   }
   return cudaSuccess;
@@ -774,8 +885,12 @@ cudaError_t chunk_prepare() {
 cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
                               const float* attn_sink, float scale, void* out, float* lse,
                               const ChunkLayout& L, void* ws, cudaStream_t st) {
-  CUtensorMap tq;
-  if (!pipe_map_2d(&tq, q, g.D, (uint64_t)g.T * g.H, 64, L.R)) return cudaErrorInvalidValue;
+  // TMA loads groups of 8 rows, which blocks of a multiple of 8 rows keep together
+  const bool tma = g.k_per_block % 8 == 0;
+  CUtensorMap tq, tkv = {};
+  if (!pipe_map_2d(&tq, q, g.D, (uint64_t)g.T * g.H, 64, L.R) ||
+      (tma && !pipe_map_pool(&tkv, kv, g.D, (uint64_t)g.total_pages, g.D >= 256 ? g.D / 128 : g.D / 64)))
+    return cudaErrorInvalidValue;
   char* base = static_cast<char*>(ws);
   Params p;
   p.kv = static_cast<const __nv_bfloat16*>(kv);
@@ -790,8 +905,8 @@ cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
   p.g = g;
   p.qk_scale_log2 = scale * kLog2e;
   p.wait_timeout_ns = current_wait_fault().timeout_ns;
-  return for_shape(L.R, g.D, [&](auto kernel, size_t smem) {
-    return launch_pdl(kernel, dim3(L.grid), dim3(kThreads), smem, st, tq, p);
+  return for_shape(L.R, g.D, tma, [&](auto kernel, size_t smem, dim3 threads) {
+    return launch_pdl(kernel, dim3(L.grid), threads, smem, st, tq, tkv, p);
   });
 }
 

@@ -20,7 +20,7 @@ constexpr int kSmemUnits = 8192;  // units whose tile offsets are also kept in s
 constexpr int kSmemSeqs = 2048;   // sequences whose unit offsets are kept in shared memory
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
-    const ChunkGeom g, int R, int grid, int u_max, ChunkHeader* __restrict__ hdr,
+    const ChunkGeom g, int R, int tile, int grid, int u_max, ChunkHeader* __restrict__ hdr,
     ChunkUnit* __restrict__ units, int* __restrict__ seq_unit, int* __restrict__ cta_unit) {
   __shared__ long long warp_sums[32];
   __shared__ long long s_total;
@@ -75,9 +75,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
       d.hi = max(p_hi + 1, 0);
       d.lo = g.window > 0 ? max(0, (int)max((long long)d.pos0 - g.window + 1, 0ll)) : 0;
       if (d.hi == 0) d.lo = 0;
-      const int lot = d.lo / kChunkTile;
-      d.nf = (min(g.first, lot * kChunkTile) + kChunkTile - 1) / kChunkTile;
-      d.ntiles = d.nf + (d.hi + kChunkTile - 1) / kChunkTile - lot;
+      const int lot = d.lo / tile;
+      d.nf = (min(g.first, lot * tile) + tile - 1) / tile;
+      d.ntiles = d.nf + (d.hi + tile - 1) / tile - lot;
       if (d.ntiles < 1) d.ntiles = 1;  // rows that see nothing: one tile of masked positions
     }
     const long long ex = scan_exclusive(d.ntiles, warp_sums, &s_total);
@@ -199,9 +199,10 @@ ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms) {
   ChunkLayout L;
   const int64_t rows = (int64_t)T * H;
   // 16-row units where a sequence has at most 16 rows on average (a step of
-  // few heads): q then takes a quarter of the shared memory and a third KV
-  // stage fits, and the rows' masks and stores are not padded to 64.
+  // few heads): q then takes a quarter of the shared memory and three KV stages
+  // of 64 positions fit, and the rows' masks and stores are not padded to 64.
   L.R = rows <= (int64_t)16 * B ? 16 : 64;
+  L.tile = chunk_tile(L.R, D);
   L.u_max = (int)((rows + L.R - 1) / L.R + B);
   L.grid = num_sms < kMaxPlanGrid ? num_sms : kMaxPlanGrid;
   size_t off = sizeof(ChunkHeader);
@@ -221,7 +222,7 @@ ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms) {
 
 cudaError_t launch_chunk_plan(const ChunkGeom& g, const ChunkLayout& L, void* ws, cudaStream_t st) {
   char* base = static_cast<char*>(ws);
-  return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, g, L.R, L.grid, L.u_max,
+  return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, g, L.R, L.tile, L.grid, L.u_max,
                     reinterpret_cast<ChunkHeader*>(base),
                     reinterpret_cast<ChunkUnit*>(base + L.units_off),
                     reinterpret_cast<int*>(base + L.seq_off),

@@ -48,11 +48,56 @@ __device__ __forceinline__ void pipe_drain(uint32_t bar, uint32_t parity, const 
     }
   }
 }
+
+// True in one lane of the (converged) warp.  Code that issues MMAs keeps its
+// control flow warp-uniform and guards only the instruction with this, so that
+// descriptors stay in uniform registers: 33 cycles per M64 N64 K16 MMA, the
+// shared-memory bound, against 47 from inside an `if (lane == 0)`.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// 3-D tiled load of one box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// 16 lanes x 8 columns of TMEM (16x256b, one repetition).
+__device__ __forceinline__ void tmem_ld_16x256b_x1(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+// Two 8x8 b16 matrices, and one, stored as they are held.
+__device__ __forceinline__ void stmatrix_x2(uint32_t addr, uint32_t r0, uint32_t r1) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(r0),
+               "r"(r1)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_x1(uint32_t addr, uint32_t r0) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x1.shared.b16 [%0], {%1};" ::"r"(addr), "r"(r0)
+               : "memory");
+}
 #endif
 
 // A 2-D bf16 tensor map over [rows, cols] (row stride cols) with boxes of
 // box_rows x box_cols, 128-byte swizzle; out-of-range elements read as zero.
 bool pipe_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
                  uint32_t box_rows);
+
+// The pool [rows, D] seen as [D / 64 panels][rows][64 columns], with boxes of 8
+// rows x `panels` panels: a box lands as `panels` swizzle atoms of 1 KB.
+bool pipe_map_pool(CUtensorMap* m, const void* base, uint64_t D, uint64_t rows, uint32_t panels);
 
 }  // namespace sda
