@@ -15,7 +15,7 @@
 //   warps 0..7   softmax and epilogue
 //   warp 8       QK MMAs and the q loads (TMA)
 //   warp 9       PV MMAs
-//   warp 10      KV tiles by TMA where blocks hold whole groups of 8 rows
+//   warp 10      KV tiles by TMA where blocks hold a multiple of 16 rows
 //   warps 12..   (gather kernel, other block sizes) 8 warps copy the tile's rows
 //                one by one with 16-byte cp.async
 // S = Q K^T (M = 64 rows, N = a tile of positions) and O^T += V^T P^T (M = 128
@@ -65,9 +65,11 @@ struct Cfg {
   static constexpr int kBlocks = (D + 127) / 128;    // 128-row blocks of O^T
   static constexpr int kHalves = D >= 256 ? 2 : 1;   // a stage is filled and freed in halves of D
   static constexpr int kPanelsH = kPanels / kHalves, kBlocksH = kBlocks / kHalves;
-  static constexpr int kGroup = kPanels * 1024;      // bytes of 8 rows
-  static constexpr int kGroups = kTile / 8;
-  static constexpr int kStage = kGroups * kGroup;
+  // a stage: halves of D, each [groups of 8 rows][panels][1 KB atom]
+  static constexpr int kGroup = kPanelsH * 1024;
+  static constexpr int kHalf = kTile / 8 * kGroup;
+  static constexpr int kStage = kHalves * kHalf;
+  static constexpr int kBox = 2 * kGroup, kBoxes = kTile / 16;  // a TMA box: 16 rows of a half
   static constexpr int kStages = D == 512 ? 3 : (D == 256 ? 5 : 6);
   static constexpr int kPanelQ = R * 128;
   static constexpr int kPBytes = R * 128;
@@ -224,63 +226,53 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
 
   if (TMA && warp == kTmaWarp) {
     // ===================================================== KV tiles by TMA
-    // A group of 8 positions lies in one block (both start at multiples of 8)
-    // and so in 8 pool rows in a row: lane i < kGroups loads group i of every
-    // tile, each half of D as soon as the PV MMAs that last read it are done,
-    // and brings its group of the tile two ahead into L2.  A group that no row
-    // sees is read from behind the pool, which fills it with zeros.
-    auto first_row = [&](const Cursor& c) {
-      if (lane >= C::kGroups) return -1;
-      const int j = chunk_tile_start(c.i, c.nf, c.lo, kTile) + lane * 8;
-      // the group's first position that is seen, if any, tells its block
+    // 16 positions lie in one block (tiles and blocks start at multiples of 16)
+    // and so in 16 pool rows in a row: lane i < kBoxes loads box i of every
+    // tile, each half of D as soon as the PV MMAs that last read it are done.  A
+    // box that no row sees is read from behind the pool, which fills it with zeros.
+    // (Boxes of 8 rows, and bulk prefetches of the tile two ahead into L2, kept
+    // this warp busier than the tensor pipe: one TMA instruction costs about 90
+    // cycles of issue.)
+    const int behind = (int)((p.g.total_pages - p.g.base) / 8);
+    auto box_of = [&](const Cursor& c) {  // in groups of 8 rows from `base` on
+      if (lane >= C::kBoxes) return behind;
+      const int j = chunk_tile_start(c.i, c.nf, c.lo, kTile) + lane * 16;
+      // the box's first position that is seen, if any, tells its block
       int x = j;
       if (x < c.lo && x >= p.g.first) x = c.lo;
-      if (x >= j + 8) return -1;
+      if (x >= j + 16) return behind;
       const int r = row_of(c, x);
-      return r < 0 ? -1 : r - (x - j);
+      return r < 0 ? behind : (int)((r - (x - j) - p.g.base) / 8);
     };
-    auto prefetch = [&](int row) {
-      if (row >= 0)
-        bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + (size_t)row * D * 2,
-                         (uint32_t)min((long long)8, (long long)p.g.total_pages - row) * D * 2);
-    };
-    Cursor c;  // runs two tiles ahead of the copies
+    Cursor c;  // runs a tile ahead of the copies
     c.init(p.units, u0, t0, nt);
-    int r0 = -1, r1 = -1;
+    int y = behind;
     if (c.left > 0) {
-      r0 = first_row(c);
+      y = box_of(c);
       c.next();
     }
-    if (c.left > 0) {
-      r1 = first_row(c);
-      c.next();
-    }
-    prefetch(r1);
     bool ok = true;
     int loads = 0;
     for (int g = 0; g < nt && ok; ++g) {
       const int s = g % KS;
-      int r2 = -1;
+      int y_next = behind;
       if (c.left > 0) {
-        r2 = first_row(c);
+        y_next = box_of(c);
         c.next();
       }
-      const int y = r0 >= 0 ? r0 : (int)p.g.total_pages;
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
         if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(kv_full(s, h), C::kStage / HV);
+        if (lane == 0) mbar_arrive_expect_tx(kv_full(s, h), C::kHalf);
         __syncwarp();
-        if (lane < C::kGroups)
-          tma_load_3d(sKV + s * C::kStage + lane * C::kGroup + h * C::kPanelsH * 1024, &tmap_kv, 0, y,
-                      h * C::kPanelsH, kv_full(s, h));
+        if (lane < C::kBoxes)
+          tma_load_4d(sKV + s * C::kStage + h * C::kHalf + lane * C::kBox, &tmap_kv, 0, 0,
+                      h * C::kPanelsH, y, kv_full(s, h));
         ++loads;
       }
-      prefetch(r2);
-      r0 = r1;
-      r1 = r2;
+      y = y_next;
     }
     // copies in flight land before the CTA's memory goes away (the last KS stages)
     for (int x = max(0, loads - KS * HV); x < loads; ++x)
@@ -326,13 +318,14 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int ch = h * kCh + lane % kCh;  // 16-byte chunk of the row: panel ch / 8
+        const int ch = h * kCh + lane % kCh;  // 16-byte chunk of the row
 #pragma unroll
         for (int x = 0; x < kRows; x += kRowsPer) {
           const int rl = x + lane / kCh;  // (past the warp's rows where kRowsPer does not divide them)
           const int slot = __shfl_sync(0xffffffffu, sl0, rl & 31);
           const int r = v * kRows + rl;
-          const uint32_t dst = stage + (r >> 3) * C::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 +
+          const uint32_t dst = stage + h * C::kHalf + (r >> 3) * C::kGroup +
+                               ((lane % kCh) >> 3) * 1024 + (r & 7) * 128 +
                                (((ch & 7) ^ (r & 7)) << 4);
           const uint4* src = slot >= 0 ? kv4 + (size_t)slot * (D / 8) + ch : kv4;
           if (rl < kRows) cp_async16(dst, src, slot >= 0 ? 16u : 0u);
@@ -394,7 +387,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_bf16(tmem + s * 64, sdesc_advance(a0, pn * C::kPanelQ + k * 32),
-                       sdesc_advance(b0, pn * 1024 + k * 32), C::kIdescQK, (pn || k) ? 1u : 0u);
+                       sdesc_advance(b0, h * C::kHalf + x * 1024 + k * 32), C::kIdescQK, (pn || k) ? 1u : 0u);
           }
           if (h == HV - 1) {
             mma_commit(bar(kSFull0 + s));
@@ -436,7 +429,9 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int b = 0; b < C::kBlocks; ++b) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            mma_bf16(tmem + C::kOCol + b * R, sdesc_advance(a0, 2 * b * 1024 + k * 2 * C::kGroup),
+            mma_bf16(tmem + C::kOCol + b * R,
+                     sdesc_advance(a0, b / C::kBlocksH * C::kHalf + 2 * (b % C::kBlocksH) * 1024 +
+                                           k * 2 * C::kGroup),
                      sdesc_advance(b0, k * 32), C::kIdescPV, k ? 1u : add);
           if ((b + 1) % C::kBlocksH == 0) mma_commit(pv_done(ks, b / C::kBlocksH));
         }
@@ -454,8 +449,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if constexpr (!TMA) setmaxnreg_inc<128>();
     // Warp w reads TMEM lane quadrant q4 = w % 4 and half hc = w / 4 of each
     // tile's positions: thread t holds rows hA = 16 q4 + t / 4 and hB = hA + 8 at
-    // the positions kHalf hc + 8 rep + 2 (t % 4) + {0, 1}.
-    constexpr int kHalf = kTile / 2, kReps = kHalf / 8, kE = 4 * kReps;
+    // the positions kPos hc + 8 rep + 2 (t % 4) + {0, 1}.
+    constexpr int kPos = kTile / 2, kReps = kPos / 8, kE = 4 * kReps;
     const int q4 = warp & 3, hc = warp >> 2, st = threadIdx.x, tq = lane & 3;
     const int hA = q4 * 16 + (lane >> 2), hB = hA + 8;
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
@@ -491,7 +486,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         tc_fence_after();
         float x[kE];
         {
-          const uint32_t ta = tmem + lane_base + s * 64 + kHalf * hc;
+          const uint32_t ta = tmem + lane_base + s * 64 + kPos * hc;
           uint32_t v[kE];
           if constexpr (kReps == 4) {
             tmem_ld_16x256b_x4(ta, v);
@@ -517,7 +512,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
           see = 0;
 #pragma unroll
           for (int e = 0; e < kE; ++e) {
-            const int j = j0 + kHalf * hc + 8 * (e >> 2) + 2 * tq + (e & 1);
+            const int j = j0 + kPos * hc + 8 * (e >> 2) + 2 * tq + (e & 1);
             const int pos = (e & 3) < 2 ? posA : posB;
             const bool ok = j <= pos && (window == 0 || j > pos - window || j < nfirst);
             see |= ok ? 1u << e : 0u;
@@ -530,11 +525,15 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (named_bar_or(1, kSmThreads, poison)) {
             uint8_t* stage = smem + C::kOffKV + (g % KS) * C::kStage;
             const int r = st >> 2, part = st & 3;  // 4 threads per cached row
-            uint8_t* atom = stage + (r >> 3) * C::kGroup + (r & 7) * 128;
+            auto chunk = [&](int ch) {  // 16 bytes of the row
+              const int pn = ch >> 3;
+              return reinterpret_cast<uint4*>(stage + pn / C::kPanelsH * C::kHalf + (r >> 3) * C::kGroup +
+                                              pn % C::kPanelsH * 1024 + (r & 7) * 128 +
+                                              (((ch & 7) ^ (r & 7)) << 4));
+            };
             uint32_t bad = 0;
             for (int ch = part; ch < D / 8 && r < kTile; ch += 4) {
-              const uint4 w =
-                  *reinterpret_cast<const uint4*>(atom + (ch >> 3) * 1024 + (((ch & 7) ^ (r & 7)) << 4));
+              const uint4 w = *chunk(ch);
               const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -543,8 +542,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
             bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
             bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
             for (int ch = part; bad && ch < D / 8; ch += 4)
-              *reinterpret_cast<uint4*>(atom + (ch >> 3) * 1024 + (((ch & 7) ^ (r & 7)) << 4)) =
-                  make_uint4(0, 0, 0, 0);
+              *chunk(ch) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();  // read by the PV MMA, issued after a later barrier
           }
         }
@@ -851,11 +849,12 @@ bool pipe_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool pipe_map_pool(CUtensorMap* m, const void* base, uint64_t D, uint64_t rows, uint32_t panels) {
-  const cuuint64_t dims[3] = {64, rows, D / 64}, strides[2] = {D * 2, 128};
-  const cuuint32_t box[3] = {64, 8, panels}, estr[3] = {1, 1, 1};
+bool pipe_map_pool(CUtensorMap* m, const void* base, uint64_t D, uint64_t groups, uint32_t panels,
+                   uint32_t box_groups) {
+  const cuuint64_t dims[4] = {64, 8, D / 64, groups}, strides[3] = {D * 2, 128, D * 16};
+  const cuuint32_t box[4] = {64, 8, panels, box_groups}, estr[4] = {1, 1, 1, 1};
   return encode_fn() &&
-         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -885,11 +884,14 @@ cudaError_t chunk_prepare() {
 cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
                               const float* attn_sink, float scale, void* out, float* lse,
                               const ChunkLayout& L, void* ws, cudaStream_t st) {
-  // TMA loads groups of 8 rows, which blocks of a multiple of 8 rows keep together
-  const bool tma = g.k_per_block % 8 == 0;
+  // TMA loads boxes of 16 rows, which blocks of a multiple of 16 rows keep
+  // together, counted in groups of 8 rows from `base` to the pool's end
+  const int64_t rows = g.total_pages - g.base;
+  const bool tma = g.k_per_block % 16 == 0 && rows > 0 && rows % 8 == 0;
   CUtensorMap tq, tkv = {};
   if (!pipe_map_2d(&tq, q, g.D, (uint64_t)g.T * g.H, 64, L.R) ||
-      (tma && !pipe_map_pool(&tkv, kv, g.D, (uint64_t)g.total_pages, g.D >= 256 ? g.D / 128 : g.D / 64)))
+      (tma && !pipe_map_pool(&tkv, static_cast<const __nv_bfloat16*>(kv) + g.base * g.D, g.D,
+                             (uint64_t)rows / 8, g.D >= 256 ? g.D / 128 : g.D / 64, 2)))
     return cudaErrorInvalidValue;
   char* base = static_cast<char*>(ws);
   Params p;

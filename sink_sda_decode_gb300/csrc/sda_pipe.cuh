@@ -63,13 +63,13 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// 3-D tiled load of one box into shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
+// 4-D tiled load of one box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w,
                                             uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
 
@@ -96,8 +96,10 @@ __device__ __forceinline__ void stmatrix_x1(uint32_t addr, uint32_t r0) {
 bool pipe_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
                  uint32_t box_rows);
 
-// The pool [rows, D] seen as [D / 64 panels][rows][64 columns], with boxes of 8
-// rows x `panels` panels: a box lands as `panels` swizzle atoms of 1 KB.
-bool pipe_map_pool(CUtensorMap* m, const void* base, uint64_t D, uint64_t rows, uint32_t panels);
+// Pool rows from `base` on seen as [groups of 8 rows][D / 64 panels][8 rows]
+// [64 columns], with boxes of box_groups groups x `panels` panels: each group of
+// a box lands as `panels` swizzle atoms of 1 KB.
+bool pipe_map_pool(CUtensorMap* m, const void* base, uint64_t D, uint64_t groups, uint32_t panels,
+                   uint32_t box_groups);
 
 }  // namespace sda
