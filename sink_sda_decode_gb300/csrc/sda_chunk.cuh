@@ -65,7 +65,8 @@ static_assert(offsetof(ChunkHeader, error) == offsetof(WsHeader, error),
 
 struct ChunkLayout {
   size_t units_off, seq_off, cta_off, ml_off, o_off, total;
-  int u_max, grid, R, tile;
+  int u_max, grid, R, tile;  // R: rows per unit; grid: CTAs, or pairs of CTAs, that share the tiles
+  bool pair;                 // units of 128 rows, 64 for each CTA of a cluster of two
 };
 // Positions per KV tile (a multiple of 16).  With 64 rows of q at D = 512 two
 // stages of 64 positions fit beside q, or three of 48: the tensor pipe needs
@@ -73,8 +74,15 @@ struct ChunkLayout {
 // scores, softmax and PV take longer than two tiles' MMAs, and three in flight
 // keep the pipe busier (attend of a 2048-token chunk over 8192 positions).
 constexpr int chunk_tile(int R, int D) { return R == 64 && D == 512 ? 48 : 64; }
-// The layout for B sequences, T tokens: R rows per unit is a function of them.
-ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms);
+// Whether KV tiles can be loaded as boxes of 16 rows: blocks hold a multiple of
+// 16 rows, and the pool from `base` on whole groups of 8 (the tensor map counts
+// in them).
+inline bool chunk_boxes(const ChunkGeom& g) {
+  const int64_t rows = g.total_pages - g.base;
+  return g.k_per_block % 16 == 0 && rows > 0 && rows % 8 == 0;
+}
+// The layout for B sequences of T tokens in all.
+ChunkLayout chunk_layout(int B, int T, int H, int D, bool boxes, int num_sms);
 
 cudaError_t chunk_prepare();  // one-time kernel attributes on the current device
 cudaError_t launch_chunk_plan(const ChunkGeom& g, const ChunkLayout& L, void* ws, cudaStream_t st);

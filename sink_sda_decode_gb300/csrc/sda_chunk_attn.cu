@@ -55,7 +55,15 @@ enum Bar : int {
   kDrainPv,
   kKvFull0,                              // + 2 * stage + half of D
   kPvDone0 = kKvFull0 + 2 * kMaxStages,  // + 2 * stage + half of D
-  kBars = kPvDone0 + 2 * kMaxStages
+  kKvFree0 = kPvDone0 + 2 * kMaxStages,  // pairs: both CTAs' PV MMAs are done with it
+  kBars = kKvFree0 + 2 * kMaxStages
+};
+
+// The three kernels: how a CTA gets its KV tiles.
+enum Mode : int {
+  kGather = 0,  // row by row
+  kTma = 1,     // boxes of 16 rows
+  kPair = 2     // boxes of 16 rows, each loaded once for the two CTAs of a cluster
 };
 
 template <int R, int D>
@@ -114,6 +122,14 @@ struct Params {
   uint64_t wait_timeout_ns;
 };
 
+__device__ __forceinline__ ChunkUnit load_unit(const ChunkUnit* u) {
+  ChunkUnit d;
+  int4* w = reinterpret_cast<int4*>(&d);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) w[i] = __ldcg(reinterpret_cast<const int4*>(u) + i);
+  return d;
+}
+
 // Walks the CTA's tiles in order; every role walks the same ones.
 struct Cursor {
   const ChunkUnit* units;
@@ -153,11 +169,12 @@ struct Cursor {
   }
 };
 
-template <int R, int D, bool TMA>
-__global__ void __launch_bounds__(TMA ? 384 : kGatherThreads, 1)
+template <int R, int D, int MODE>
+__global__ void __launch_bounds__(MODE == kGather ? kGatherThreads : 384, 1)
 chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
                   const __grid_constant__ CUtensorMap tmap_kv, const Params p) {
   using C = Cfg<R, D>;
+  constexpr bool TMA = MODE != kGather, PAIR = MODE == kPair;
   constexpr int KS = C::kStages;
   constexpr int HV = C::kHalves;
   constexpr int kTile = C::kTile;
@@ -171,6 +188,11 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
   auto bar = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
   auto kv_full = [&](int s, int h) { return bar(kKvFull0 + 2 * s + h); };
   auto pv_done = [&](int s, int h) { return bar(kPvDone0 + 2 * s + h); };
+  // when a stage's half may be overwritten
+  auto kv_free = [&](int s, int h) { return bar((PAIR ? kKvFree0 : kPvDone0) + 2 * s + h); };
+  // A pair works on units of 2 R rows, CTA `rank` on R of them, over the same KV tiles.
+  const int rank = PAIR ? (int)(blockIdx.x & 1) : 0, worker = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  constexpr int kUnitRows = PAIR ? 2 * R : R;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -178,8 +200,9 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     mbar_init(bar(kQEmpty), 1);
     for (int s = 0; s < KS; ++s) {
       for (int h = 0; h < HV; ++h) {
-        mbar_init(kv_full(s, h), TMA ? 1 : kLoadWarps);
+        mbar_init(kv_full(s, h), TMA ? 1 : kLoadWarps * 32);
         mbar_init(pv_done(s, h), 1);
+        if (PAIR) mbar_init(kv_free(s, h), 2);
       }
     }
     for (int s = 0; s < 2; ++s) {
@@ -199,16 +222,17 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR) cluster_sync();  // the other CTA's barriers are ready
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // everything above overlaps the plan; global memory only below
   pdl_trigger();
   const int per = __ldcg(&p.hdr->per), n_tiles = __ldcg(&p.hdr->n_tiles);
-  const long long t0l = (long long)blockIdx.x * per;
+  const long long t0l = (long long)worker * per;
   const int t0 = (int)min(t0l, (long long)n_tiles);
-  const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // this CTA's tiles
-  const int u0 = __ldcg(p.cta_unit + blockIdx.x);
+  const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // this CTA's (or pair's) tiles
+  const int u0 = __ldcg(p.cta_unit + worker);
   const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
 
   // Pool row of position j of the cursor's unit; -1: no row of the unit sees
@@ -262,21 +286,31 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
+        if (g >= KS) ok = pipe_wait(kv_free(s, h), ((g / KS) - 1) & 1, wc);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        // (of a pair, the other CTA's loads may land before this arrival: the
+        // phase completes with it)
         if (lane == 0) mbar_arrive_expect_tx(kv_full(s, h), C::kHalf);
         __syncwarp();
-        if (lane < C::kBoxes)
-          tma_load_4d(sKV + s * C::kStage + h * C::kHalf + lane * C::kBox, &tmap_kv, 0, 0,
-                      h * C::kPanelsH, y, kv_full(s, h));
+        const uint32_t dst = sKV + s * C::kStage + h * C::kHalf + lane * C::kBox;
+        if constexpr (PAIR) {
+          // each CTA loads a half of D (D <= 128: every other box) for both
+          if (lane < C::kBoxes && (HV == 2 ? h == rank : (lane & 1) == rank))
+            tma_load_4d_multicast(dst, &tmap_kv, 0, 0, h * C::kPanelsH, y, kv_full(s, h), 3);
+        } else {
+          if (lane < C::kBoxes) tma_load_4d(dst, &tmap_kv, 0, 0, h * C::kPanelsH, y, kv_full(s, h));
+        }
         ++loads;
       }
       y = y_next;
     }
     // copies in flight land before the CTA's memory goes away (the last KS stages)
-    for (int x = max(0, loads - KS * HV); x < loads; ++x)
+    for (int x = max(0, loads - KS * HV); x < loads; ++x) {
       pipe_drain(kv_full((x / HV) % KS, x % HV), (x / HV / KS) & 1, wc);
+      // and so do the other CTA's arrivals
+      if (PAIR) pipe_drain(kv_free((x / HV) % KS, x % HV), (x / HV / KS) & 1, wc);
+    }
   } else if (!TMA && warp >= kLoadWarp0) {
     // ===================================================== KV rows one by one
     setmaxnreg_dec<64>();
@@ -312,10 +346,9 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         c.next();
       }
       const uint32_t stage = sKV + s * C::kStage;
-      int issued = 0;
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
+        if (g >= KS) ok = pipe_wait(kv_free(s, h), ((g / KS) - 1) & 1, wc);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int ch = h * kCh + lane % kCh;  // 16-byte chunk of the row
@@ -330,25 +363,15 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const uint4* src = slot >= 0 ? kv4 + (size_t)slot * (D / 8) + ch : kv4;
           if (rl < kRows) cp_async16(dst, src, slot >= 0 ? 16u : 0u);
         }
-        cp_async_commit();
-        ++issued;
-      }
-      if (HV == 2 && issued == HV) {
-        cp_async_wait_group<1>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv_full(s, 0));
-      }
-      cp_async_wait_group<0>();
-      if (issued == HV) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv_full(s, HV - 1));
+        // arrives once this thread's copies have landed, so that the warp goes
+        // on to the next stage meanwhile (the reader fences to the async proxy)
+        cp_async_arrive(kv_full(s, h));
       }
       prefetch(sl2);
       sl0 = sl1;
       sl1 = sl2;
     }
+    cp_async_wait_all();
   } else if (warp == kQkWarp) {
     // ===================================================== QK MMAs
     Cursor c;
@@ -356,7 +379,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     int pieces = 0, q_loads = 0;
     bool ok = true;
     auto load_q = [&]() {
-      const int row = __ldcg(&p.units[c.u].row0);
+      const int row = __ldcg(&p.units[c.u].row0) + rank * R;
       if (elect_one()) {
         mbar_arrive_expect_tx(bar(kQFull), C::kPanels * C::kPanelQ);
 #pragma unroll
@@ -379,6 +402,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (ok) ok = pipe_wait(kv_full(ks, h), (g / KS) & 1, wc);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (!TMA) fence_proxy_async_smem();  // the copies were made through the generic proxy
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -420,6 +444,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     for (int g = 0; g < nt; ++g) {
       const int s = g & 1, ks = g % KS;
       if (!__all_sync(0xffffffffu, pipe_wait(bar(kPReady0 + s), (g >> 1) & 1, wc))) break;
+      if (!TMA) fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t a0 = sdesc_sw128(sKV + ks * C::kStage, 1024, C::kGroup);
       const uint64_t b0 = sdesc_sw128(sP + s * C::kPBytes, 16, 1024);
@@ -433,7 +458,10 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
                      sdesc_advance(a0, b / C::kBlocksH * C::kHalf + 2 * (b % C::kBlocksH) * 1024 +
                                            k * 2 * C::kGroup),
                      sdesc_advance(b0, k * 32), C::kIdescPV, k ? 1u : add);
-          if ((b + 1) % C::kBlocksH == 0) mma_commit(pv_done(ks, b / C::kBlocksH));
+          if ((b + 1) % C::kBlocksH == 0) {
+            if (PAIR) mma_commit_multicast(kv_free(ks, b / C::kBlocksH), 3);
+            mma_commit(pv_done(ks, b / C::kBlocksH));
+          }
         }
       }
       __syncwarp();
@@ -466,13 +494,16 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // even after a wait timed out.
     int g = 0;
     for (int u = u0; g < nt; ++u) {
-      const ChunkUnit un = p.units[u];
+      ChunkUnit un = load_unit(p.units + u);
+      un.row0 += rank * R;
+      un.h0 += rank * R;
+      un.nrows = max(0, min(R, un.nrows - rank * R));
       const int i0 = g == 0 ? t0 - un.cum : 0;
       const int i1 = min(un.ntiles, i0 + nt - g);
       const bool whole = i0 == 0 && i1 == un.ntiles;
       const bool vA = hA < un.nrows, vB = hB < un.nrows;
       const int posA = un.pos0 + (un.h0 + hA) / H, posB = un.pos0 + (un.h0 + hB) / H;
-      const int p_hi = un.pos0 + (un.h0 + un.nrows - 1) / H;
+      const int p_lo = un.pos0 + un.h0 / H, p_hi = un.pos0 + (un.h0 + max(un.nrows, 1) - 1) / H;
       const float sinkA = whole && vA ? __ldg(p.attn_sink + (un.h0 + hA) % H) : 0.f;
       const float sinkB = whole && vB ? __ldg(p.attn_sink + (un.h0 + hB) % H) : 0.f;
       float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;  // l: this thread's share
@@ -480,7 +511,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int s = g & 1;
         const int j0 = chunk_tile_start(i, un.nf, un.lo, kTile);
         // whether every row of the unit sees the whole tile
-        const bool full = j0 + kTile - 1 <= un.pos0 &&
+        const bool full = j0 + kTile - 1 <= p_lo &&
                           (window == 0 || j0 > p_hi - window || j0 + kTile <= nfirst);
         pipe_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
         tc_fence_after();
@@ -688,7 +719,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       __syncwarp();
       tc_fence_after();
       named_bar_sync(1, kSmThreads);
-      const int slot = 2 * (int)blockIdx.x + (i0 == 0 ? 1 : 0);
+      const int slot = 2 * worker + (i0 == 0 ? 1 : 0);
       if (tq == 0 && hc == 0) {
 #pragma unroll
         for (int w2 = 0; w2 < 2; ++w2) {
@@ -711,7 +742,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
               p.lse[un.row0 + r] = lse;
             }
           } else {
-            p.part_ml[(size_t)slot * R + r] = make_float2(m, l);
+            p.part_ml[(size_t)slot * kUnitRows + rank * R + r] = make_float2(m, l);
           }
           s_fac[r] = f;
         }
@@ -787,7 +818,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
             uint32_t ov[16];
             tmem_ld16(tmem + lane_base + C::kOCol + b * R + c * 16, ov);
             tmem_wait_ld();
-            float* o = p.part_o + ((size_t)slot * R + c * 16) * D + d;
+            float* o = p.part_o + ((size_t)slot * kUnitRows + rank * R + c * 16) * D + d;
             if (d < D) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[(size_t)e * D] = __uint_as_float(ov[e]);
@@ -800,21 +831,26 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
   }
 
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  // (neither CTA of a pair leaves while the other may still reach its memory)
+  if (PAIR) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
   if (warp == kQkWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <typename F>
-cudaError_t for_shape(int R, int D, bool tma, F&& f) {
-#define SDA_CASE(RV, DV)                                                                      \
-  if (R == RV && D == DV)                                                                     \
-    return tma ? f(chunk_attn_kernel<RV, DV, true>, (size_t)Cfg<RV, DV>::kSmem, dim3(384))    \
-               : f(chunk_attn_kernel<RV, DV, false>, (size_t)Cfg<RV, DV>::kSmem, dim3(kGatherThreads));
-  SDA_CASE(16, 64) SDA_CASE(16, 128) SDA_CASE(16, 256) SDA_CASE(16, 512)
-  SDA_CASE(64, 64) SDA_CASE(64, 128) SDA_CASE(64, 256) SDA_CASE(64, 512)
-#undef SDA_CASE
+cudaError_t for_shape(int R, int D, int mode, F&& f) {
+#define SDA_MODE(RV, DV, MV)                  \
+  if (R == RV && D == DV && mode == MV)       \
+    return f(chunk_attn_kernel<RV, DV, MV>, (size_t)Cfg<RV, DV>::kSmem, dim3(MV == kGather ? kGatherThreads : 384));
+#define SDA_DIM(DV)                                            \
+  SDA_MODE(16, DV, kGather) SDA_MODE(16, DV, kTma)             \
+  SDA_MODE(64, DV, kGather) SDA_MODE(64, DV, kTma) SDA_MODE(64, DV, kPair)
+  SDA_DIM(64) SDA_DIM(128) SDA_DIM(256) SDA_DIM(512)
+#undef SDA_DIM
+#undef SDA_MODE
   return cudaErrorInvalidValue;
 }
 
@@ -865,13 +901,15 @@ bool pipe_map_pool(CUtensorMap* m, const void* base, uint64_t D, uint64_t groups
 cudaError_t chunk_prepare() {
   for (int R : {16, 64}) {
     for (int D : {64, 128, 256, 512}) {
-      for (bool tma : {false, true}) {
-        const cudaError_t e = for_shape(R, D, tma, [&](auto kernel, size_t smem, dim3) {
+      for (int mode : {kGather, kTma, kPair}) {
+        if (R == 16 && mode == kPair) continue;
+        const cudaError_t e = for_shape(R, D, mode, [&](auto kernel, size_t smem, dim3) {
           cudaError_t r =
               cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
           cudaFuncAttributes a;
           if (r == cudaSuccess) r = cudaFuncGetAttributes(&a, kernel);
-          if (r == cudaSuccess && !tma && a.numRegs < kGatherRegs) r = cudaErrorInvalidConfiguration;
+          if (r == cudaSuccess && mode == kGather && a.numRegs < kGatherRegs)
+            r = cudaErrorInvalidConfiguration;
           return r;
         });
         if (e != cudaSuccess) return e;
@@ -884,14 +922,14 @@ cudaError_t chunk_prepare() {
 cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
                               const float* attn_sink, float scale, void* out, float* lse,
                               const ChunkLayout& L, void* ws, cudaStream_t st) {
-  // TMA loads boxes of 16 rows, which blocks of a multiple of 16 rows keep
-  // together, counted in groups of 8 rows from `base` to the pool's end
   const int64_t rows = g.total_pages - g.base;
-  const bool tma = g.k_per_block % 16 == 0 && rows > 0 && rows % 8 == 0;
+  const int mode = L.pair ? kPair : (chunk_boxes(g) ? kTma : kGather);
+  const int R = L.pair ? L.R / 2 : L.R;
   CUtensorMap tq, tkv = {};
-  if (!pipe_map_2d(&tq, q, g.D, (uint64_t)g.T * g.H, 64, L.R) ||
-      (tma && !pipe_map_pool(&tkv, static_cast<const __nv_bfloat16*>(kv) + g.base * g.D, g.D,
-                             (uint64_t)rows / 8, g.D >= 256 ? g.D / 128 : g.D / 64, 2)))
+  if (!pipe_map_2d(&tq, q, g.D, (uint64_t)g.T * g.H, 64, R) ||
+      (mode != kGather && !pipe_map_pool(&tkv, static_cast<const __nv_bfloat16*>(kv) + g.base * g.D,
+                                         g.D, (uint64_t)rows / 8,
+                                         g.D >= 256 ? g.D / 128 : g.D / 64, 2)))
     return cudaErrorInvalidValue;
   char* base = static_cast<char*>(ws);
   Params p;
@@ -907,8 +945,9 @@ cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
   p.g = g;
   p.qk_scale_log2 = scale * kLog2e;
   p.wait_timeout_ns = current_wait_fault().timeout_ns;
-  return for_shape(L.R, g.D, tma, [&](auto kernel, size_t smem, dim3 threads) {
-    return launch_pdl(kernel, dim3(L.grid), threads, smem, st, tq, tkv, p);
+  return for_shape(R, g.D, mode, [&](auto kernel, size_t smem, dim3 threads) {
+    return launch_pdl_cluster(kernel, dim3(L.pair ? 2 * L.grid : L.grid), threads, L.pair ? 2 : 1,
+                              smem, st, tq, tkv, p);
   });
 }
 

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
 
 }  // namespace
 
-ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms) {
+ChunkLayout chunk_layout(int B, int T, int H, int D, bool boxes, int num_sms) {
   ChunkLayout L;
   const int64_t rows = (int64_t)T * H;
   // 16-row units where a sequence has at most 16 rows on average (a step of
@@ -203,8 +203,15 @@ ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms) {
   // of 64 positions fit, and the rows' masks and stores are not padded to 64.
   L.R = rows <= (int64_t)16 * B ? 16 : 64;
   L.tile = chunk_tile(L.R, D);
-  L.u_max = (int)((rows + L.R - 1) / L.R + B);
   L.grid = num_sms < kMaxPlanGrid ? num_sms : kMaxPlanGrid;
+  // With more than 128 rows a sequence on average two CTAs take 64 each of a
+  // unit of 128 and load every KV tile once for both.
+  L.pair = boxes && rows > (int64_t)128 * B;
+  if (L.pair) {
+    L.R = 128;
+    L.grid /= 2;
+  }
+  L.u_max = (int)((rows + L.R - 1) / L.R + B);
   size_t off = sizeof(ChunkHeader);
   L.units_off = off;
   off = align256(off + (size_t)L.u_max * sizeof(ChunkUnit));
