@@ -965,10 +965,7 @@ sda_status sda_chunk_attention_workspace_size(int B, int T, int H, int D, size_t
     note_cuda_error(e, "sda_chunk_attention_workspace_size");
     return SDA_ERR_CUDA;
   }
-  // whichever way the tiles are loaded
-  const size_t a = chunk_layout(B, T, H, D, false, caps.num_sms).total;
-  const size_t b = chunk_layout(B, T, H, D, true, caps.num_sms).total;
-  *bytes = a > b ? a : b;
+  *bytes = chunk_layout(B, T, H, D, caps.num_sms).total;
   return SDA_OK;
 }
 
@@ -1004,7 +1001,7 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
     note_cuda_error(e, "sda_chunk_attention");
     return SDA_ERR_CUDA;
   }
-  const ChunkLayout L = chunk_layout(B, T, H, D, chunk_boxes(g), caps.num_sms);
+  const ChunkLayout L = chunk_layout(B, T, H, D, caps.num_sms);
   if (workspace_bytes < L.total) return SDA_ERR_WORKSPACE;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   e = launch_chunk_plan(g, L, workspace, st);

@@ -82,7 +82,7 @@ inline bool chunk_boxes(const ChunkGeom& g) {
   return g.k_per_block % 16 == 0 && rows > 0 && rows % 8 == 0;
 }
 // The layout for B sequences of T tokens in all.
-ChunkLayout chunk_layout(int B, int T, int H, int D, bool boxes, int num_sms);
+ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms);
 
 cudaError_t chunk_prepare();  // one-time kernel attributes on the current device
 cudaError_t launch_chunk_plan(const ChunkGeom& g, const ChunkLayout& L, void* ws, cudaStream_t st);

@@ -24,8 +24,9 @@
 // swizzle atoms of 1 KB.
 #include <cuda_bf16.h>
 
-#include "sda_chunk.cuh"
-#include "sda_pipe.cuh"
+#include <type_traits>
+
+#include "sda_chunk_dev.cuh"
 
 namespace sda {
 
@@ -43,7 +44,6 @@ constexpr int kMaxStages = 6;
 constexpr int kGatherThreads = 640, kGatherRegs = 96;
 static_assert(kSmThreads * 128 + kLoadWarps * 32 * 64 + 128 * 96 <= kGatherThreads * kGatherRegs,
               "register split exceeds the launch allocation");
-constexpr float kHeadroom = 8.0f;  // log2: the running reference is raised when a score exceeds it by this
 
 enum Bar : int {
   kQFull = 0,
@@ -55,15 +55,7 @@ enum Bar : int {
   kDrainPv,
   kKvFull0,                              // + 2 * stage + half of D
   kPvDone0 = kKvFull0 + 2 * kMaxStages,  // + 2 * stage + half of D
-  kKvFree0 = kPvDone0 + 2 * kMaxStages,  // pairs: both CTAs' PV MMAs are done with it
-  kBars = kKvFree0 + 2 * kMaxStages
-};
-
-// The three kernels: how a CTA gets its KV tiles.
-enum Mode : int {
-  kGather = 0,  // row by row
-  kTma = 1,     // boxes of 16 rows
-  kPair = 2     // boxes of 16 rows, each loaded once for the two CTAs of a cluster
+  kBars = kPvDone0 + 2 * kMaxStages
 };
 
 template <int R, int D>
@@ -107,74 +99,11 @@ struct Cfg {
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-struct Params {
-  const __nv_bfloat16* kv;
-  const float* attn_sink;
-  __nv_bfloat16* out;
-  float* lse;
-  ChunkHeader* hdr;
-  const ChunkUnit* units;
-  const int* cta_unit;
-  float2* part_ml;
-  float* part_o;
-  ChunkGeom g;
-  float qk_scale_log2;
-  uint64_t wait_timeout_ns;
-};
-
-__device__ __forceinline__ ChunkUnit load_unit(const ChunkUnit* u) {
-  ChunkUnit d;
-  int4* w = reinterpret_cast<int4*>(&d);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) w[i] = __ldcg(reinterpret_cast<const int4*>(u) + i);
-  return d;
-}
-
-// Walks the CTA's tiles in order; every role walks the same ones.
-struct Cursor {
-  const ChunkUnit* units;
-  int u;           // unit
-  int i;           // logical tile within the unit
-  int left;        // tiles left to this CTA, this one included
-  bool first;      // first tile of this CTA's piece of the unit
-  int b, lo, hi, nf, ntiles;
-  __device__ __forceinline__ void load() {
-    const int4 a = __ldcg(reinterpret_cast<const int4*>(units + u) + 1);
-    ntiles = __ldcg(&units[u].ntiles);
-    b = __ldcg(&units[u].b);
-    lo = a.y;
-    hi = a.z;
-    nf = a.w;
-  }
-  __device__ __forceinline__ void init(const ChunkUnit* us, int u0, int t0, int n) {
-    units = us;
-    u = u0;
-    left = n;
-    first = true;
-    if (left > 0) {
-      load();
-      i = t0 - __ldcg(&units[u].cum);
-    }
-  }
-  __device__ __forceinline__ bool last() const { return left == 1 || i == ntiles - 1; }
-  __device__ __forceinline__ void next() {
-    first = false;
-    --left;
-    if (++i == ntiles && left > 0) {
-      ++u;
-      i = 0;
-      first = true;
-      load();
-    }
-  }
-};
-
-template <int R, int D, int MODE>
-__global__ void __launch_bounds__(MODE == kGather ? kGatherThreads : 384, 1)
+template <int R, int D, bool TMA>
+__global__ void __launch_bounds__(TMA ? 384 : kGatherThreads, 1)
 chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
-                  const __grid_constant__ CUtensorMap tmap_kv, const Params p) {
+                  const __grid_constant__ CUtensorMap tmap_kv, const ChunkParams p) {
   using C = Cfg<R, D>;
-  constexpr bool TMA = MODE != kGather, PAIR = MODE == kPair;
   constexpr int KS = C::kStages;
   constexpr int HV = C::kHalves;
   constexpr int kTile = C::kTile;
@@ -188,11 +117,6 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
   auto bar = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
   auto kv_full = [&](int s, int h) { return bar(kKvFull0 + 2 * s + h); };
   auto pv_done = [&](int s, int h) { return bar(kPvDone0 + 2 * s + h); };
-  // when a stage's half may be overwritten
-  auto kv_free = [&](int s, int h) { return bar((PAIR ? kKvFree0 : kPvDone0) + 2 * s + h); };
-  // A pair works on units of 2 R rows, CTA `rank` on R of them, over the same KV tiles.
-  const int rank = PAIR ? (int)(blockIdx.x & 1) : 0, worker = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-  constexpr int kUnitRows = PAIR ? 2 * R : R;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -202,7 +126,6 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       for (int h = 0; h < HV; ++h) {
         mbar_init(kv_full(s, h), TMA ? 1 : kLoadWarps * 32);
         mbar_init(pv_done(s, h), 1);
-        if (PAIR) mbar_init(kv_free(s, h), 2);
       }
     }
     for (int s = 0; s < 2; ++s) {
@@ -222,51 +145,29 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     tmem_relinquish();
   }
   tc_fence_before();
-  if (PAIR) cluster_sync();  // the other CTA's barriers are ready
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // everything above overlaps the plan; global memory only below
   pdl_trigger();
   const int per = __ldcg(&p.hdr->per), n_tiles = __ldcg(&p.hdr->n_tiles);
-  const long long t0l = (long long)worker * per;
+  const long long t0l = (long long)blockIdx.x * per;
   const int t0 = (int)min(t0l, (long long)n_tiles);
-  const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // this CTA's (or pair's) tiles
-  const int u0 = __ldcg(p.cta_unit + worker);
+  const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // this CTA's tiles
+  const int u0 = __ldcg(p.cta_unit + blockIdx.x);
   const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
-
-  // Pool row of position j of the cursor's unit; -1: no row of the unit sees
-  // it (it is not read: zeros).
-  auto row_of = [&](const Cursor& c, int j) {
-    if (j >= c.hi || (j < c.lo && j >= p.g.first)) return -1;
-    const int blk = __ldg(p.g.block_table + (size_t)c.b * p.g.max_blocks + j / p.g.k_per_block);
-    const long long s = p.g.base + (long long)blk * p.g.k_per_block + j % p.g.k_per_block;
-    if (blk < 0 || s >= p.g.total_pages) {
-      atomicExch(&p.hdr->error, 3);
-      return -1;
-    }
-    return (int)s;
-  };
 
   if (TMA && warp == kTmaWarp) {
     // ===================================================== KV tiles by TMA
-    // 16 positions lie in one block (tiles and blocks start at multiples of 16)
-    // and so in 16 pool rows in a row: lane i < kBoxes loads box i of every
-    // tile, each half of D as soon as the PV MMAs that last read it are done.  A
-    // box that no row sees is read from behind the pool, which fills it with zeros.
-    // (Boxes of 8 rows, and bulk prefetches of the tile two ahead into L2, kept
-    // this warp busier than the tensor pipe: one TMA instruction costs about 90
-    // cycles of issue.)
+    // Lane i < kBoxes loads box i of 16 rows of every tile, each half of D as soon
+    // as the PV MMAs that last read it are done.  (Boxes of 8 rows, and bulk
+    // prefetches of the tile two ahead into L2, kept this warp busier than the
+    // tensor pipe: one TMA instruction costs about 90 cycles of issue.)
     const int behind = (int)((p.g.total_pages - p.g.base) / 8);
-    auto box_of = [&](const Cursor& c) {  // in groups of 8 rows from `base` on
-      if (lane >= C::kBoxes) return behind;
-      const int j = chunk_tile_start(c.i, c.nf, c.lo, kTile) + lane * 16;
-      // the box's first position that is seen, if any, tells its block
-      int x = j;
-      if (x < c.lo && x >= p.g.first) x = c.lo;
-      if (x >= j + 16) return behind;
-      const int r = row_of(c, x);
-      return r < 0 ? behind : (int)((r - (x - j) - p.g.base) / 8);
+    auto box_of = [&](const Cursor& c) {
+      return lane < C::kBoxes
+                 ? box_group(p, c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + lane * 16)
+                 : behind;
     };
     Cursor c;  // runs a tile ahead of the copies
     c.init(p.units, u0, t0, nt);
@@ -286,31 +187,20 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        if (g >= KS) ok = pipe_wait(kv_free(s, h), ((g / KS) - 1) & 1, wc);
+        if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        // (of a pair, the other CTA's loads may land before this arrival: the
-        // phase completes with it)
         if (lane == 0) mbar_arrive_expect_tx(kv_full(s, h), C::kHalf);
         __syncwarp();
         const uint32_t dst = sKV + s * C::kStage + h * C::kHalf + lane * C::kBox;
-        if constexpr (PAIR) {
-          // each CTA loads a half of D (D <= 128: every other box) for both
-          if (lane < C::kBoxes && (HV == 2 ? h == rank : (lane & 1) == rank))
-            tma_load_4d_multicast(dst, &tmap_kv, 0, 0, h * C::kPanelsH, y, kv_full(s, h), 3);
-        } else {
-          if (lane < C::kBoxes) tma_load_4d(dst, &tmap_kv, 0, 0, h * C::kPanelsH, y, kv_full(s, h));
-        }
+        if (lane < C::kBoxes) tma_load_4d(dst, &tmap_kv, 0, 0, h * C::kPanelsH, y, kv_full(s, h));
         ++loads;
       }
       y = y_next;
     }
     // copies in flight land before the CTA's memory goes away (the last KS stages)
-    for (int x = max(0, loads - KS * HV); x < loads; ++x) {
+    for (int x = max(0, loads - KS * HV); x < loads; ++x)
       pipe_drain(kv_full((x / HV) % KS, x % HV), (x / HV / KS) & 1, wc);
-      // and so do the other CTA's arrivals
-      if (PAIR) pipe_drain(kv_free((x / HV) % KS, x % HV), (x / HV / KS) & 1, wc);
-    }
   } else if (!TMA && warp >= kLoadWarp0) {
     // ===================================================== KV rows one by one
     setmaxnreg_dec<64>();
@@ -320,7 +210,9 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const int v = warp - kLoadWarp0;
     const uint4* kv4 = reinterpret_cast<const uint4*>(p.kv);
     auto slot_of = [&](const Cursor& c) {  // lanes 0 .. kRows - 1: rows kRows v + lane
-      return lane < kRows ? row_of(c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + v * kRows + lane) : -1;
+      return lane < kRows
+                 ? seen_row(p, c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + v * kRows + lane)
+                 : -1;
     };
     auto prefetch = [&](int slot) {
       if (slot >= 0) bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + (size_t)slot * D * 2, D * 2);
@@ -348,7 +240,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const uint32_t stage = sKV + s * C::kStage;
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        if (g >= KS) ok = pipe_wait(kv_free(s, h), ((g / KS) - 1) & 1, wc);
+        if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int ch = h * kCh + lane % kCh;  // 16-byte chunk of the row
@@ -379,7 +271,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     int pieces = 0, q_loads = 0;
     bool ok = true;
     auto load_q = [&]() {
-      const int row = __ldcg(&p.units[c.u].row0) + rank * R;
+      const int row = __ldcg(&p.units[c.u].row0);
       if (elect_one()) {
         mbar_arrive_expect_tx(bar(kQFull), C::kPanels * C::kPanelQ);
 #pragma unroll
@@ -458,10 +350,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
                      sdesc_advance(a0, b / C::kBlocksH * C::kHalf + 2 * (b % C::kBlocksH) * 1024 +
                                            k * 2 * C::kGroup),
                      sdesc_advance(b0, k * 32), C::kIdescPV, k ? 1u : add);
-          if ((b + 1) % C::kBlocksH == 0) {
-            if (PAIR) mma_commit_multicast(kv_free(ks, b / C::kBlocksH), 3);
-            mma_commit(pv_done(ks, b / C::kBlocksH));
-          }
+          if ((b + 1) % C::kBlocksH == 0) mma_commit(pv_done(ks, b / C::kBlocksH));
         }
       }
       __syncwarp();
@@ -494,18 +383,16 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // even after a wait timed out.
     int g = 0;
     for (int u = u0; g < nt; ++u) {
-      ChunkUnit un = load_unit(p.units + u);
-      un.row0 += rank * R;
-      un.h0 += rank * R;
-      un.nrows = max(0, min(R, un.nrows - rank * R));
+      const ChunkUnit un = load_unit(p.units + u);
       const int i0 = g == 0 ? t0 - un.cum : 0;
       const int i1 = min(un.ntiles, i0 + nt - g);
       const bool whole = i0 == 0 && i1 == un.ntiles;
       const bool vA = hA < un.nrows, vB = hB < un.nrows;
       const int posA = un.pos0 + (un.h0 + hA) / H, posB = un.pos0 + (un.h0 + hB) / H;
-      const int p_lo = un.pos0 + un.h0 / H, p_hi = un.pos0 + (un.h0 + max(un.nrows, 1) - 1) / H;
+      const int p_lo = un.pos0, p_hi = un.pos0 + (un.h0 + un.nrows - 1) / H;
       const float sinkA = whole && vA ? __ldg(p.attn_sink + (un.h0 + hA) % H) : 0.f;
       const float sinkB = whole && vB ? __ldg(p.attn_sink + (un.h0 + hB) % H) : 0.f;
+      const float scA = vA ? sc : 0.f, scB = vB ? sc : 0.f;
       float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;  // l: this thread's share
       for (int i = i0; i < i1; ++i, ++g) {
         const int s = g & 1;
@@ -513,6 +400,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // whether every row of the unit sees the whole tile
         const bool full = j0 + kTile - 1 <= p_lo &&
                           (window == 0 || j0 > p_hi - window || j0 + kTile <= nfirst);
+        // P buffer s is free once the PV of tile g - 2 is done (long before the scores are)
+        if (g >= 2) pipe_wait(pv_done((g - 2) % KS, HV - 1), ((g - 2) / KS) & 1, wc);
         pipe_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
         tc_fence_after();
         float x[kE];
@@ -577,11 +466,6 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
             fence_proxy_async_smem();  // read by the PV MMA, issued after a later barrier
           }
         }
-        // P buffer s is free once the PV of tile g - 2 is done
-        if (g >= 2) {
-          if (lane == 0) pipe_wait(pv_done((g - 2) % KS, HV - 1), ((g - 2) / KS) & 1, wc);
-          __syncwarp();
-        }
         // p = 2^(x scale - m) in bf16 into rows hA, hB of P (K-major, 128-byte
         // swizzle) with two stmatrix.x4.  The MMA multiplies the rounded p, the
         // denominator sums the unrounded ones: each weight is off by at most
@@ -591,8 +475,10 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
           return prow + (uint32_t)(((kReps * hc + c) ^ (lane & 7)) << 4);
         };
         float sumA, sumB;
-        auto weights = [&]() {
-          bool over = false;
+        // (rows past the unit's end have factor 0: their weights, never used, stay finite
+        // and cast no vote)
+        auto weights = [&](auto masked) {
+          float top = -INFINITY;
           sumA = sumB = 0.f;
           uint32_t pa[kReps], pb[kReps];
 #pragma unroll
@@ -600,9 +486,9 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
             float e[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const bool ok = (see >> (4 * rep + k)) & 1u;
-              const float arg = fmaf(x[4 * rep + k], sc, -((k < 2) ? mA : mB));
-              over = over || (ok && ((k < 2) ? vA : vB) && arg > kHeadroom);
+              const float arg = fmaf(x[4 * rep + k], k < 2 ? scA : scB, -((k < 2) ? mA : mB));
+              const bool ok = !decltype(masked)::value || ((see >> (4 * rep + k)) & 1u);
+              top = fmaxf(top, ok ? arg : -INFINITY);
               e[k] = ok ? ex2_approx(arg) : 0.f;
             }
             sumA += e[0] + e[1];
@@ -623,14 +509,14 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
               stmatrix_x1(pchunk(2) + 1024, pb[2]);
             }
           }
-          return over;
+          return top > kHeadroom;
         };
         // The first tile of a piece sets m to its exact row maxima; a later one
         // is weighted against the current m, and only if a score exceeds it by
         // the headroom do the warps raise m and rescale O^T (p stays below 2^8).
         bool exact = i == i0;
         if (!exact) {
-          const bool over = weights();
+          const bool over = full ? weights(std::false_type{}) : weights(std::true_type{});
           fence_proxy_async_smem();
           exact = named_bar_or(1, kSmThreads, over);
         }
@@ -639,8 +525,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
           for (int e = 0; e < kE; ++e) {
             if ((see >> e) & 1u) {
-              if ((e & 3) < 2) eA = fmaxf(eA, x[e] * sc);
-              else eB = fmaxf(eB, x[e] * sc);
+              if ((e & 3) < 2) eA = fmaxf(eA, x[e] * scA);
+              else eB = fmaxf(eB, x[e] * scB);
             }
           }
 #pragma unroll
@@ -669,7 +555,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
             lB *= alphaB;
             mB = eB;
           }
-          weights();
+          weights(std::true_type{});
           fence_proxy_async_smem();
           if (i > i0) {
             if (tq == 0 && hc == 0) {
@@ -719,7 +605,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       __syncwarp();
       tc_fence_after();
       named_bar_sync(1, kSmThreads);
-      const int slot = 2 * worker + (i0 == 0 ? 1 : 0);
+      const int slot = 2 * (int)blockIdx.x + (i0 == 0 ? 1 : 0);
       if (tq == 0 && hc == 0) {
 #pragma unroll
         for (int w2 = 0; w2 < 2; ++w2) {
@@ -742,7 +628,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
               p.lse[un.row0 + r] = lse;
             }
           } else {
-            p.part_ml[(size_t)slot * kUnitRows + rank * R + r] = make_float2(m, l);
+            p.part_ml[(size_t)slot * R + r] = make_float2(m, l);
           }
           s_fac[r] = f;
         }
@@ -818,7 +704,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
             uint32_t ov[16];
             tmem_ld16(tmem + lane_base + C::kOCol + b * R + c * 16, ov);
             tmem_wait_ld();
-            float* o = p.part_o + ((size_t)slot * kUnitRows + rank * R + c * 16) * D + d;
+            float* o = p.part_o + ((size_t)slot * R + c * 16) * D + d;
             if (d < D) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[(size_t)e * D] = __uint_as_float(ov[e]);
@@ -833,24 +719,21 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
 
   __syncwarp();
   tc_fence_before();
-  // (neither CTA of a pair leaves while the other may still reach its memory)
-  if (PAIR) cluster_sync();
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   if (warp == kQkWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <typename F>
-cudaError_t for_shape(int R, int D, int mode, F&& f) {
-#define SDA_MODE(RV, DV, MV)                  \
-  if (R == RV && D == DV && mode == MV)       \
-    return f(chunk_attn_kernel<RV, DV, MV>, (size_t)Cfg<RV, DV>::kSmem, dim3(MV == kGather ? kGatherThreads : 384));
-#define SDA_DIM(DV)                                            \
-  SDA_MODE(16, DV, kGather) SDA_MODE(16, DV, kTma)             \
-  SDA_MODE(64, DV, kGather) SDA_MODE(64, DV, kTma) SDA_MODE(64, DV, kPair)
-  SDA_DIM(64) SDA_DIM(128) SDA_DIM(256) SDA_DIM(512)
-#undef SDA_DIM
-#undef SDA_MODE
+cudaError_t for_shape(int R, int D, bool tma, F&& f) {
+#define SDA_CASE(RV, DV)                                                                   \
+  if (R == RV && D == DV)                                                                  \
+    return tma ? f(chunk_attn_kernel<RV, DV, true>, (size_t)Cfg<RV, DV>::kSmem, dim3(384)) \
+               : f(chunk_attn_kernel<RV, DV, false>, (size_t)Cfg<RV, DV>::kSmem,           \
+                   dim3(kGatherThreads));
+  SDA_CASE(16, 64) SDA_CASE(16, 128) SDA_CASE(16, 256) SDA_CASE(16, 512)
+  SDA_CASE(64, 64) SDA_CASE(64, 128) SDA_CASE(64, 256) SDA_CASE(64, 512)
+#undef SDA_CASE
   return cudaErrorInvalidValue;
 }
 
@@ -901,38 +784,26 @@ bool pipe_map_pool(CUtensorMap* m, const void* base, uint64_t D, uint64_t groups
 cudaError_t chunk_prepare() {
   for (int R : {16, 64}) {
     for (int D : {64, 128, 256, 512}) {
-      for (int mode : {kGather, kTma, kPair}) {
-        if (R == 16 && mode == kPair) continue;
-        const cudaError_t e = for_shape(R, D, mode, [&](auto kernel, size_t smem, dim3) {
+      for (bool tma : {false, true}) {
+        const cudaError_t e = for_shape(R, D, tma, [&](auto kernel, size_t smem, dim3) {
           cudaError_t r =
               cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
           cudaFuncAttributes a;
           if (r == cudaSuccess) r = cudaFuncGetAttributes(&a, kernel);
-          if (r == cudaSuccess && mode == kGather && a.numRegs < kGatherRegs)
-            r = cudaErrorInvalidConfiguration;
+          if (r == cudaSuccess && !tma && a.numRegs < kGatherRegs) r = cudaErrorInvalidConfiguration;
           return r;
         });
         if (e != cudaSuccess) return e;
       }
     }
   }
-  return cudaSuccess;
+  return pair_prepare();
 }
 
-cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
-                              const float* attn_sink, float scale, void* out, float* lse,
-                              const ChunkLayout& L, void* ws, cudaStream_t st) {
-  const int64_t rows = g.total_pages - g.base;
-  const int mode = L.pair ? kPair : (chunk_boxes(g) ? kTma : kGather);
-  const int R = L.pair ? L.R / 2 : L.R;
-  CUtensorMap tq, tkv = {};
-  if (!pipe_map_2d(&tq, q, g.D, (uint64_t)g.T * g.H, 64, R) ||
-      (mode != kGather && !pipe_map_pool(&tkv, static_cast<const __nv_bfloat16*>(kv) + g.base * g.D,
-                                         g.D, (uint64_t)rows / 8,
-                                         g.D >= 256 ? g.D / 128 : g.D / 64, 2)))
-    return cudaErrorInvalidValue;
+ChunkParams chunk_params(const void* kv, const ChunkGeom& g, const float* attn_sink, float scale,
+                         void* out, float* lse, const ChunkLayout& L, void* ws) {
   char* base = static_cast<char*>(ws);
-  Params p;
+  ChunkParams p;
   p.kv = static_cast<const __nv_bfloat16*>(kv);
   p.attn_sink = attn_sink;
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -945,9 +816,22 @@ cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
   p.g = g;
   p.qk_scale_log2 = scale * kLog2e;
   p.wait_timeout_ns = current_wait_fault().timeout_ns;
-  return for_shape(R, g.D, mode, [&](auto kernel, size_t smem, dim3 threads) {
-    return launch_pdl_cluster(kernel, dim3(L.pair ? 2 * L.grid : L.grid), threads, L.pair ? 2 : 1,
-                              smem, st, tq, tkv, p);
+  return p;
+}
+
+cudaError_t launch_chunk_attn(const void* q, const void* kv, const ChunkGeom& g,
+                              const float* attn_sink, float scale, void* out, float* lse,
+                              const ChunkLayout& L, void* ws, cudaStream_t st) {
+  const bool tma = chunk_boxes(g);
+  const ChunkParams p = chunk_params(kv, g, attn_sink, scale, out, lse, L, ws);
+  CUtensorMap tq, tkv = {};
+  if (!pipe_map_2d(&tq, q, g.D, (uint64_t)g.T * g.H, 64, L.pair ? L.R / 2 : L.R) ||
+      (tma && !pipe_map_pool(&tkv, p.kv + g.base * g.D, g.D, (uint64_t)(g.total_pages - g.base) / 8,
+                             g.D >= 256 ? g.D / 128 : g.D / 64, 2)))
+    return cudaErrorInvalidValue;
+  if (L.pair) return launch_chunk_pair(tq, tkv, p, tma, L, st);
+  return for_shape(L.R, g.D, tma, [&](auto kernel, size_t smem, dim3 threads) {
+    return launch_pdl(kernel, dim3(L.grid), threads, smem, st, tq, tkv, p);
   });
 }
 

@@ -1,0 +1,876 @@
+// sda_chunk_pair.cu -- the chunk attention for sequences with many rows: two
+// CTAs of a cluster work as one on 128 rows of q (tcgen05 cta_group::2).
+//
+// What bounds the one-CTA kernel at D = 512 is shared-memory bandwidth: with 64
+// rows of q, every 48 positions its MMAs read 190 KB of shared memory (128 bytes
+// a cycle) while TMA writes 48 KB.  A pair halves the operand that its CTAs share:
+//   S [128 x 64] = Q K^T     CTA r holds q rows 64 r .. and positions 32 r .. of the tile
+//   O^T [D x 128] += V^T P^T CTA r holds the D / 2 columns from r D / 2 on of all 64
+//                            positions (so O^T of those columns, for all 128 rows) and
+//                            the weights P of its own 64 rows
+// Measured: 26 cycles for QK's M128 N64 K16 and 65 for PV's M256 N128 K16, 1365 a
+// tile against 1839 with one CTA a tile.  A cached row then lies in shared memory as
+// key (32 rows, all of D) and as value (64 rows, half of D); the two rings are freed
+// by different MMAs, so that the keys of the next tile land while the weights of
+// this one are computed.
+//
+// S [M = 128, cta_group::2]: TMEM lanes 0..63 of CTA r hold its rows at the tile's
+// first 32 positions, lanes 64..127 the same rows at the other 32.
+//
+// Roles in each CTA (the MMA warps issue in CTA 0, for both):
+//   warps 0..7   softmax and epilogue of the CTA's own 64 rows / own half of D
+//   warp 8       QK MMAs; q loads        warp 9   PV MMAs, and the decision below
+//   warp 10, 11  keys and values: by TMA, or (gather kernel) passing on to CTA 0
+//                that the CTA's loader warps have landed a stage
+//   warps 12..19 (gather kernel) 4 warps copy keys, 4 values, 16-byte cp.async
+//
+// O^T of a row lies in both CTAs, so raising the row's running reference (rare) takes
+// both: with its weights of tile g ready, each CTA tells CTA 0 whether it raised one;
+// PV warp 0 passes the answers on to all softmax warps ("decided"), which look at it
+// before they go on with tile g + 1; if a reference was raised they scale O^T first,
+// and the PV MMAs of tile g wait for that.
+#include <type_traits>
+
+#include "sda_chunk_dev.cuh"
+
+namespace sda {
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kR = 64;      // rows of q of a CTA
+constexpr int kTile = 64;   // positions of a tile
+constexpr int kKeys = 32;   // of them, keys of a CTA
+constexpr int kSmThreads = 256, kSmWarps = 8;
+constexpr int kQkWarp = 8, kPvWarp = 9, kKeyWarp = 10, kValWarp = 11;
+constexpr int kLoadWarp0 = 12, kLoadWarps = 4;  // gather kernel: 4 for keys, then 4 for values
+// Gather kernel: 640 threads launch with 96 registers each; the softmax warps
+// grow to 128 and the loaders shrink to 64.
+constexpr int kGatherThreads = 640, kGatherRegs = 96;
+static_assert(kSmThreads * 128 + 2 * kLoadWarps * 32 * 64 + 128 * 96 <= kGatherThreads * kGatherRegs,
+              "register split exceeds the launch allocation");
+constexpr int kMaxStages = 3;
+
+enum Bar : int {
+  kQFull = 0,   // CTA 0: q of both CTAs
+  kQEmpty,      // both
+  kSFull0,      // both
+  kSEmpty0 = kSFull0 + 2,   // CTA 0: the softmax warps of both
+  kPReady0 = kSEmpty0 + 2,  // CTA 0: weights of both
+  kDecided0 = kPReady0 + 2, // both
+  kScaled = kDecided0 + 2,  // CTA 0: the softmax warps of both
+  kFac,                     // both: the final factors of both CTAs' rows
+  kKFull0,                             // CTA 0
+  kVFull0 = kKFull0 + kMaxStages,      // CTA 0
+  kKFree0 = kVFull0 + kMaxStages,      // both
+  kVFree0 = kKFree0 + kMaxStages,      // both
+  kKLanded0 = kVFree0 + kMaxStages,    // gather kernel: this CTA's keys / values
+  kVLanded0 = kKLanded0 + kMaxStages,
+  kBars = kVLanded0 + kMaxStages
+};
+enum Cmd : int { kRaise0 = 1, kRaise1 = 2, kPoison = 4 };
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64, kPanelsH = kPanels / 2;
+  static constexpr int kBlocks = D / 256;             // PV MMAs of 256 rows of O^T
+  static constexpr int kStages = D == 512 ? 2 : 3;
+  static constexpr int kGroup = kPanelsH * 1024;      // 8 rows of half of D
+  static constexpr int kKHalf = kKeys / 8 * kGroup;
+  static constexpr int kKBytes = 2 * kKHalf;          // keys: [half of D][4 groups]
+  static constexpr int kVBytes = kTile / 8 * kGroup;  // values: [8 groups] of the CTA's half
+  static constexpr int kBox = 2 * kGroup;             // a TMA box: 16 rows of a half
+  static constexpr int kPBytes = kR * 128;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kPanels * kR * 128;
+  static constexpr int kOffV = kOffK + kStages * kKBytes;
+  static constexpr int kOffP = kOffV + kStages * kVBytes;  // two P buffers; the epilogue's staging
+  static constexpr int kOffBar = kOffP + 2 * kPBytes;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;     // tmem base, abort flag
+  static constexpr int kOffFlag = kOffMisc + 16;           // int [2 tiles][2 CTAs] (CTA 0)
+  static constexpr int kOffCmd = kOffFlag + 16;            // int [2 tiles]
+  static constexpr int kOffAlpha = kOffCmd + 16;           // float [2 tiles][128 rows]
+  static constexpr int kOffFac = kOffAlpha + 1024;         // float [128 rows]
+  static constexpr int kOffPart = kOffFac + 512;           // float [2 tiles][4 parts][64]: maxima; at the end l, m
+  static constexpr int kSmem = kOffPart + 2048 + 1024;
+  static constexpr int kOCol = 64;                         // O^T block b at columns 64 + 128 b
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kTile, false, false);
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(256, 128, true, false);
+  static_assert(kOCol + 128 * kBlocks <= 512, "TMEM columns");
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+// ---------------------------------------------------------------- pair PTX
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs once this thread's earlier pair MMAs are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t cta) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t mapped) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t mapped, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapped), "r"(v) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// pipe_wait for barriers that threads of the other CTA arrive on.
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const PipeWait& w) {
+  if (try_wait_cluster(bar, parity)) return true;
+  if (*w.abort_flag) return false;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*w.abort_flag) return false;
+      if (globaltimer_ns() - t0 > w.timeout_ns) {
+        *w.abort_flag = 1;
+        atomicExch(w.error, 1);
+        return false;
+      }
+    }
+  }
+}
+// Tiled loads into this CTA that complete on a barrier of the pair's CTA 0.
+__device__ __forceinline__ void tma_pair_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w,
+                                            uint32_t bar0) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar0)
+      : "memory");
+}
+__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar0) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar0)
+      : "memory");
+}
+
+template <int D, bool TMA>
+__global__ void __launch_bounds__(TMA ? 384 : kGatherThreads, 1)
+chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                  const __grid_constant__ CUtensorMap tmap_kv, const ChunkParams p) {
+  using C = Cfg<D>;
+  constexpr int KS = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t sQ = sbase + C::kOffQ, sK = sbase + C::kOffK, sV = sbase + C::kOffV,
+                 sP = sbase + C::kOffP;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
+  const int rank = (int)(blockIdx.x & 1), worker = (int)(blockIdx.x >> 1);
+  auto bar0 = [&](int i) { return map_cta(bar(i), 0); };  // of CTA 0
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(kQFull), 1);
+    mbar_init(bar(kQEmpty), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kSFull0 + s), 1);
+      mbar_init(bar(kSEmpty0 + s), 2 * kSmWarps);
+      mbar_init(bar(kPReady0 + s), 2);
+      mbar_init(bar(kDecided0 + s), 1);
+    }
+    mbar_init(bar(kScaled), 2 * kSmWarps);
+    mbar_init(bar(kFac), 2);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(bar(kKFull0 + s), TMA ? 1 : 2);  // an expected count of bytes, or one CTA each
+      mbar_init(bar(kVFull0 + s), TMA ? 1 : 2);
+      mbar_init(bar(kKFree0 + s), 1);
+      mbar_init(bar(kVFree0 + s), 1);
+      mbar_init(bar(kKLanded0 + s), kLoadWarps * 32);
+      mbar_init(bar(kVLanded0 + s), kLoadWarps * 32);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmap_q);
+    if (TMA) tma_prefetch_desc(&tmap_kv);
+  }
+  if (warp == kQkWarp) {  // both CTAs' warps together
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // both CTAs' barriers and TMEM are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // everything above overlaps the plan; global memory only below
+  pdl_trigger();
+  const int per = __ldcg(&p.hdr->per), n_tiles = __ldcg(&p.hdr->n_tiles);
+  const long long t0l = (long long)worker * per;
+  const int t0 = (int)min(t0l, (long long)n_tiles);
+  const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // the pair's tiles
+  const int u0 = __ldcg(p.cta_unit + worker);
+  const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
+
+  if (warp == kKeyWarp || warp == kValWarp) {
+    const bool keys = warp == kKeyWarp;
+    const int full0 = keys ? kKFull0 : kVFull0, free0 = keys ? kKFree0 : kVFree0;
+    bool ok = true;
+    int g = 0;
+    if constexpr (TMA) {
+      // ===================================================== keys / values by TMA
+      // Lane i < 4 loads a box of 16 rows of half of D: of the keys, half i / 2 of
+      // rows 16 (i % 2) .. of the CTA's 32; of the values, the CTA's half of rows 16 i ..
+      const int off = keys ? rank * kKeys + (lane & 1) * 16 : lane * 16;
+      const int half = keys ? (lane >> 1) & 1 : rank;
+      const uint32_t dst0 = keys ? sK + half * C::kKHalf + (lane & 1) * C::kBox : sV + lane * C::kBox;
+      const uint32_t bytes = keys ? C::kKBytes : C::kVBytes;
+      const int behind = (int)((p.g.total_pages - p.g.base) / 8);
+      auto box_of = [&](const Cursor& c) {
+        return lane < 4 ? box_group(p, c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + off) : behind;
+      };
+      Cursor c;  // runs a tile ahead of the copies
+      c.init(p.units, u0, t0, nt);
+      int y = behind;
+      if (c.left > 0) {
+        y = box_of(c);
+        c.next();
+      }
+      for (; g < nt; ++g) {
+        const int s = g % KS;
+        int y_next = behind;
+        if (c.left > 0) {
+          y_next = box_of(c);
+          c.next();
+        }
+        if (g >= KS) ok = pipe_wait(bar(free0 + s), ((g / KS) - 1) & 1, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        // (CTA 1's bytes may land before CTA 0 has said how many to expect: the
+        // barrier's phase cannot end before that arrival)
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(full0 + s), 2 * bytes);
+        __syncwarp();
+        if (lane < 4)
+          tma_pair_4d(dst0 + s * bytes, &tmap_kv, 0, 0, half * C::kPanelsH, y, bar0(full0 + s));
+        y = y_next;
+      }
+    } else {
+      // ===================================================== passing on landed stages
+      for (; g < nt; ++g) {
+        const int s = g % KS;
+        ok = pipe_wait(bar((keys ? kKLanded0 : kVLanded0) + s), (g / KS) & 1, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        fence_proxy_async_smem();  // the copies were made through the generic proxy
+        if (lane == 0) arrive_cluster(bar0(full0 + s));
+        __syncwarp();
+      }
+    }
+    // Every stage that was filled has been read (so its copies have landed) and
+    // every arrival of the MMA warps has come in before this CTA's memory goes away.
+    for (int x = max(0, g - KS); x < g; ++x) pipe_drain(bar(free0 + x % KS), (x / KS) & 1, wc);
+  } else if (!TMA && warp >= kLoadWarp0) {
+    // ===================================================== rows one by one
+    setmaxnreg_dec<64>();
+    const bool keys = warp < kLoadWarp0 + kLoadWarps;
+    const int v = (warp - kLoadWarp0) % kLoadWarps;
+    const int free0 = keys ? kKFree0 : kVFree0, landed0 = keys ? kKLanded0 : kVLanded0;
+    // a warp copies 8 key rows of D, or 16 value rows of half of D
+    constexpr int kChK = D / 8, kChV = D / 16;
+    const int rows = keys ? kKeys / kLoadWarps : kTile / kLoadWarps;
+    const int off = keys ? rank * kKeys + v * rows : v * rows;
+    const uint4* kv4 = reinterpret_cast<const uint4*>(p.kv);
+    auto slot_of = [&](const Cursor& c) {
+      return lane < rows ? seen_row(p, c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + off + lane) : -1;
+    };
+    Cursor c;  // runs two tiles ahead of the copies
+    c.init(p.units, u0, t0, nt);
+    int sl0 = -1, sl1 = -1;
+    if (c.left > 0) {
+      sl0 = slot_of(c);
+      c.next();
+    }
+    if (c.left > 0) {
+      sl1 = slot_of(c);
+      c.next();
+    }
+    bool ok = true;
+    for (int g = 0; g < nt; ++g) {
+      const int s = g % KS;
+      int sl2 = -1;
+      if (c.left > 0) {
+        sl2 = slot_of(c);
+        c.next();
+      }
+      if (g >= KS) ok = pipe_wait(bar(free0 + s), ((g / KS) - 1) & 1, wc);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      auto copy = [&](uint32_t dst, int slot, int ch) {
+        const uint4* src = slot >= 0 ? kv4 + (size_t)slot * (D / 8) + ch : kv4;
+        cp_async16(dst, src, slot >= 0 ? 16u : 0u);
+      };
+      if (keys) {
+        for (int x = 0; x < kKeys / kLoadWarps; ++x) {
+          const int slot = __shfl_sync(0xffffffffu, sl0, x);
+          const int r = v * (kKeys / kLoadWarps) + x;
+          const uint32_t row = sK + s * C::kKBytes + (r >> 3) * C::kGroup + (r & 7) * 128;
+#pragma unroll
+          for (int c0 = 0; c0 < kChK; c0 += 32) {
+            const int ch = c0 + lane, pn = ch >> 3;
+            copy(row + pn / C::kPanelsH * C::kKHalf + pn % C::kPanelsH * 1024 + (((ch & 7) ^ (r & 7)) << 4),
+                 slot, ch);
+          }
+        }
+      } else {
+        constexpr int kRowsPer = 32 / kChV;
+        for (int x = 0; x < kTile / kLoadWarps; x += kRowsPer) {
+          const int rl = x + lane / kChV;
+          const int slot = __shfl_sync(0xffffffffu, sl0, rl);
+          const int r = v * (kTile / kLoadWarps) + rl, ch = lane % kChV;
+          copy(sV + s * C::kVBytes + (r >> 3) * C::kGroup + (ch >> 3) * 1024 + (r & 7) * 128 +
+                   (((ch & 7) ^ (r & 7)) << 4),
+               slot, rank * kChV + ch);
+        }
+      }
+      cp_async_arrive(bar(landed0 + s));  // once this thread's copies have landed
+      sl0 = sl1;
+      sl1 = sl2;
+    }
+    cp_async_wait_all();
+  } else if (warp == kQkWarp) {
+    // ===================================================== q loads (both), QK MMAs (CTA 0)
+    Cursor c;
+    c.init(p.units, u0, t0, nt);
+    constexpr uint32_t kQBytes = C::kPanels * kR * 128;
+    int pieces = 0;
+    bool ok = true;
+    auto load_q = [&]() {
+      const int row = __ldcg(&p.units[c.u].row0) + rank * kR;
+      if (elect_one()) {
+        if (rank == 0) mbar_arrive_expect_tx(bar(kQFull), 2 * kQBytes);
+#pragma unroll
+        for (int x = 0; x < C::kPanels; ++x)
+          tma_pair_2d(sQ + x * kR * 128, &tmap_q, x * 64, row, bar0(kQFull));
+      }
+      __syncwarp();
+    };
+    bool loaded = false;
+    if (c.left > 0) {
+      load_q();
+      loaded = true;
+    }
+    const uint64_t a0 = sdesc_sw128(sQ, 16, 1024);
+    for (int g = 0; g < nt; ++g) {
+      const int s = g & 1, ks = g % KS;
+      const bool last = c.last();
+      if (rank == 0) {
+        if (g >= 2) ok = pair_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
+        if (ok && c.first) ok = pipe_wait(bar(kQFull), pieces & 1, wc);
+        if (ok) ok = pair_wait(bar(kKFull0 + ks), (g / KS) & 1, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (!TMA) fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t b0 = sdesc_sw128(sK + ks * C::kKBytes, 16, C::kGroup);
+        if (elect_one()) {
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_pair(tmem + s * 32, sdesc_advance(a0, pn * kR * 128 + k * 32),
+                       sdesc_advance(b0, pn / C::kPanelsH * C::kKHalf + pn % C::kPanelsH * 1024 + k * 32),
+                       C::kIdescQK, (pn || k) ? 1u : 0u);
+          }
+          commit_pair(bar(kSFull0 + s));
+          commit_pair(bar(kKFree0 + ks));
+          if (last) commit_pair(bar(kQEmpty));
+        }
+        __syncwarp();
+      }
+      c.next();
+      if (last) {  // q of the next unit, once this unit's MMAs have read q
+        ok = __all_sync(0xffffffffu, pipe_wait(bar(kQEmpty), pieces & 1, wc));
+        loaded = false;
+        if (!ok) break;
+        if (c.left > 0) {
+          load_q();
+          loaded = true;
+        }
+        ++pieces;
+      }
+    }
+    // a q load that nothing has read (after a timeout) lands before the memory goes away
+    if (loaded && rank == 0) pipe_drain(bar(kQFull), pieces & 1, wc);
+  } else if (warp == kPvWarp) {
+    // ===================================================== decision, PV MMAs (CTA 0)
+    if (rank == 0) {
+      Cursor c;
+      c.init(p.units, u0, t0, nt);
+      volatile int* flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag);
+      int scaled = 0;
+      for (int g = 0; g < nt; ++g) {
+        const int s = g & 1, ks = g % KS;
+        bool ok = pair_wait(bar(kPReady0 + s), (g >> 1) & 1, wc);
+        const int f0 = flag[2 * s], f1 = flag[2 * s + 1];
+        const int cmd = (f0 & 1 ? kRaise0 : 0) | (f1 & 1 ? kRaise1 : 0) | ((f0 | f1) & 2 ? kPoison : 0);
+        if (cmd && ok) ok = pair_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);  // values to be looked at
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane < 2) {  // one lane tells each CTA
+          store_cluster(map_cta(sbase + C::kOffCmd + 4 * s, lane), (uint32_t)cmd);
+          arrive_cluster(map_cta(bar(kDecided0 + s), lane));
+        }
+        __syncwarp();
+        if (cmd) {
+          ok = pair_wait(bar(kScaled), scaled & 1, wc);
+          ++scaled;
+        }
+        if (ok) ok = pair_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (!TMA) fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t a0 = sdesc_sw128(sV + ks * C::kVBytes, 1024, C::kGroup);
+        const uint64_t b0 = sdesc_sw128(sP + s * C::kPBytes, 16, 1024);
+        const uint32_t add = c.first ? 0u : 1u;
+        if (elect_one()) {
+#pragma unroll
+          for (int b = 0; b < C::kBlocks; ++b) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_pair(tmem + C::kOCol + b * 128, sdesc_advance(a0, 2 * b * 1024 + k * 2 * C::kGroup),
+                       sdesc_advance(b0, k * 32), C::kIdescPV, k ? 1u : add);
+          }
+          commit_pair(bar(kVFree0 + ks));
+        }
+        __syncwarp();
+        c.next();
+      }
+    }
+  } else if (warp < kSmWarps) {
+    // ===================================================== softmax and epilogue
+    // Warp w reads TMEM lane quadrant q4 = w % 4 -- rows 32 (q4 % 2) .. + 31 at the
+    // tile's positions 32 kh .., kh = q4 / 2 -- and of these the 16 positions from
+    // 16 hc on, hc = w / 4.  Thread t holds rows base + t / 4 + 8 i, i = 0..3, at the
+    // positions 8 rep + 2 (t % 4) + {0, 1}, rep = 0, 1: element 4 i + 2 rep + {0, 1}.
+    if constexpr (!TMA) setmaxnreg_inc<128>();
+    const int q4 = warp & 3, hc = warp >> 2, st = threadIdx.x, tq = lane & 3;
+    const int kh = q4 >> 1, rb = (q4 & 1) * 32, part = 2 * kh + hc, row0 = rb + (lane >> 2);
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    float* s_alpha = reinterpret_cast<float*>(smem + C::kOffAlpha);
+    float* s_fac = reinterpret_cast<float*>(smem + C::kOffFac);
+    float* s_part = reinterpret_cast<float*>(smem + C::kOffPart);
+    volatile int* s_cmd = reinterpret_cast<volatile int*>(smem + C::kOffCmd);
+    const float sc = p.qk_scale_log2;
+    const int H = p.g.H, window = p.g.window, nfirst = p.g.first;
+    const uint32_t s_empty[2] = {bar0(kSEmpty0), bar0(kSEmpty0 + 1)};
+    const uint32_t p_ready[2] = {bar0(kPReady0), bar0(kPReady0 + 1)};
+    const uint32_t my_flag = map_cta(sbase + C::kOffFlag, 0) + 4 * rank;
+    int g = 0, wholes = 0;
+    // What was decided on tile x: scales O^T or clears bad values if it has to be
+    // (the PV MMAs of tile x wait for that).  Uniform over both CTAs' softmax warps.
+    auto decided = [&](int x) {
+      const int s = x & 1;
+      pair_wait(bar(kDecided0 + s), (x >> 1) & 1, wc);
+      const int cmd = *abort_flag ? 0 : s_cmd[s];
+      if (cmd == 0) return;
+      if (cmd & (kRaise0 | kRaise1)) {
+        // O^T is quiescent once the PV MMAs of tile x - 1 are done
+        if (x > 0) pipe_wait(bar(kVFree0 + (x - 1) % KS), ((x - 1) / KS) & 1, wc);
+        tc_fence_after();
+        const int c0 = cmd & kRaise0 ? 0 : 64, c1 = cmd & kRaise1 ? 128 : 64;
+#pragma unroll 1
+        for (int b = 0; b < C::kBlocks; ++b) {
+#pragma unroll 1
+          for (int col = c0 + 16 * hc; col < c1; col += 32) {
+            uint32_t ov[16];
+            const uint32_t ta = tmem + lane_base + C::kOCol + b * 128 + col;
+            tmem_ld16(ta, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              ov[e] = __float_as_uint(__uint_as_float(ov[e]) * s_alpha[s * 128 + col + e]);
+            tmem_st16(ta, ov);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      if (cmd & kPoison) {
+        // Values with an infinity or NaN, which some row does not see: its weight
+        // there is 0, but 0 x inf = NaN in the MMA.  They are cleared; the rows that
+        // do see them have a NaN weight already.
+        const int r = st >> 2, part4 = st & 3;  // 4 threads per row
+        auto chunk = [&](int ch) {
+          return reinterpret_cast<uint4*>(smem + C::kOffV + (x % KS) * C::kVBytes + (r >> 3) * C::kGroup +
+                                          (ch >> 3) * 1024 + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+        };
+        uint32_t bad = 0;
+        for (int ch = part4; ch < D / 16; ch += 4) {
+          const uint4 w = *chunk(ch);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            bad |= (ws[e] & 0x7f80u) == 0x7f80u || (ws[e] & 0x7f800000u) == 0x7f800000u;
+        }
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+        for (int ch = part4; bad && ch < D / 16; ch += 4) *chunk(ch) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) arrive_cluster(bar0(kScaled));
+    };
+
+    for (int u = u0; g < nt; ++u) {
+      const ChunkUnit un = load_unit(p.units + u);
+      const int i0 = g == 0 ? t0 - un.cum : 0;
+      const int i1 = min(un.ntiles, i0 + nt - g);
+      const bool whole = i0 == 0 && i1 == un.ntiles;
+      const int h0 = un.h0 + rank * kR, nrows = max(0, min(kR, un.nrows - rank * kR));
+      const int p_lo = un.pos0 + h0 / H, p_hi = un.pos0 + (h0 + max(nrows, 1) - 1) / H;
+      float m[4], l[4], scr[4];  // l: this thread's share
+      int pos[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        // (rows past the unit's end have factor 0: their weights, never used, stay
+        // finite and raise nothing)
+        scr[i] = row0 + 8 * i < nrows ? sc : 0.f;
+        pos[i] = un.pos0 + (h0 + row0 + 8 * i) / H;
+      }
+      for (int i = i0; i < i1; ++i, ++g) {
+        const int s = g & 1;
+        const int j0 = chunk_tile_start(i, un.nf, un.lo, kTile);
+        // whether every row of this CTA sees the whole tile
+        const bool full = j0 + kTile - 1 <= p_lo &&
+                          (window == 0 || j0 > p_hi - window || j0 + kTile <= nfirst);
+        pipe_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
+        tc_fence_after();
+        float x[16];
+        {
+          uint32_t va[8], vb[8];
+          const uint32_t ta = tmem + lane_base + s * 32 + 16 * hc;
+          tmem_ld_16x256b_x2(ta, va);
+          tmem_ld_16x256b_x2(ta + (16u << 16), vb);
+          tmem_wait_ld();
+          // register 4 rep + k: row + 8 (k / 2), position 8 rep + 2 (t % 4) + k % 2
+#pragma unroll
+          for (int rep = 0; rep < 2; ++rep) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[4 * (k >> 1) + 2 * rep + (k & 1)] = __uint_as_float(va[4 * rep + k]);
+              x[8 + 4 * (k >> 1) + 2 * rep + (k & 1)] = __uint_as_float(vb[4 * rep + k]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(s_empty[s]);
+        // tile g - 1 (a piece's last tile is looked at before its epilogue)
+        if (i > i0) decided(g - 1);
+        uint32_t see = 0xffffu;
+        int flags = 0;
+        if (!full) {
+          see = 0;
+          bool poison = false;  // a score that is masked and not finite
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = j0 + 32 * kh + 16 * hc + 8 * ((e >> 1) & 1) + 2 * tq + (e & 1);
+            const bool ok = j <= pos[e >> 2] && (window == 0 || j > pos[e >> 2] - window || j < nfirst);
+            see |= ok ? 1u << e : 0u;
+            poison |= !ok && !(fabsf(x[e]) < INFINITY);
+          }
+          if (named_bar_or(1, kSmThreads, poison)) flags = 2;
+        }
+        // P buffer s is free once the PV MMAs of tile g - 2 are done
+        if (g >= 2) pipe_wait(bar(kVFree0 + (g - 2) % KS), ((g - 2) / KS) & 1, wc);
+        // p = 2^(x scale - m) in bf16 into P (K-major, 128-byte swizzle).  The MMA
+        // multiplies the rounded p, the denominator sums the unrounded ones: each
+        // weight is off by at most 2^-8 of itself, as the output's own rounding.
+        const uint32_t pbuf = sP + s * C::kPBytes;
+        float sum[4];
+        auto weights = [&](auto masked) {
+          float top = -INFINITY;
+          uint32_t pk[4][2];
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            float e[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float arg = fmaf(x[4 * i4 + k], scr[i4], -m[i4]);
+              const bool ok = !decltype(masked)::value || ((see >> (4 * i4 + k)) & 1u);
+              top = fmaxf(top, ok ? arg : -INFINITY);
+              e[k] = ok ? ex2_approx(arg) : 0.f;
+            }
+            sum[i4] = (e[0] + e[1]) + (e[2] + e[3]);
+            const __nv_bfloat162 a = __floats2bfloat162_rn(e[0], e[1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(e[2], e[3]);
+            pk[i4][0] = *reinterpret_cast<const uint32_t*>(&a);
+            pk[i4][1] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          // matrices of a stmatrix.x4: rows + 8 (mi % 2), chunk + mi / 2
+          const int mi = lane >> 3, r8 = lane & 7;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int r = rb + 16 * half + 8 * (mi & 1) + r8, ch = 4 * kh + 2 * hc + (mi >> 1);
+            stmatrix_x4(pbuf + (r >> 3) * 1024 + r8 * 128 + ((ch ^ r8) << 4), pk[2 * half][0],
+                        pk[2 * half + 1][0], pk[2 * half][1], pk[2 * half + 1][1]);
+          }
+          return top > kHeadroom;
+        };
+        // The first tile of a piece sets m to its exact row maxima; a later one is
+        // weighted against the current m, and only if a score exceeds it by the
+        // headroom is m raised (p stays below 2^8).
+        bool exact = i == i0;
+        if (!exact) {
+          const bool over = full ? weights(std::false_type{}) : weights(std::true_type{});
+          fence_proxy_async_smem();
+          exact = named_bar_or(1, kSmThreads, over);
+        }
+        if (exact) {
+          float* hm = s_part + (g & 1) * 256;
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if ((see >> e) & 1u) top[e >> 2] = fmaxf(top[e >> 2], x[e] * scr[e >> 2]);
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            top[i4] = fmaxf(top[i4], __shfl_xor_sync(0xffffffffu, top[i4], 1));
+            top[i4] = fmaxf(top[i4], __shfl_xor_sync(0xffffffffu, top[i4], 2));
+            if (tq == 0) hm[part * 64 + row0 + 8 * i4] = top[i4];
+          }
+          named_bar_sync(1, kSmThreads);
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const int r = row0 + 8 * i4;
+            const float t = fmaxf(fmaxf(hm[r], hm[64 + r]), fmaxf(hm[128 + r], hm[192 + r]));
+            float alpha = 1.f;
+            if (t > m[i4] + kHeadroom || (m[i4] == -INFINITY && t > m[i4])) {
+              alpha = ex2_approx(m[i4] - t);  // 0 when m was -inf
+              l[i4] *= alpha;
+              m[i4] = t;
+            }
+            if (i > i0 && tq == 0 && part == 0) {  // both CTAs hold O^T of this row
+#pragma unroll
+              for (int cta = 0; cta < 2; ++cta)
+                store_cluster(map_cta(sbase + C::kOffAlpha + 4 * (s * 128 + rank * 64 + r), cta),
+                              __float_as_uint(alpha));
+            }
+          }
+          if (i > i0) {
+            flags |= 1;
+            fence_cluster();
+          }
+          weights(std::true_type{});
+          fence_proxy_async_smem();
+          named_bar_sync(1, kSmThreads);
+        }
+#pragma unroll
+        for (int i4 = 0; i4 < 4; ++i4) l[i4] += sum[i4];
+        if (st == 0) {
+          store_cluster(my_flag + 8 * s, (uint32_t)flags);
+          arrive_cluster(p_ready[s]);
+        }
+      }
+      // ---------------------------------------------- end of the piece
+      decided(g - 1);
+      // (the last tile's barriers lie behind every read of the maxima)
+      float* s_l = s_part;            // [4 parts][64]
+      float* s_m = s_part + 256;      // [64]
+      named_bar_sync(1, kSmThreads);
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) {
+        float t = l[i4];
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        if (tq == 0) {
+          s_l[part * 64 + row0 + 8 * i4] = t;
+          if (part == 0) s_m[row0 + 8 * i4] = m[i4];
+        }
+      }
+      named_bar_sync(1, kSmThreads);
+      const int slot = 2 * worker + (i0 == 0 ? 1 : 0);
+      if (st < kR) {
+        const float mr = s_m[st], lr = (s_l[st] + s_l[64 + st]) + (s_l[128 + st] + s_l[192 + st]);
+        if (whole) {
+          float f = 0.f;
+          if (st < nrows) {
+            const float ms = __ldg(p.attn_sink + (h0 + st) % H) * kLog2e;
+            const float M = fmaxf(mr, ms);
+            float lse = M * kLn2;
+            if (M != -INFINITY && ms != INFINITY) {
+              const float a = mr == -INFINITY ? 0.f : ex2_approx(mr - M);
+              const float den = fmaf(lr, a, ex2_approx(ms - M));
+              f = a / den;
+              lse = (M + log2f(den)) * kLn2;
+            }
+            p.lse[un.row0 + rank * kR + st] = lse;
+          }
+#pragma unroll
+          for (int cta = 0; cta < 2; ++cta)
+            store_cluster(map_cta(sbase + C::kOffFac + 4 * (rank * kR + st), cta), __float_as_uint(f));
+          fence_cluster();
+        } else {
+          p.part_ml[(size_t)slot * 2 * kR + rank * kR + st] = make_float2(mr, lr);
+        }
+      }
+      if (whole) {  // the factors of all 128 rows, from both CTAs
+        named_bar_sync(1, kSmThreads);
+        if (st < 2) arrive_cluster(map_cta(bar(kFac), st));
+        pair_wait(bar(kFac), wholes & 1, wc);
+        ++wholes;
+      }
+      pipe_wait(bar(kVFree0 + (g - 1) % KS), ((g - 1) / KS) & 1, wc);  // O^T is complete
+      tc_fence_after();
+      __syncwarp();
+      if (whole) {
+        // 64 rows of a block of O^T at a time through the P buffers: scaled, packed to
+        // bf16 and transposed with stmatrix into two boxes of 64 rows x 64 columns,
+        // then row by row to out.  Warp w takes 32 columns of D (q4) and 32 rows (hc).
+        uint8_t* stg = smem + C::kOffP;
+        const int r0 = hc * 32;
+#pragma unroll 1
+        for (int x = 0; x < 2 * C::kBlocks; ++x) {
+          const int b = x >> 1, rh = (x & 1) * 64;  // block of D, half of the rows
+          uint32_t rr[2][16];
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            tmem_ld_16x256b_x4(tmem + ((uint32_t)(q4 * 32 + 16 * half) << 16) + C::kOCol + b * 128 + rh + r0,
+                               rr[half]);
+          tmem_wait_ld();
+          float fac[8];
+#pragma unroll
+          for (int rep = 0; rep < 4; ++rep) {
+            fac[2 * rep] = s_fac[rh + r0 + 8 * rep + 2 * tq];
+            fac[2 * rep + 1] = s_fac[rh + r0 + 8 * rep + 2 * tq + 1];
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int rep = 0; rep < 4; ++rep) {
+#pragma unroll
+              for (int dg = 0; dg < 2; ++dg) {
+                // "+ 0.f" turns -0 into +0 when the factor is 0 (sink = +inf)
+                const __nv_bfloat162 v2 = __floats2bfloat162_rn(
+                    __uint_as_float(rr[half][4 * rep + 2 * dg]) * fac[2 * rep] + 0.f,
+                    __uint_as_float(rr[half][4 * rep + 2 * dg + 1]) * fac[2 * rep + 1] + 0.f);
+                pk[2 * rep + dg] = *reinterpret_cast<const uint32_t*>(&v2);
+              }
+            }
+            const int mt = lane >> 3, jr = lane & 7;
+            const int dl = q4 * 32 + 16 * half + 8 * (mt & 1);
+            const int box = dl >> 6, chunk = (dl & 63) >> 3;
+#pragma unroll
+            for (int rep0 = 0; rep0 < 4; rep0 += 2) {
+              const int r = r0 + 8 * (rep0 + (mt >> 1)) + jr;
+              stmatrix_x4_trans(smem_addr(stg) + box * (kR * 128) + r * 128 + ((chunk ^ (r & 7)) << 4),
+                                pk[2 * rep0], pk[2 * rep0 + 1], pk[2 * rep0 + 2], pk[2 * rep0 + 3]);
+            }
+          }
+          named_bar_sync(1, kSmThreads);
+          const int n = min(64, un.nrows - rh);
+          for (int e = st; e < n * 16; e += kSmThreads) {
+            const int r = e >> 4, ch = e & 15;
+            const uint4 w = *reinterpret_cast<const uint4*>(stg + (ch >> 3) * (kR * 128) + r * 128 +
+                                                            (((ch & 7) ^ (r & 7)) << 4));
+            *reinterpret_cast<uint4*>(p.out + (size_t)(un.row0 + rh + r) * D + rank * (D / 2) + b * 128 +
+                                      ch * 8) = w;
+          }
+          named_bar_sync(1, kSmThreads);  // the area may be rewritten
+        }
+      } else {
+#pragma unroll 1
+        for (int b = 0; b < C::kBlocks; ++b) {
+          const int d = rank * (D / 2) + b * 128 + q4 * 32 + lane;
+#pragma unroll 1
+          for (int col = 16 * hc; col < 128; col += 32) {
+            uint32_t ov[16];
+            tmem_ld16(tmem + lane_base + C::kOCol + b * 128 + col, ov);
+            tmem_wait_ld();
+            float* o = p.part_o + ((size_t)slot * 2 * kR + col) * D + d;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[(size_t)e * D] = __uint_as_float(ov[e]);
+          }
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(1, kSmThreads);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the other may still reach its memory
+  tc_fence_after();
+  if (warp == kQkWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+template <typename F>
+cudaError_t for_shape(int D, bool tma, F&& f) {
+#define SDA_CASE(DV)                                                                        \
+  if (D == DV)                                                                              \
+    return tma ? f(chunk_pair_kernel<DV, true>, (size_t)Cfg<DV>::kSmem, dim3(384))          \
+               : f(chunk_pair_kernel<DV, false>, (size_t)Cfg<DV>::kSmem, dim3(kGatherThreads));
+  SDA_CASE(256) SDA_CASE(512)
+#undef SDA_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t pair_prepare() {
+  for (int D : {256, 512}) {
+    for (bool tma : {false, true}) {
+      const cudaError_t e = for_shape(D, tma, [&](auto kernel, size_t smem, dim3) {
+        cudaError_t r =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncAttributes a;
+        if (r == cudaSuccess) r = cudaFuncGetAttributes(&a, kernel);
+        if (r == cudaSuccess && !tma && a.numRegs < kGatherRegs) r = cudaErrorInvalidConfiguration;
+        return r;
+      });
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_chunk_pair(const CUtensorMap& tq, const CUtensorMap& tkv, const ChunkParams& p,
+                              bool tma, const ChunkLayout& L, cudaStream_t st) {
+  return for_shape(p.g.D, tma, [&](auto kernel, size_t smem, dim3 threads) {
+    return launch_pdl_cluster(kernel, dim3(2 * L.grid), threads, 2, smem, st, tq, tkv, p);
+  });
+}
+
+}  // namespace sda

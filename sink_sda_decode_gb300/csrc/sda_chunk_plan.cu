@@ -121,11 +121,20 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
 }
 
 // Merge of the pieces of cut units.  Block (x = k - 1, y): boundary k of the
-// tile ranges; it acts if boundary k is the first to cut its unit, and its
-// warps take that unit's rows y * kWarps + warp.  Piece 0 lies in slot
-// 2 (k - 1) + 1 (the unit starts in CTA k - 1's range), piece i in slot
-// 2 (k - 1 + i).
+// tile ranges; it acts if boundary k is the first to cut its unit.  A warp takes
+// 128 columns (all of D below that) of one row; its lanes hold the pieces' (m, l)
+// and weights, 32 at a time, and eight pieces' partials are in flight together:
+// a unit cut into 19 pieces (8 sequences of 65536 positions) is bound by the
+// latency of those loads.  Piece 0 lies in slot 2 (k - 1) + 1 (the unit starts in
+// CTA k - 1's range), piece i in slot 2 (k - 1 + i).
 constexpr int kCombineWarps = 8;
+
+template <int D>
+struct CombineCfg {
+  static constexpr int kWarpsRow = D < 128 ? 1 : D / 128;  // warps of a row
+  static constexpr int kRows = kCombineWarps / kWarpsRow;  // rows of a block
+  static constexpr int kPer = D < 128 ? 2 : 4;             // columns of a lane
+};
 
 template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
@@ -133,84 +142,95 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
     float* __restrict__ lse, const ChunkHeader* __restrict__ hdr,
     const ChunkUnit* __restrict__ units, const int* __restrict__ cta_unit,
     const float2* __restrict__ part_ml, const float* __restrict__ part_o) {
+  using C = CombineCfg<D>;
   pdl_wait();
   pdl_trigger();
   const int k = blockIdx.x + 1;
-  if (k >= hdr->ctas) return;
-  const int per = hdr->per;
   const int u = cta_unit[k];
-  const int cum = units[u].cum;
+  const int ctas = hdr->ctas, per = hdr->per, n_units = hdr->n_units;
+  if (k >= ctas || u >= n_units) return;
+  const ChunkUnit un = units[u];
   const long long t0 = (long long)k * per;
-  if (cum >= t0 || cum < t0 - per) return;  // not cut here, or cut by an earlier boundary already
-  const int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= units[u].nrows) return;
-  const long long end = (long long)cum + units[u].ntiles;
-  const int np = 1 + (int)((end - t0 + per - 1) / per);
-  auto slot = [&](int i) { return i == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + i); };
-  const int h = (units[u].h0 + row) % H;
-  const float ms = attn_sink[h] * kLog2e;
-  float mk = -INFINITY;
-  for (int i = lane; i < np; i += 32) mk = fmaxf(mk, part_ml[(size_t)slot(i) * R + row].x);
+  if (un.cum >= t0 || un.cum < t0 - per) return;  // not cut here, or cut by an earlier boundary already
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * C::kRows + warp / C::kWarpsRow;
+  const int col = (warp % C::kWarpsRow) * 128 + lane * C::kPer;
+  if (row >= un.nrows) return;
+  const int np = 1 + (int)(((long long)un.cum + un.ntiles - t0 + per - 1) / per);
+  auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + i)); };
+  auto ml_of = [&](int i) {
+    return i < np ? part_ml[slot(i) * R + row] : make_float2(-INFINITY, 0.f);
+  };
+  const float ms = attn_sink[(un.h0 + row) % H] * kLog2e;
+  const float2 ml0 = ml_of(lane);  // of the first 32 pieces
+  float mk = ml0.x;
+  for (int i = lane + 32; i < np; i += 32) mk = fmaxf(mk, ml_of(i).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
   const float M = fmaxf(ms, mk);
   const bool dead = ms == INFINITY || M == -INFINITY;
   float den = 0.f;
-  for (int i = lane; i < np; i += 32) {
-    const float2 ml = part_ml[(size_t)slot(i) * R + row];
-    // (a piece whose rows are all masked has m = -inf, l = 0)
-    den += dead || ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - M);
+  float acc[C::kPer] = {};
+  for (int i0 = 0; i0 < np && !dead; i0 += 32) {
+    const float2 ml = i0 == 0 ? ml0 : ml_of(i0 + lane);
+    // (a piece whose rows are all masked has m = -inf, l = 0 and weight 0)
+    const float w = i0 + lane < np ? ex2_approx(ml.x - M) : 0.f;
+    den += ml.x == -INFINITY ? ml.y : ml.y * w;
+    const int n = min(32, np - i0);
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      float v[8][C::kPer];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float* o = part_o + (slot(i0 + min(j0 + j, n - 1)) * R + row) * D + col;
+        if constexpr (C::kPer == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o);
+          v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(o);
+          v[j][0] = x.x, v[j][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+        if (j0 + j < n) {
+#pragma unroll
+          for (int x = 0; x < C::kPer; ++x) acc[x] += wj * v[j][x];
+        }
+      }
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
   if (!dead) den += ex2_approx(ms - M);
-  constexpr int kPer = D / 32 < 4 ? 2 : 4;     // consecutive values per lane and group
-  constexpr int kGroups = D / (32 * kPer);
-  float acc[kGroups][kPer] = {};
-  for (int i = 0; i < np && !dead; ++i) {
-    const float m = part_ml[(size_t)slot(i) * R + row].x;
-    const float w = ex2_approx(m - M);
-    const float* o = part_o + ((size_t)slot(i) * R + row) * D + lane * kPer;
-#pragma unroll
-    for (int e = 0; e < kGroups; ++e) {
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) acc[e][x] += w * o[e * 32 * kPer + x];
-    }
-  }
   const float inv = dead ? 0.f : 1.f / den;
-  const size_t orow = (size_t)units[u].row0 + row;
+  const size_t orow = (size_t)un.row0 + row;
 #pragma unroll
-  for (int e = 0; e < kGroups; ++e) {
-#pragma unroll
-    for (int x = 0; x < kPer; x += 2) {
-      // "+ 0.f" turns -0 into +0 (a factor of 0 when the sink is +inf)
-      const __nv_bfloat162 v =
-          __floats2bfloat162_rn(acc[e][x] * inv + 0.f, acc[e][x + 1] * inv + 0.f);
-      *reinterpret_cast<__nv_bfloat162*>(out + orow * D + e * 32 * kPer + lane * kPer + x) = v;
-    }
+  for (int x = 0; x < C::kPer; x += 2) {
+    // "+ 0.f" turns -0 into +0 (a factor of 0 when the sink is +inf)
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[x] * inv + 0.f, acc[x + 1] * inv + 0.f);
+    *reinterpret_cast<__nv_bfloat162*>(out + orow * D + col + x) = v;
   }
-  if (lane == 0) lse[orow] = dead ? M * kLn2 : (M + log2f(den)) * kLn2;
+  if (col == 0) lse[orow] = dead ? M * kLn2 : (M + log2f(den)) * kLn2;
 }
 
 }  // namespace
 
-ChunkLayout chunk_layout(int B, int T, int H, int D, bool boxes, int num_sms) {
+ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms) {
   ChunkLayout L;
   const int64_t rows = (int64_t)T * H;
   // 16-row units where a sequence has at most 16 rows on average (a step of
   // few heads): q then takes a quarter of the shared memory and three KV stages
   // of 64 positions fit, and the rows' masks and stores are not padded to 64.
   L.R = rows <= (int64_t)16 * B ? 16 : 64;
-  L.tile = chunk_tile(L.R, D);
   L.grid = num_sms < kMaxPlanGrid ? num_sms : kMaxPlanGrid;
-  // With more than 128 rows a sequence on average two CTAs take 64 each of a
-  // unit of 128 and load every KV tile once for both.
-  L.pair = boxes && rows > (int64_t)128 * B;
+  // With more than 128 rows a sequence on average, pairs of CTAs take units of 128 rows.
+  L.pair = D >= 256 && rows > (int64_t)128 * B;
   if (L.pair) {
     L.R = 128;
     L.grid /= 2;
   }
+  L.tile = chunk_tile(L.R, D);
   L.u_max = (int)((rows + L.R - 1) / L.R + B);
   size_t off = sizeof(ChunkHeader);
   L.units_off = off;
@@ -240,8 +260,8 @@ cudaError_t launch_chunk_combine(const float* attn_sink, const ChunkGeom& g, voi
                                  const ChunkLayout& L, void* ws, cudaStream_t st) {
   char* base = static_cast<char*>(ws);
   if (L.grid < 2) return cudaSuccess;
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(L.grid - 1, L.R / kCombineWarps), dim3(kCombineWarps * 32), 0,
+  auto go = [&](auto kernel, int rows) {
+    return launch_pdl(kernel, dim3(L.grid - 1, L.R / rows), dim3(kCombineWarps * 32), 0,
                       st, attn_sink, g.H, L.R, static_cast<__nv_bfloat16*>(out), lse,
                       reinterpret_cast<const ChunkHeader*>(base),
                       reinterpret_cast<const ChunkUnit*>(base + L.units_off),
@@ -250,10 +270,10 @@ cudaError_t launch_chunk_combine(const float* attn_sink, const ChunkGeom& g, voi
                       reinterpret_cast<const float*>(base + L.o_off));
   };
   switch (g.D) {
-    case 64: return go(chunk_combine_kernel<64>);
-    case 128: return go(chunk_combine_kernel<128>);
-    case 256: return go(chunk_combine_kernel<256>);
-    case 512: return go(chunk_combine_kernel<512>);
+    case 64: return go(chunk_combine_kernel<64>, CombineCfg<64>::kRows);
+    case 128: return go(chunk_combine_kernel<128>, CombineCfg<128>::kRows);
+    case 256: return go(chunk_combine_kernel<256>, CombineCfg<256>::kRows);
+    case 512: return go(chunk_combine_kernel<512>, CombineCfg<512>::kRows);
     default: return cudaErrorInvalidValue;
   }
 }

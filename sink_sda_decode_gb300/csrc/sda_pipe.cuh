@@ -73,25 +73,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
-// The same, into every CTA of the cluster whose bit is set in `mask`, at the
-// same offsets: data and completion.
-__device__ __forceinline__ void tma_load_4d_multicast(uint32_t dst, const void* tmap, int x, int y,
-                                                      int z, int w, uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "h"(mask)
-      : "memory");
-}
-// Arrive on `bar` of every CTA of the cluster in `mask` once every previously
-// issued tcgen05.mma of this thread is done.
-__device__ __forceinline__ void mma_commit_multicast(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
-      "h"(mask)
-      : "memory");
-}
 // Arrive on `bar` once this thread's earlier cp.async have landed (counted in
 // the barrier's arrivals).
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
