@@ -187,8 +187,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
-        ok = __all_sync(0xffffffffu, ok);
+        if (g >= KS) ok = warp_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(kv_full(s, h), C::kHalf);
         __syncwarp();
@@ -240,8 +239,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const uint32_t stage = sKV + s * C::kStage;
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        if (g >= KS) ok = pipe_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
-        ok = __all_sync(0xffffffffu, ok);
+        if (g >= KS) ok = warp_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
         if (!ok) break;
         const int ch = h * kCh + lane % kCh;  // 16-byte chunk of the row
 #pragma unroll
@@ -285,14 +283,13 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const uint64_t a0 = sdesc_sw128(sQ, 16, 1024);
     for (int g = 0; g < nt; ++g) {
       const int s = g & 1, ks = g % KS;
-      if (g >= 2) ok = pipe_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
-      if (ok && c.first) ok = pipe_wait(bar(kQFull), pieces & 1, wc);
+      if (g >= 2) ok = warp_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
+      if (ok && c.first) ok = warp_wait(bar(kQFull), pieces & 1, wc);
       const uint64_t b0 = sdesc_sw128(sKV + ks * C::kStage, 16, C::kGroup);
       const bool last = c.last();
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        if (ok) ok = pipe_wait(kv_full(ks, h), (g / KS) & 1, wc);
-        ok = __all_sync(0xffffffffu, ok);
+        if (ok) ok = warp_wait(kv_full(ks, h), (g / KS) & 1, wc);
         if (!ok) break;
         if (!TMA) fence_proxy_async_smem();  // the copies were made through the generic proxy
         tc_fence_after();
@@ -316,7 +313,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       c.next();
       if (last) {
         if (c.left > 0) {  // q of the next unit, once this unit's MMAs have read q
-          ok = __all_sync(0xffffffffu, pipe_wait(bar(kQEmpty), pieces & 1, wc));
+          ok = warp_wait(bar(kQEmpty), pieces & 1, wc);
           if (!ok) break;
           load_q();
         }
@@ -335,7 +332,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     c.init(p.units, u0, t0, nt);
     for (int g = 0; g < nt; ++g) {
       const int s = g & 1, ks = g % KS;
-      if (!__all_sync(0xffffffffu, pipe_wait(bar(kPReady0 + s), (g >> 1) & 1, wc))) break;
+      if (!warp_wait(bar(kPReady0 + s), (g >> 1) & 1, wc)) break;
       if (!TMA) fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t a0 = sdesc_sw128(sKV + ks * C::kStage, 1024, C::kGroup);
@@ -401,8 +398,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const bool full = j0 + kTile - 1 <= p_lo &&
                           (window == 0 || j0 > p_hi - window || j0 + kTile <= nfirst);
         // P buffer s is free once the PV of tile g - 2 is done (long before the scores are)
-        if (g >= 2) pipe_wait(pv_done((g - 2) % KS, HV - 1), ((g - 2) / KS) & 1, wc);
-        pipe_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
+        if (g >= 2) warp_wait(pv_done((g - 2) % KS, HV - 1), ((g - 2) / KS) & 1, wc);
+        warp_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
         tc_fence_after();
         float x[kE];
         {
@@ -564,7 +561,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             named_bar_sync(1, kSmThreads);
             // O^T must be quiescent: wait for the PV of tile g - 1
-            if (lane == 0) pipe_wait(pv_done((g - 1) % KS, HV - 1), ((g - 1) / KS) & 1, wc);
+            warp_wait(pv_done((g - 1) % KS, HV - 1), ((g - 1) / KS) & 1, wc);
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -601,7 +598,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         s_lsum[hc * 64 + hA] = lA;
         s_lsum[hc * 64 + hB] = lB;
       }
-      if (lane == 0) pipe_wait(pv_done((g - 1) % KS, HV - 1), ((g - 1) / KS) & 1, wc);
+      warp_wait(pv_done((g - 1) % KS, HV - 1), ((g - 1) / KS) & 1, wc);
       __syncwarp();
       tc_fence_after();
       named_bar_sync(1, kSmThreads);

@@ -123,8 +123,12 @@ __device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t cta) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
   return r;
 }
+// (A release at cluster scope costs its thread about 1000 cycles.  What goes to the
+// other CTA on every tile is an arrival alone, after reads of TMEM or after stores to
+// the CTA's own shared memory that the MMAs read; stores to the other CTA are rare
+// and have a fence_cluster() of their own.)
 __device__ __forceinline__ void arrive_cluster(uint32_t mapped) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
 }
 __device__ __forceinline__ void store_cluster(uint32_t mapped, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapped), "r"(v) : "memory");
@@ -157,6 +161,9 @@ __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const P
       }
     }
   }
+}
+__device__ __forceinline__ bool pair_warp_wait(uint32_t bar, uint32_t parity, const PipeWait& w) {
+  return __all_sync(0xffffffffu, pair_wait(bar, parity, w));
 }
 // Tiled loads into this CTA that complete on a barrier of the pair's CTA 0.
 __device__ __forceinline__ void tma_pair_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w,
@@ -214,6 +221,8 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       mbar_init(bar(kVLanded0 + s), kLoadWarps * 32);
     }
     *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) reinterpret_cast<int*>(smem + C::kOffFlag)[i] = 0;
+    for (int i = 0; i < 2; ++i) reinterpret_cast<int*>(smem + C::kOffCmd)[i] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmap_q);
     if (TMA) tma_prefetch_desc(&tmap_kv);
@@ -270,8 +279,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
           y_next = box_of(c);
           c.next();
         }
-        if (g >= KS) ok = pipe_wait(bar(free0 + s), ((g / KS) - 1) & 1, wc);
-        ok = __all_sync(0xffffffffu, ok);
+        if (g >= KS) ok = warp_wait(bar(free0 + s), ((g / KS) - 1) & 1, wc);
         if (!ok) break;
         // (CTA 1's bytes may land before CTA 0 has said how many to expect: the
         // barrier's phase cannot end before that arrival)
@@ -285,8 +293,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // ===================================================== passing on landed stages
       for (; g < nt; ++g) {
         const int s = g % KS;
-        ok = pipe_wait(bar((keys ? kKLanded0 : kVLanded0) + s), (g / KS) & 1, wc);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(bar((keys ? kKLanded0 : kVLanded0) + s), (g / KS) & 1, wc);
         if (!ok) break;
         fence_proxy_async_smem();  // the copies were made through the generic proxy
         if (lane == 0) arrive_cluster(bar0(full0 + s));
@@ -329,8 +336,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         sl2 = slot_of(c);
         c.next();
       }
-      if (g >= KS) ok = pipe_wait(bar(free0 + s), ((g / KS) - 1) & 1, wc);
-      ok = __all_sync(0xffffffffu, ok);
+      if (g >= KS) ok = warp_wait(bar(free0 + s), ((g / KS) - 1) & 1, wc);
       if (!ok) break;
       auto copy = [&](uint32_t dst, int slot, int ch) {
         const uint4* src = slot >= 0 ? kv4 + (size_t)slot * (D / 8) + ch : kv4;
@@ -391,10 +397,9 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int s = g & 1, ks = g % KS;
       const bool last = c.last();
       if (rank == 0) {
-        if (g >= 2) ok = pair_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
-        if (ok && c.first) ok = pipe_wait(bar(kQFull), pieces & 1, wc);
-        if (ok) ok = pair_wait(bar(kKFull0 + ks), (g / KS) & 1, wc);
-        ok = __all_sync(0xffffffffu, ok);
+        if (g >= 2) ok = pair_warp_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
+        if (ok && c.first) ok = warp_wait(bar(kQFull), pieces & 1, wc);
+        if (ok) ok = pair_warp_wait(bar(kKFull0 + ks), (g / KS) & 1, wc);
         if (!ok) break;
         if (!TMA) fence_proxy_async_smem();
         tc_fence_after();
@@ -416,7 +421,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       c.next();
       if (last) {  // q of the next unit, once this unit's MMAs have read q
-        ok = __all_sync(0xffffffffu, pipe_wait(bar(kQEmpty), pieces & 1, wc));
+        ok = warp_wait(bar(kQEmpty), pieces & 1, wc);
         loaded = false;
         if (!ok) break;
         if (c.left > 0) {
@@ -434,26 +439,29 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       Cursor c;
       c.init(p.units, u0, t0, nt);
       volatile int* flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag);
-      int scaled = 0;
+      int scaled = 0, said[2] = {0, 0};
       for (int g = 0; g < nt; ++g) {
         const int s = g & 1, ks = g % KS;
-        bool ok = pair_wait(bar(kPReady0 + s), (g >> 1) & 1, wc);
+        bool ok = pair_warp_wait(bar(kPReady0 + s), (g >> 1) & 1, wc);
         const int f0 = flag[2 * s], f1 = flag[2 * s + 1];
         const int cmd = (f0 & 1 ? kRaise0 : 0) | (f1 & 1 ? kRaise1 : 0) | ((f0 | f1) & 2 ? kPoison : 0);
-        if (cmd && ok) ok = pair_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);  // values to be looked at
-        ok = __all_sync(0xffffffffu, ok);
+        if (cmd && ok) ok = pair_warp_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);  // values to be looked at
         if (!ok) break;
         if (lane < 2) {  // one lane tells each CTA
-          store_cluster(map_cta(sbase + C::kOffCmd + 4 * s, lane), (uint32_t)cmd);
+          if (cmd != said[s]) {
+            store_cluster(map_cta(sbase + C::kOffCmd + 4 * s, lane), (uint32_t)cmd);
+            fence_cluster();
+          }
           arrive_cluster(map_cta(bar(kDecided0 + s), lane));
         }
+        said[s] = cmd;
         __syncwarp();
         if (cmd) {
-          ok = pair_wait(bar(kScaled), scaled & 1, wc);
+          if (lane < 2) flag[2 * s + lane] = 0;  // for tile g + 2, which says nothing unless it has to
+          ok = pair_warp_wait(bar(kScaled), scaled & 1, wc);
           ++scaled;
         }
-        if (ok) ok = pair_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);
-        ok = __all_sync(0xffffffffu, ok);
+        if (ok) ok = pair_warp_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);
         if (!ok) break;
         if (!TMA) fence_proxy_async_smem();
         tc_fence_after();
@@ -498,12 +506,12 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // (the PV MMAs of tile x wait for that).  Uniform over both CTAs' softmax warps.
     auto decided = [&](int x) {
       const int s = x & 1;
-      pair_wait(bar(kDecided0 + s), (x >> 1) & 1, wc);
+      pair_warp_wait(bar(kDecided0 + s), (x >> 1) & 1, wc);
       const int cmd = *abort_flag ? 0 : s_cmd[s];
       if (cmd == 0) return;
       if (cmd & (kRaise0 | kRaise1)) {
         // O^T is quiescent once the PV MMAs of tile x - 1 are done
-        if (x > 0) pipe_wait(bar(kVFree0 + (x - 1) % KS), ((x - 1) / KS) & 1, wc);
+        if (x > 0) warp_wait(bar(kVFree0 + (x - 1) % KS), ((x - 1) / KS) & 1, wc);
         tc_fence_after();
         const int c0 = cmd & kRaise0 ? 0 : 64, c1 = cmd & kRaise1 ? 128 : 64;
 #pragma unroll 1
@@ -573,7 +581,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // whether every row of this CTA sees the whole tile
         const bool full = j0 + kTile - 1 <= p_lo &&
                           (window == 0 || j0 > p_hi - window || j0 + kTile <= nfirst);
-        pipe_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
+        warp_wait(bar(kSFull0 + s), (g >> 1) & 1, wc);
         tc_fence_after();
         float x[16];
         {
@@ -612,7 +620,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (named_bar_or(1, kSmThreads, poison)) flags = 2;
         }
         // P buffer s is free once the PV MMAs of tile g - 2 are done
-        if (g >= 2) pipe_wait(bar(kVFree0 + (g - 2) % KS), ((g - 2) / KS) & 1, wc);
+        if (g >= 2) warp_wait(bar(kVFree0 + (g - 2) % KS), ((g - 2) / KS) & 1, wc);
         // p = 2^(x scale - m) in bf16 into P (K-major, 128-byte swizzle).  The MMA
         // multiplies the rounded p, the denominator sums the unrounded ones: each
         // weight is off by at most 2^-8 of itself, as the output's own rounding.
@@ -697,7 +705,10 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) l[i4] += sum[i4];
         if (st == 0) {
-          store_cluster(my_flag + 8 * s, (uint32_t)flags);
+          if (flags) {
+            store_cluster(my_flag + 8 * s, (uint32_t)flags);
+            fence_cluster();
+          }
           arrive_cluster(p_ready[s]);
         }
       }
@@ -746,10 +757,10 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (whole) {  // the factors of all 128 rows, from both CTAs
         named_bar_sync(1, kSmThreads);
         if (st < 2) arrive_cluster(map_cta(bar(kFac), st));
-        pair_wait(bar(kFac), wholes & 1, wc);
+        pair_warp_wait(bar(kFac), wholes & 1, wc);
         ++wholes;
       }
-      pipe_wait(bar(kVFree0 + (g - 1) % KS), ((g - 1) / KS) & 1, wc);  // O^T is complete
+      warp_wait(bar(kVFree0 + (g - 1) % KS), ((g - 1) / KS) & 1, wc);  // O^T is complete
       tc_fence_after();
       __syncwarp();
       if (whole) {
