@@ -26,8 +26,8 @@
 //
 // O^T of a row lies in both CTAs, so raising the row's running reference (rare) takes
 // both: with its weights of tile g ready, each CTA tells CTA 0 whether it raised one;
-// PV warp 0 passes the answers on to all softmax warps ("decided"), which look at it
-// before they go on with tile g + 1; if a reference was raised they scale O^T first,
+// the PV warp passes the answers on to all softmax warps ("decided"), which look at it
+// before they give tile g + 1 to the MMAs; if a reference was raised they scale O^T,
 // and the PV MMAs of tile g wait for that.
 #include <type_traits>
 
@@ -60,7 +60,7 @@ enum Bar : int {
   kPReady0 = kSEmpty0 + 2,  // CTA 0: weights of both
   kDecided0 = kPReady0 + 2, // both
   kScaled = kDecided0 + 2,  // CTA 0: the softmax warps of both
-  kFac,                     // both: the final factors of both CTAs' rows
+  kFac,                     // both: the final factors of the other CTA's rows
   kKFull0,                             // CTA 0
   kVFull0 = kKFull0 + kMaxStages,      // CTA 0
   kKFree0 = kVFull0 + kMaxStages,      // both
@@ -123,48 +123,23 @@ __device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t cta) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
   return r;
 }
-// (A release at cluster scope costs its thread about 1000 cycles.  What goes to the
-// other CTA on every tile is an arrival alone, after reads of TMEM or after stores to
-// the CTA's own shared memory that the MMAs read; stores to the other CTA are rare
-// and have a fence_cluster() of their own.)
+// (A release at cluster scope costs its thread about 1000 cycles, an acquire in a wait
+// about 400.  What goes to the other CTA on every tile is an arrival alone, after reads
+// of TMEM or after stores to the CTA's own shared memory that the MMAs read; stores to
+// the other CTA are rare and have a fence_cluster() of their own on both sides.)
 __device__ __forceinline__ void arrive_cluster(uint32_t mapped) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
 }
 __device__ __forceinline__ void store_cluster(uint32_t mapped, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapped), "r"(v) : "memory");
 }
+// Stores to the other CTA's shared memory, and counts the 4 bytes on its barrier.
+__device__ __forceinline__ void store_async(uint32_t mapped, uint32_t v, uint32_t mapped_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(mapped),
+               "r"(v), "r"(mapped_bar)
+               : "memory");
+}
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// pipe_wait for barriers that threads of the other CTA arrive on.
-__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const PipeWait& w) {
-  if (try_wait_cluster(bar, parity)) return true;
-  if (*w.abort_flag) return false;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if ((it & 63u) == 0) {
-      if (*w.abort_flag) return false;
-      if (globaltimer_ns() - t0 > w.timeout_ns) {
-        *w.abort_flag = 1;
-        atomicExch(w.error, 1);
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ bool pair_warp_wait(uint32_t bar, uint32_t parity, const PipeWait& w) {
-  return __all_sync(0xffffffffu, pair_wait(bar, parity, w));
-}
 // Tiled loads into this CTA that complete on a barrier of the pair's CTA 0.
 __device__ __forceinline__ void tma_pair_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w,
                                             uint32_t bar0) {
@@ -211,7 +186,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       mbar_init(bar(kDecided0 + s), 1);
     }
     mbar_init(bar(kScaled), 2 * kSmWarps);
-    mbar_init(bar(kFac), 2);
+    mbar_init(bar(kFac), 1);
     for (int s = 0; s < KS; ++s) {
       mbar_init(bar(kKFull0 + s), TMA ? 1 : 2);  // an expected count of bytes, or one CTA each
       mbar_init(bar(kVFull0 + s), TMA ? 1 : 2);
@@ -397,9 +372,9 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int s = g & 1, ks = g % KS;
       const bool last = c.last();
       if (rank == 0) {
-        if (g >= 2) ok = pair_warp_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
+        if (g >= 2) ok = warp_wait(bar(kSEmpty0 + s), ((g >> 1) - 1) & 1, wc);
         if (ok && c.first) ok = warp_wait(bar(kQFull), pieces & 1, wc);
-        if (ok) ok = pair_warp_wait(bar(kKFull0 + ks), (g / KS) & 1, wc);
+        if (ok) ok = warp_wait(bar(kKFull0 + ks), (g / KS) & 1, wc);
         if (!ok) break;
         if (!TMA) fence_proxy_async_smem();
         tc_fence_after();
@@ -442,10 +417,10 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       int scaled = 0, said[2] = {0, 0};
       for (int g = 0; g < nt; ++g) {
         const int s = g & 1, ks = g % KS;
-        bool ok = pair_warp_wait(bar(kPReady0 + s), (g >> 1) & 1, wc);
+        bool ok = warp_wait(bar(kPReady0 + s), (g >> 1) & 1, wc);
         const int f0 = flag[2 * s], f1 = flag[2 * s + 1];
         const int cmd = (f0 & 1 ? kRaise0 : 0) | (f1 & 1 ? kRaise1 : 0) | ((f0 | f1) & 2 ? kPoison : 0);
-        if (cmd && ok) ok = pair_warp_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);  // values to be looked at
+        if (cmd && ok) ok = warp_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);  // values to be looked at
         if (!ok) break;
         if (lane < 2) {  // one lane tells each CTA
           if (cmd != said[s]) {
@@ -457,11 +432,12 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         said[s] = cmd;
         __syncwarp();
         if (cmd) {
+          fence_cluster();
           if (lane < 2) flag[2 * s + lane] = 0;  // for tile g + 2, which says nothing unless it has to
-          ok = pair_warp_wait(bar(kScaled), scaled & 1, wc);
+          ok = warp_wait(bar(kScaled), scaled & 1, wc);
           ++scaled;
         }
-        if (ok) ok = pair_warp_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);
+        if (ok) ok = warp_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);
         if (!ok) break;
         if (!TMA) fence_proxy_async_smem();
         tc_fence_after();
@@ -506,9 +482,10 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // (the PV MMAs of tile x wait for that).  Uniform over both CTAs' softmax warps.
     auto decided = [&](int x) {
       const int s = x & 1;
-      pair_warp_wait(bar(kDecided0 + s), (x >> 1) & 1, wc);
+      warp_wait(bar(kDecided0 + s), (x >> 1) & 1, wc);
       const int cmd = *abort_flag ? 0 : s_cmd[s];
       if (cmd == 0) return;
+      fence_cluster();
       if (cmd & (kRaise0 | kRaise1)) {
         // O^T is quiescent once the PV MMAs of tile x - 1 are done
         if (x > 0) warp_wait(bar(kVFree0 + (x - 1) % KS), ((x - 1) / KS) & 1, wc);
@@ -603,8 +580,6 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(s_empty[s]);
-        // tile g - 1 (a piece's last tile is looked at before its epilogue)
-        if (i > i0) decided(g - 1);
         uint32_t see = 0xffffu;
         int flags = 0;
         if (!full) {
@@ -669,7 +644,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if ((see >> e) & 1u) top[e >> 2] = fmaxf(top[e >> 2], x[e] * scr[e >> 2]);
+            top[e >> 2] = fmaxf(top[e >> 2], (see >> e) & 1u ? x[e] * scr[e >> 2] : -INFINITY);
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
             top[i4] = fmaxf(top[i4], __shfl_xor_sync(0xffffffffu, top[i4], 1));
@@ -698,12 +673,17 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
             flags |= 1;
             fence_cluster();
           }
-          weights(std::true_type{});
+          if (full) weights(std::false_type{});
+          else weights(std::true_type{});
           fence_proxy_async_smem();
           named_bar_sync(1, kSmThreads);
         }
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) l[i4] += sum[i4];
+        // What was decided on tile g - 1 has long come in by now; its PV MMAs, if they
+        // wait for O^T to be scaled, come before tile g's.  (A piece's last tile is
+        // looked at before its epilogue.)
+        if (i > i0) decided(g - 1);
         if (st == 0) {
           if (flags) {
             store_cluster(my_flag + 8 * s, (uint32_t)flags);
@@ -746,44 +726,45 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             p.lse[un.row0 + rank * kR + st] = lse;
           }
-#pragma unroll
-          for (int cta = 0; cta < 2; ++cta)
-            store_cluster(map_cta(sbase + C::kOffFac + 4 * (rank * kR + st), cta), __float_as_uint(f));
-          fence_cluster();
+          s_fac[rank * kR + st] = f;
+          store_async(map_cta(sbase + C::kOffFac + 4 * (rank * kR + st), rank ^ 1), __float_as_uint(f),
+                      map_cta(bar(kFac), rank ^ 1));
+          if (st == 0) mbar_arrive_expect_tx(bar(kFac), kR * 4);
         } else {
           p.part_ml[(size_t)slot * 2 * kR + rank * kR + st] = make_float2(mr, lr);
         }
       }
       if (whole) {  // the factors of all 128 rows, from both CTAs
         named_bar_sync(1, kSmThreads);
-        if (st < 2) arrive_cluster(map_cta(bar(kFac), st));
-        pair_warp_wait(bar(kFac), wholes & 1, wc);
+        warp_wait(bar(kFac), wholes & 1, wc);
         ++wholes;
       }
       warp_wait(bar(kVFree0 + (g - 1) % KS), ((g - 1) / KS) & 1, wc);  // O^T is complete
       tc_fence_after();
       __syncwarp();
       if (whole) {
-        // 64 rows of a block of O^T at a time through the P buffers: scaled, packed to
-        // bf16 and transposed with stmatrix into two boxes of 64 rows x 64 columns,
-        // then row by row to out.  Warp w takes 32 columns of D (q4) and 32 rows (hc).
-        uint8_t* stg = smem + C::kOffP;
-        const int r0 = hc * 32;
+        // Each warp on its own, 32 columns of D (q4) x 32 rows (hc, and a step's half of
+        // the unit's rows) at a time through 2 KB of the P buffers: scaled, packed to
+        // bf16, transposed with stmatrix (row r: 64 bytes, 16-byte chunk c at
+        // c ^ (r / 2 % 4)) and stored to out as 64-byte pieces of rows.
+        const uint32_t stg = sP + warp * 2048;
+        const int mt = lane >> 3, jr = lane & 7;
 #pragma unroll 1
         for (int x = 0; x < 2 * C::kBlocks; ++x) {
-          const int b = x >> 1, rh = (x & 1) * 64;  // block of D, half of the rows
+          const int b = x >> 1, r0 = (x & 1) * 64 + hc * 32;  // block of D, first row
           uint32_t rr[2][16];
 #pragma unroll
           for (int half = 0; half < 2; ++half)
-            tmem_ld_16x256b_x4(tmem + ((uint32_t)(q4 * 32 + 16 * half) << 16) + C::kOCol + b * 128 + rh + r0,
+            tmem_ld_16x256b_x4(tmem + ((uint32_t)(q4 * 32 + 16 * half) << 16) + C::kOCol + b * 128 + r0,
                                rr[half]);
           tmem_wait_ld();
           float fac[8];
 #pragma unroll
           for (int rep = 0; rep < 4; ++rep) {
-            fac[2 * rep] = s_fac[rh + r0 + 8 * rep + 2 * tq];
-            fac[2 * rep + 1] = s_fac[rh + r0 + 8 * rep + 2 * tq + 1];
+            fac[2 * rep] = s_fac[r0 + 8 * rep + 2 * tq];
+            fac[2 * rep + 1] = s_fac[r0 + 8 * rep + 2 * tq + 1];
           }
+          __syncwarp();  // the step before has read the staging area
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t pk[8];
@@ -798,26 +779,24 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 pk[2 * rep + dg] = *reinterpret_cast<const uint32_t*>(&v2);
               }
             }
-            const int mt = lane >> 3, jr = lane & 7;
-            const int dl = q4 * 32 + 16 * half + 8 * (mt & 1);
-            const int box = dl >> 6, chunk = (dl & 63) >> 3;
+            // matrix mt of a stmatrix.x4: rows 8 (rep0 + mt / 2) .., columns 16 half + 8 (mt % 2) ..
 #pragma unroll
             for (int rep0 = 0; rep0 < 4; rep0 += 2) {
-              const int r = r0 + 8 * (rep0 + (mt >> 1)) + jr;
-              stmatrix_x4_trans(smem_addr(stg) + box * (kR * 128) + r * 128 + ((chunk ^ (r & 7)) << 4),
-                                pk[2 * rep0], pk[2 * rep0 + 1], pk[2 * rep0 + 2], pk[2 * rep0 + 3]);
+              const int r = 8 * (rep0 + (mt >> 1)) + jr, ch = 2 * half + (mt & 1);
+              stmatrix_x4_trans(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4), pk[2 * rep0],
+                                pk[2 * rep0 + 1], pk[2 * rep0 + 2], pk[2 * rep0 + 3]);
             }
           }
-          named_bar_sync(1, kSmThreads);
-          const int n = min(64, un.nrows - rh);
-          for (int e = st; e < n * 16; e += kSmThreads) {
-            const int r = e >> 4, ch = e & 15;
-            const uint4 w = *reinterpret_cast<const uint4*>(stg + (ch >> 3) * (kR * 128) + r * 128 +
-                                                            (((ch & 7) ^ (r & 7)) << 4));
-            *reinterpret_cast<uint4*>(p.out + (size_t)(un.row0 + rh + r) * D + rank * (D / 2) + b * 128 +
-                                      ch * 8) = w;
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 8 * e + (lane >> 2), ch = lane & 3;
+            const uint4 w = *reinterpret_cast<const uint4*>(smem + C::kOffP + warp * 2048 + r * 64 +
+                                                            ((ch ^ ((r >> 1) & 3)) << 4));
+            if (r0 + r < un.nrows)
+              *reinterpret_cast<uint4*>(p.out + (size_t)(un.row0 + r0 + r) * D + rank * (D / 2) + b * 128 +
+                                        q4 * 32 + ch * 8) = w;
           }
-          named_bar_sync(1, kSmThreads);  // the area may be rewritten
         }
       } else {
 #pragma unroll 1
