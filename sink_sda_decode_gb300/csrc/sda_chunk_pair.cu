@@ -18,11 +18,13 @@
 // first 32 positions, lanes 64..127 the same rows at the other 32.
 //
 // Roles in each CTA (the MMA warps issue in CTA 0, for both):
-//   warps 0..7   softmax and epilogue of the CTA's own 64 rows / own half of D
+//   warps 0..7   softmax of the CTA's own 64 rows
 //   warp 8       QK MMAs; q loads        warp 9   PV MMAs, and the decision below
 //   warp 10, 11  keys and values: by TMA, or (gather kernel) passing on to CTA 0
 //                that the CTA's loader warps have landed a stage
-//   warps 12..19 (gather kernel) 4 warps copy keys, 4 values, 16-byte cp.async
+//   warps 12..15 epilogue of the CTA's own half of D, while the softmax warps are
+//                already at the next unit (with the window of 128 a unit has 4 tiles)
+//   warps 16..23 (gather kernel) 4 warps copy keys, 4 values, 16-byte cp.async
 //
 // O^T of a row lies in both CTAs, so raising the row's running reference (rare) takes
 // both: with its weights of tile g ready, each CTA tells CTA 0 whether it raised one;
@@ -44,11 +46,13 @@ constexpr int kTile = 64;   // positions of a tile
 constexpr int kKeys = 32;   // of them, keys of a CTA
 constexpr int kSmThreads = 256, kSmWarps = 8;
 constexpr int kQkWarp = 8, kPvWarp = 9, kKeyWarp = 10, kValWarp = 11;
-constexpr int kLoadWarp0 = 12, kLoadWarps = 4;  // gather kernel: 4 for keys, then 4 for values
-// Gather kernel: 640 threads launch with 96 registers each; the softmax warps
-// grow to 128 and the loaders shrink to 64.
-constexpr int kGatherThreads = 640, kGatherRegs = 96;
-static_assert(kSmThreads * 128 + 2 * kLoadWarps * 32 * 64 + 128 * 96 <= kGatherThreads * kGatherRegs,
+constexpr int kEpiWarp0 = 12, kEpiWarps = 4;
+constexpr int kLoadWarp0 = 16, kLoadWarps = 4;  // gather kernel: 4 for keys, then 4 for values
+constexpr int kTmaThreads = 512;
+// Gather kernel: 768 threads launch with 80 registers each; the softmax warps
+// grow to 120, the loaders shrink to 48 and the others to 72.
+constexpr int kGatherThreads = 768, kGatherRegs = 80;
+static_assert(kSmThreads * 120 + 2 * kLoadWarps * 32 * 48 + 256 * 72 <= kGatherThreads * kGatherRegs,
               "register split exceeds the launch allocation");
 constexpr int kMaxStages = 3;
 
@@ -60,7 +64,8 @@ enum Bar : int {
   kPReady0 = kSEmpty0 + 2,  // CTA 0: weights of both
   kDecided0 = kPReady0 + 2, // both
   kScaled = kDecided0 + 2,  // CTA 0: the softmax warps of both
-  kFac,                     // both: the final factors of the other CTA's rows
+  kFac,                     // both: the final factors of the CTA's own and the other's rows
+  kODone,                   // both: the epilogue warps of both have read O^T and the factors
   kKFull0,                             // CTA 0
   kVFull0 = kKFull0 + kMaxStages,      // CTA 0
   kKFree0 = kVFull0 + kMaxStages,      // both
@@ -85,19 +90,21 @@ struct Cfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kPanels * kR * 128;
   static constexpr int kOffV = kOffK + kStages * kKBytes;
-  static constexpr int kOffP = kOffV + kStages * kVBytes;  // two P buffers; the epilogue's staging
+  static constexpr int kOffP = kOffV + kStages * kVBytes;  // two P buffers
   static constexpr int kOffBar = kOffP + 2 * kPBytes;
-  static constexpr int kOffMisc = kOffBar + 8 * kBars;     // tmem base, abort flag
+  static constexpr int kOffMisc = kOffBar + (8 * kBars + 15) / 16 * 16;  // tmem base, abort flag
   static constexpr int kOffFlag = kOffMisc + 16;           // int [2 tiles][2 CTAs] (CTA 0)
   static constexpr int kOffCmd = kOffFlag + 16;            // int [2 tiles]
   static constexpr int kOffAlpha = kOffCmd + 16;           // float [2 tiles][128 rows]
   static constexpr int kOffFac = kOffAlpha + 1024;         // float [128 rows]
-  static constexpr int kOffPart = kOffFac + 512;           // float [2 tiles][4 parts][64]: maxima; at the end l, m
+  static constexpr int kOffStage = kOffFac + 512;          // epilogue staging: 2 KB a warp
+  static constexpr int kOffPart = kOffStage + kEpiWarps * 2048;           // float [2 tiles][4 parts][64]: maxima; at the end l, m
   static constexpr int kSmem = kOffPart + 2048 + 1024;
   static constexpr int kOCol = 64;                         // O^T block b at columns 64 + 128 b
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kTile, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(256, 128, true, false);
   static_assert(kOCol + 128 * kBlocks <= 512, "TMEM columns");
+  static_assert(kOffStage % 16 == 0, "16-byte staging accesses");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -158,7 +165,7 @@ __device__ __forceinline__ void tma_pair_2d(uint32_t dst, const void* tmap, int 
 }
 
 template <int D, bool TMA>
-__global__ void __launch_bounds__(TMA ? 384 : kGatherThreads, 1)
+__global__ void __launch_bounds__(TMA ? kTmaThreads : kGatherThreads, 1)
 chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
                   const __grid_constant__ CUtensorMap tmap_kv, const ChunkParams p) {
   using C = Cfg<D>;
@@ -186,7 +193,8 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       mbar_init(bar(kDecided0 + s), 1);
     }
     mbar_init(bar(kScaled), 2 * kSmWarps);
-    mbar_init(bar(kFac), 1);
+    mbar_init(bar(kFac), 1);  // once the CTA's own are written; the other's are counted in bytes
+    mbar_init(bar(kODone), 2 * kEpiWarps);
     for (int s = 0; s < KS; ++s) {
       mbar_init(bar(kKFull0 + s), TMA ? 1 : 2);  // an expected count of bytes, or one CTA each
       mbar_init(bar(kVFull0 + s), TMA ? 1 : 2);
@@ -223,6 +231,9 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
   const int u0 = __ldcg(p.cta_unit + worker);
   const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
 
+  if constexpr (!TMA) {
+    if (warp >= kQkWarp && warp < kLoadWarp0) setmaxnreg_dec<72>();
+  }
   if (warp == kKeyWarp || warp == kValWarp) {
     const bool keys = warp == kKeyWarp;
     const int full0 = keys ? kKFull0 : kVFull0, free0 = keys ? kKFree0 : kVFree0;
@@ -280,7 +291,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
     for (int x = max(0, g - KS); x < g; ++x) pipe_drain(bar(free0 + x % KS), (x / KS) & 1, wc);
   } else if (!TMA && warp >= kLoadWarp0) {
     // ===================================================== rows one by one
-    setmaxnreg_dec<64>();
+    setmaxnreg_dec<48>();
     const bool keys = warp < kLoadWarp0 + kLoadWarps;
     const int v = (warp - kLoadWarp0) % kLoadWarps;
     const int free0 = keys ? kKFree0 : kVFree0, landed0 = keys ? kKLanded0 : kVLanded0;
@@ -414,7 +425,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       Cursor c;
       c.init(p.units, u0, t0, nt);
       volatile int* flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag);
-      int scaled = 0, said[2] = {0, 0};
+      int scaled = 0, pieces = 0, said[2] = {0, 0};
       for (int g = 0; g < nt; ++g) {
         const int s = g & 1, ks = g % KS;
         bool ok = warp_wait(bar(kPReady0 + s), (g >> 1) & 1, wc);
@@ -438,6 +449,9 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
           ++scaled;
         }
         if (ok) ok = warp_wait(bar(kVFull0 + ks), (g / KS) & 1, wc);
+        // O^T of the piece before has been read
+        if (ok && c.first && pieces > 0) ok = warp_wait(bar(kODone), (pieces - 1) & 1, wc);
+        pieces += c.first;
         if (!ok) break;
         if (!TMA) fence_proxy_async_smem();
         tc_fence_after();
@@ -464,7 +478,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // tile's positions 32 kh .., kh = q4 / 2 -- and of these the 16 positions from
     // 16 hc on, hc = w / 4.  Thread t holds rows base + t / 4 + 8 i, i = 0..3, at the
     // positions 8 rep + 2 (t % 4) + {0, 1}, rep = 0, 1: element 4 i + 2 rep + {0, 1}.
-    if constexpr (!TMA) setmaxnreg_inc<128>();
+    if constexpr (!TMA) setmaxnreg_inc<120>();
     const int q4 = warp & 3, hc = warp >> 2, st = threadIdx.x, tq = lane & 3;
     const int kh = q4 >> 1, rb = (q4 & 1) * 32, part = 2 * kh + hc, row0 = rb + (lane >> 2);
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
@@ -477,7 +491,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const uint32_t s_empty[2] = {bar0(kSEmpty0), bar0(kSEmpty0 + 1)};
     const uint32_t p_ready[2] = {bar0(kPReady0), bar0(kPReady0 + 1)};
     const uint32_t my_flag = map_cta(sbase + C::kOffFlag, 0) + 4 * rank;
-    int g = 0, wholes = 0;
+    int g = 0, pieces = 0;
     // What was decided on tile x: scales O^T or clears bad values if it has to be
     // (the PV MMAs of tile x wait for that).  Uniform over both CTAs' softmax warps.
     auto decided = [&](int x) {
@@ -541,6 +555,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const bool whole = i0 == 0 && i1 == un.ntiles;
       const int h0 = un.h0 + rank * kR, nrows = max(0, min(kR, un.nrows - rank * kR));
       const int p_lo = un.pos0 + h0 / H, p_hi = un.pos0 + (h0 + max(nrows, 1) - 1) / H;
+      const float sink = whole && st < nrows ? __ldg(p.attn_sink + (h0 + st) % H) : 0.f;  // of row st
       float m[4], l[4], scr[4];  // l: this thread's share
       int pos[4];
 #pragma unroll
@@ -681,9 +696,8 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) l[i4] += sum[i4];
         // What was decided on tile g - 1 has long come in by now; its PV MMAs, if they
-        // wait for O^T to be scaled, come before tile g's.  (A piece's last tile is
-        // looked at before its epilogue.)
-        if (i > i0) decided(g - 1);
+        // wait for O^T to be scaled, come before tile g's.
+        if (g > 0) decided(g - 1);
         if (st == 0) {
           if (flags) {
             store_cluster(my_flag + 8 * s, (uint32_t)flags);
@@ -693,7 +707,6 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       }
       // ---------------------------------------------- end of the piece
-      decided(g - 1);
       // (the last tile's barriers lie behind every read of the maxima)
       float* s_l = s_part;            // [4 parts][64]
       float* s_m = s_part + 256;      // [64]
@@ -709,13 +722,14 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       }
       named_bar_sync(1, kSmThreads);
-      const int slot = 2 * worker + (i0 == 0 ? 1 : 0);
+      // the factors of the piece before have been read in both CTAs
+      if (pieces > 0) warp_wait(bar(kODone), (pieces - 1) & 1, wc);
       if (st < kR) {
         const float mr = s_m[st], lr = (s_l[st] + s_l[64 + st]) + (s_l[128 + st] + s_l[192 + st]);
+        float f = 0.f;
         if (whole) {
-          float f = 0.f;
           if (st < nrows) {
-            const float ms = __ldg(p.attn_sink + (h0 + st) % H) * kLog2e;
+            const float ms = sink * kLog2e;
             const float M = fmaxf(mr, ms);
             float lse = M * kLn2;
             if (M != -INFINITY && ms != INFINITY) {
@@ -726,32 +740,43 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             p.lse[un.row0 + rank * kR + st] = lse;
           }
-          s_fac[rank * kR + st] = f;
-          store_async(map_cta(sbase + C::kOffFac + 4 * (rank * kR + st), rank ^ 1), __float_as_uint(f),
-                      map_cta(bar(kFac), rank ^ 1));
-          if (st == 0) mbar_arrive_expect_tx(bar(kFac), kR * 4);
         } else {
+          const int slot = 2 * worker + (i0 == 0 ? 1 : 0);
           p.part_ml[(size_t)slot * 2 * kR + rank * kR + st] = make_float2(mr, lr);
         }
+        s_fac[rank * kR + st] = f;
+        store_async(map_cta(sbase + C::kOffFac + 4 * (rank * kR + st), rank ^ 1), __float_as_uint(f),
+                    map_cta(bar(kFac), rank ^ 1));
       }
-      if (whole) {  // the factors of all 128 rows, from both CTAs
-        named_bar_sync(1, kSmThreads);
-        warp_wait(bar(kFac), wholes & 1, wc);
-        ++wholes;
-      }
+      named_bar_sync(1, kSmThreads);  // (s_part may be rewritten, too)
+      if (st == 0) mbar_arrive_expect_tx(bar(kFac), kR * 4);
+      ++pieces;
+    }
+    if (g > 0) decided(g - 1);
+  } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
+    // ===================================================== epilogue
+    // Warp q4 takes the TMEM lanes 32 q4 .., so columns 32 q4 .. of each block of the
+    // CTA's half of D, for all 128 rows, 32 rows at a time.
+    const int q4 = warp & 3, tq = lane & 3, mt = lane >> 3, jr = lane & 7;
+    const float* s_fac = reinterpret_cast<const float*>(smem + C::kOffFac);
+    uint8_t* stg = smem + C::kOffStage + q4 * 2048;
+    int g = 0, pieces = 0;
+    for (int u = u0; g < nt; ++u) {
+      const ChunkUnit un = load_unit(p.units + u);
+      const int i0 = g == 0 ? t0 - un.cum : 0;
+      const int i1 = min(un.ntiles, i0 + nt - g);
+      const bool whole = i0 == 0 && i1 == un.ntiles;
+      g += i1 - i0;
+      warp_wait(bar(kFac), pieces & 1, wc);
       warp_wait(bar(kVFree0 + (g - 1) % KS), ((g - 1) / KS) & 1, wc);  // O^T is complete
       tc_fence_after();
-      __syncwarp();
       if (whole) {
-        // Each warp on its own, 32 columns of D (q4) x 32 rows (hc, and a step's half of
-        // the unit's rows) at a time through 2 KB of the P buffers: scaled, packed to
-        // bf16, transposed with stmatrix (row r: 64 bytes, 16-byte chunk c at
-        // c ^ (r / 2 % 4)) and stored to out as 64-byte pieces of rows.
-        const uint32_t stg = sP + warp * 2048;
-        const int mt = lane >> 3, jr = lane & 7;
+        // scaled, packed to bf16, transposed with stmatrix (row r: 64 bytes, 16-byte
+        // chunk c at c ^ (r / 2 % 4)) and stored to out as 64-byte pieces of rows
 #pragma unroll 1
-        for (int x = 0; x < 2 * C::kBlocks; ++x) {
-          const int b = x >> 1, r0 = (x & 1) * 64 + hc * 32;  // block of D, first row
+        for (int x = 0; x < 4 * C::kBlocks; ++x) {
+          const int b = x >> 2, r0 = (x & 3) * 32;  // block of D, first row
+          if (r0 >= un.nrows) continue;
           uint32_t rr[2][16];
 #pragma unroll
           for (int half = 0; half < 2; ++half)
@@ -783,7 +808,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
             for (int rep0 = 0; rep0 < 4; rep0 += 2) {
               const int r = 8 * (rep0 + (mt >> 1)) + jr, ch = 2 * half + (mt & 1);
-              stmatrix_x4_trans(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4), pk[2 * rep0],
+              stmatrix_x4_trans(smem_addr(stg) + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4), pk[2 * rep0],
                                 pk[2 * rep0 + 1], pk[2 * rep0 + 2], pk[2 * rep0 + 3]);
             }
           }
@@ -791,21 +816,21 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = 8 * e + (lane >> 2), ch = lane & 3;
-            const uint4 w = *reinterpret_cast<const uint4*>(smem + C::kOffP + warp * 2048 + r * 64 +
-                                                            ((ch ^ ((r >> 1) & 3)) << 4));
+            const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
             if (r0 + r < un.nrows)
               *reinterpret_cast<uint4*>(p.out + (size_t)(un.row0 + r0 + r) * D + rank * (D / 2) + b * 128 +
                                         q4 * 32 + ch * 8) = w;
           }
         }
       } else {
+        const int slot = 2 * worker + (i0 == 0 ? 1 : 0);
 #pragma unroll 1
         for (int b = 0; b < C::kBlocks; ++b) {
           const int d = rank * (D / 2) + b * 128 + q4 * 32 + lane;
 #pragma unroll 1
-          for (int col = 16 * hc; col < 128; col += 32) {
+          for (int col = 0; col < un.nrows; col += 16) {
             uint32_t ov[16];
-            tmem_ld16(tmem + lane_base + C::kOCol + b * 128 + col, ov);
+            tmem_ld16(tmem + ((uint32_t)(q4 * 32) << 16) + C::kOCol + b * 128 + col, ov);
             tmem_wait_ld();
             float* o = p.part_o + ((size_t)slot * 2 * kR + col) * D + d;
 #pragma unroll
@@ -814,8 +839,12 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       }
       tc_fence_before();
-      named_bar_sync(1, kSmThreads);
+      __syncwarp();
+      if (lane < 2) arrive_cluster(map_cta(bar(kODone), lane));
+      ++pieces;
     }
+    // (the other CTA's last arrivals come in before this CTA's memory goes away)
+    if (pieces > 0) pipe_drain(bar(kODone), (pieces - 1) & 1, wc);
   }
 
   __syncwarp();
@@ -830,7 +859,7 @@ template <typename F>
 cudaError_t for_shape(int D, bool tma, F&& f) {
 #define SDA_CASE(DV)                                                                        \
   if (D == DV)                                                                              \
-    return tma ? f(chunk_pair_kernel<DV, true>, (size_t)Cfg<DV>::kSmem, dim3(384))          \
+    return tma ? f(chunk_pair_kernel<DV, true>, (size_t)Cfg<DV>::kSmem, dim3(kTmaThreads))  \
                : f(chunk_pair_kernel<DV, false>, (size_t)Cfg<DV>::kSmem, dim3(kGatherThreads));
   SDA_CASE(256) SDA_CASE(512)
 #undef SDA_CASE

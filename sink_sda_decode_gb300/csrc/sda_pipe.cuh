@@ -10,12 +10,30 @@
 namespace sda {
 
 #ifdef __CUDACC__
+// How long a try of a wait may sleep: warps that poll more often slow the others
+// down (attention of a 2048-token chunk over 8192 positions: 1.43 ms without the
+// hint, 1.37 with it).
+constexpr uint32_t kWaitHintNs = 10000000;
+
 // Where a bounded wait reports a timeout, and after how long.
 struct PipeWait {
   volatile int* abort_flag;  // shared: set once any role of the CTA gave up
   int* error;                // global error word (1 = a wait timed out)
   uint64_t timeout_ns;
 };
+
+// try_wait that may sleep for up to `ns` before it answers.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
 
 // Bounded wait.  Returns false (and raises the abort flags) on timeout; once
 // any role has aborted, every later wait returns false at once, so all roles
@@ -25,8 +43,8 @@ __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, const P
   if (*w.abort_flag) return false;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0) {
+    if (mbar_try_wait_for(bar, parity, kWaitHintNs)) return true;
+    if ((it & 15u) == 0) {
       if (*w.abort_flag) return false;
       if (ptx::globaltimer_ns() - t0 > w.timeout_ns) {
         *w.abort_flag = 1;
