@@ -60,6 +60,7 @@ cudaError_t device_caps(DeviceCaps* caps) {
       if (d.err == cudaSuccess) d.err = umma_prepare(nh);
     if (d.err == cudaSuccess) d.err = chunk_prepare();
     if (d.err == cudaSuccess) d.err = mass_prepare();
+    if (d.err == cudaSuccess) d.err = evict_prepare();
   });
   *caps = d.caps;
   return d.err;

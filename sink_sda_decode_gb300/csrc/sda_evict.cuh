@@ -21,6 +21,7 @@ struct EvictArgs {
   int32_t* status;
 };
 
+cudaError_t evict_prepare();  // one-time kernel attributes on the current device
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
 
 }  // namespace sda

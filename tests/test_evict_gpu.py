@@ -34,7 +34,8 @@ def same(r, ref, W):
 @pytest.mark.parametrize("kind", ["random", "ties", "special"])
 @pytest.mark.parametrize("S,budget,first,recent", [
     (1, 1, 0, 0), (1, 0, 0, 0), (7, 3, 1, 1), (64, 63, 0, 63), (100, 100, 0, 0), (700, 512, 4, 128),
-    (1025, 1, 0, 0), (1025, 1, 1, 0), (3001, 130, 2, 128), (5000, 4096, 4, 17), (20000, 333, 0, 0)])
+    (1025, 1, 0, 0), (1025, 1, 1, 0), (3001, 130, 2, 128), (5000, 4096, 4, 17), (20000, 333, 0, 0),
+    (4096, 700, 3, 5), (4097, 700, 3, 5), (210000, 1000, 4, 128)])
 def test_evict(kind, S, budget, first, recent):
     B = 5
     s, t = inputs(S + budget, B, S, kind)
