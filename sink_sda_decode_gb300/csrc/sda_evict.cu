@@ -11,7 +11,7 @@
 // gives every position its rank among the kept or the freed ones.
 //
 // evict_cluster_kernel: one CTA (tables of up to 4096 columns) or a cluster of 8
-// a sequence, each CTA with its share of the positions in shared memory, so that
+// or 6 a sequence, each CTA with its share of the positions in shared memory, so that
 // scores and slots are read once; the digits' histograms and the kept counts of
 // the CTAs are put together through distributed shared memory, and each warp
 // writes the kept and the freed of 32 positions in a row at a time.  16 sequences
@@ -34,8 +34,9 @@ namespace sda {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kBins = 2048;
-static_assert(kBins == 2 * kThreads, "two histogram bins per thread");
+constexpr int kBins = 4096;       // of the widest digit (12 bits)
+static_assert(kBins == 4 * kThreads, "four histogram bins per thread");
+constexpr int kStreamBins = 2048;  // evict_stream_kernel: digits of 11, 11 and 10 bits
 
 __device__ __forceinline__ uint32_t weight_key(float f) {
   uint32_t u = __float_as_uint(f);
@@ -102,9 +103,13 @@ __global__ void __launch_bounds__(kThreads) evict_indptr_kernel(const EvictArgs 
   if (threadIdx.x == 0) *a.status = bad ? 1 : 0;
 }
 
-// Rows of up to kOneCta columns take one CTA, longer ones a cluster of kCluster.
-constexpr int kOneCta = 4096, kCluster = 8, kFused = 4096;
+// Rows of up to kOneCta columns take one CTA, longer ones a cluster of 8 or 6: 14
+// clusters of 8 run at once on a GB300, or 24 of 6, so that more than 14 sequences
+// take clusters of 6 where their share fits (16 sequences of up to 131072: 31 us in
+// clusters of 6, 42 us in two waves of clusters of 8).
+constexpr int kOneCta = 4096, kFused = 4096, kClusters8 = 14;
 constexpr size_t kMaxSmem = 200 * 1024;
+static_assert(kMaxSmem / 8 / 32 <= kBins / 2, "the bits of a share's rows of 32 fit the histogram");
 // Positions of a CTA's share of n positions: a multiple of 32.
 __host__ __device__ inline int64_t share_of(int64_t n, int ctas) {
   return ((n + ctas - 1) / ctas + 31) / 32 * 32;
@@ -120,6 +125,14 @@ __device__ __forceinline__ uint32_t map_cta(const void* p, uint32_t cta) {
 __device__ __forceinline__ uint32_t load_cta(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load4_cta(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 template <int CS>
@@ -138,7 +151,7 @@ __device__ __forceinline__ void all_sync() {
 template <int CS, bool FUSED>
 __global__ void __launch_bounds__(kThreads) evict_cluster_kernel(const EvictArgs a) {
   extern __shared__ uint32_t s_pos[];  // [share] scores, then [share] slots
-  __shared__ uint32_t hist[kBins];
+  __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ uint32_t warp_sums[kThreads / 32];
   __shared__ uint32_t s_digit, s_above, s_count, s_before, s_all;
   __shared__ uint2 s_tot;                     // this CTA's (certainly kept, tied) positions
@@ -212,54 +225,55 @@ __global__ void __launch_bounds__(kThreads) evict_cluster_kernel(const EvictArgs
     prefix = 0xffffffffu;  // no key reaches it (+inf is 0xff800000)
     mask = 0xffffffffu;
   } else {
+    // Digits: sign and exponent (9 bits, a few values among many keys: four
+    // histograms, lanes take turns), then 11 and 12 bits of the mantissa.
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const uint32_t dmask = pass == 2 ? 0x3ffu : 0x7ffu;
-      for (int x0 = c0; x0 < c1; x0 += kThreads) {
-        const int x = x0 + tid;
-        const uint32_t key = x < c1 ? weight_key(sc[x]) : 0u;
-        const bool in = x < c1 && (key & mask) == prefix;
-        if (pass == 0) {
-          // the leading bits (sign, exponent) of a warp's keys are few values
-          nan_seen |= x < c1 && key == 0u;
-          const uint32_t d = in ? key >> 21 : 0xffffffffu;
-          const uint32_t same = __match_any_sync(0xffffffffu, d);
-          if (in && lane == __ffs(same) - 1) atomicAdd(&hist[d], (uint32_t)__popc(same));
-        } else if (in) {
-          atomicAdd(&hist[(key >> shift) & dmask], 1u);
-        }
+      const int shift = pass == 0 ? 23 : (pass == 1 ? 12 : 0);
+      const int bins = pass == 0 ? 512 : (pass == 1 ? 2048 : 4096);
+      const uint32_t copy = pass == 0 ? (uint32_t)(lane & 3) * 512u : 0u;
+      for (int x = c0 + tid; x < c1; x += kThreads) {
+        const uint32_t key = weight_key(sc[x]);
+        if (pass == 0) nan_seen |= key == 0u;
+        if ((key & mask) == prefix) atomicAdd(&hist[copy + ((key >> shift) & (bins - 1))], 1u);
+      }
+      if (pass == 0) {
+        __syncthreads();
+        if (tid < 512) hist[tid] += hist[512 + tid] + hist[1024 + tid] + hist[1536 + tid];
       }
       all_sync<CS>();
-      // bins 2047 - 2i and 2046 - 2i belong to thread i: sums over the CTAs, suffix sums
-      uint32_t hi = 0, lo = 0;
-      if constexpr (CS > 1) {
-        uint32_t h[CS], l[CS];
+      // sums over the CTAs, 4 bins a thread
+      uint4 sum = make_uint4(0, 0, 0, 0);
+      if (4 * tid < bins) {
+        if constexpr (CS > 1) {
+          uint4 v[CS];
 #pragma unroll
-        for (int c = 0; c < CS; ++c) {
-          l[c] = load_cta(map_cta(&hist[kBins - 2 - 2 * tid], c));
-          h[c] = load_cta(map_cta(&hist[kBins - 1 - 2 * tid], c));
+          for (int c = 0; c < CS; ++c) v[c] = load4_cta(map_cta(&hist[4 * tid], c));
+#pragma unroll
+          for (int c = 0; c < CS; ++c)
+            sum.x += v[c].x, sum.y += v[c].y, sum.z += v[c].z, sum.w += v[c].w;
+        } else {
+          sum = *reinterpret_cast<const uint4*>(&hist[4 * tid]);
         }
-#pragma unroll
-        for (int c = 0; c < CS; ++c) hi += h[c], lo += l[c];
-      } else {
-        hi = hist[kBins - 1 - 2 * tid];
-        lo = hist[kBins - 2 - 2 * tid];
       }
+      // keys in the threads before this one, and so (from the total) in those behind
+      const uint32_t mine = sum.x + sum.y + sum.z + sum.w;
       uint32_t total;
-      const uint32_t above = scan_exclusive(hi + lo, warp_sums, &total);
-      if (above < need && above + hi >= need) {
-        s_digit = kBins - 1 - 2 * tid;
-        s_above = above;
-        s_count = hi;
-      } else if (above + hi < need && above + hi + lo >= need) {
-        s_digit = kBins - 2 - 2 * tid;
-        s_above = above + hi;
-        s_count = lo;
+      const uint32_t before = scan_exclusive(mine, warp_sums, &total);
+      uint32_t above = total - before - mine;  // keys in higher bins
+      const uint32_t q[4] = {sum.w, sum.z, sum.y, sum.x};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (above < need && above + q[e] >= need) {
+          s_digit = 4 * tid + 3 - e;
+          s_above = above;
+          s_count = q[e];
+        }
+        above += q[e];
       }
       all_sync<CS>();  // (every CTA has read the histograms, too)
       prefix |= s_digit << shift;
-      mask |= dmask << shift;
+      mask |= (uint32_t)(bins - 1) << shift;
       need -= s_above;
       const bool whole = need == s_count;  // the same in every CTA
       for (int x = tid; x < kBins; x += kThreads) hist[x] = 0;
@@ -267,20 +281,22 @@ __global__ void __launch_bounds__(kThreads) evict_cluster_kernel(const EvictArgs
       if (whole) break;
     }
   }
-  // Warp w takes the positions [32 rows w, 32 rows (w + 1)), a row of 32 at a time.
+  // Warp w takes the positions [32 rows w, 32 rows (w + 1)), a row of 32 at a time:
+  // which are kept for certain, and which are tied, as bits (where the histograms were).
   const int rows = (cnt + kThreads - 1) / kThreads;
   const int w0 = warp * rows * 32;
-  auto kind = [&](int x) {  // 0: not kept, 1: tied, 2: certainly kept (and 3: no position)
-    if (x >= cnt) return 3;
-    if (x < c0 || x >= c1) return 2;
-    const uint32_t m = weight_key(sc[x]) & mask;
-    return m > prefix ? 2 : (m == prefix ? 1 : 0);
-  };
+  uint2* bits = reinterpret_cast<uint2*>(hist) + warp * rows;
   uint32_t gt = 0, eq = 0;
+#pragma unroll 4
   for (int r = 0; r < rows; ++r) {
-    const int kd = kind(w0 + r * 32 + lane);
-    gt += __popc(__ballot_sync(0xffffffffu, kd == 2));
-    eq += __popc(__ballot_sync(0xffffffffu, kd == 1));
+    const int x = w0 + r * 32 + lane;
+    const uint32_t m = x < cnt ? weight_key(sc[x]) & mask : 0u;
+    const bool race = x >= c0 && x < c1;
+    const uint32_t gb = __ballot_sync(0xffffffffu, x < cnt && (!race || m > prefix));
+    const uint32_t eb = __ballot_sync(0xffffffffu, race && m == prefix);
+    if (lane == 0) bits[r] = make_uint2(gb, eb);
+    gt += __popc(gb);
+    eq += __popc(eb);
   }
   if (lane == 0) s_warp[warp] = make_uint2(gt, eq);
   __syncthreads();
@@ -303,16 +319,17 @@ __global__ void __launch_bounds__(kThreads) evict_cluster_kernel(const EvictArgs
   int32_t* oslots = a.out_slots + (int64_t)b * a.out_S;
   uint32_t g_before = pre.x, e_before = pre.y;
   const uint32_t lt = (1u << lane) - 1;
+#pragma unroll 4
   for (int r = 0; r < rows; ++r) {
     const int x = w0 + r * 32 + lane;
-    const int kd = kind(x);
-    const uint32_t gb = __ballot_sync(0xffffffffu, kd == 2), eb = __ballot_sync(0xffffffffu, kd == 1);
+    const uint32_t gb = bits[r].x, eb = bits[r].y;
+    const bool sure = (gb >> lane) & 1u, tied = (eb >> lane) & 1u;
     const uint32_t e = e_before + __popc(eb & lt);          // tied positions before this one
     const uint32_t rk = g_before + __popc(gb & lt) + min(e, need);  // its rank among the kept
-    if (kd == 2 || (kd == 1 && e < need)) {
+    if (sure || (tied && e < need)) {
       orow[rk] = sc[x];
       oslots[rk] = sl[x];
-    } else if (kd < 2) {
+    } else if (x < cnt) {
       a.freed[foff + p0 + x - (int)rk] = sl[x];
     }
     g_before += __popc(gb);
@@ -334,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) evict_cluster_kernel(const EvictArgs
 __global__ void __launch_bounds__(kThreads) evict_stream_kernel(const EvictArgs a) {
   pdl_wait();
   pdl_trigger();
-  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t hist[kStreamBins];
   __shared__ uint32_t warp_sums[kThreads / 32];
   __shared__ uint32_t s_digit, s_above, s_count;
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -360,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) evict_stream_kernel(const EvictArgs 
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
       const uint32_t dmask = pass == 2 ? 0x3ffu : 0x7ffu;
-      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+      for (int i = tid; i < kStreamBins; i += kThreads) hist[i] = 0;
       __syncthreads();
       for (int p = m0 + tid; p < m1; p += kThreads) {
         const uint32_t key = weight_key(row[p]);
@@ -369,15 +386,15 @@ __global__ void __launch_bounds__(kThreads) evict_stream_kernel(const EvictArgs 
       }
       __syncthreads();
       // bins 2047 - 2i and 2046 - 2i belong to thread i: suffix sums
-      const uint32_t hi = hist[kBins - 1 - 2 * tid], lo = hist[kBins - 2 - 2 * tid];
+      const uint32_t hi = hist[kStreamBins - 1 - 2 * tid], lo = hist[kStreamBins - 2 - 2 * tid];
       uint32_t total;
       const uint32_t above = scan_exclusive(hi + lo, warp_sums, &total);
       if (above < need && above + hi >= need) {
-        s_digit = kBins - 1 - 2 * tid;
+        s_digit = kStreamBins - 1 - 2 * tid;
         s_above = above;
         s_count = hi;
       } else if (above + hi < need && above + hi + lo >= need) {
-        s_digit = kBins - 2 - 2 * tid;
+        s_digit = kStreamBins - 2 - 2 * tid;
         s_above = above + hi;
         s_count = lo;
       }
@@ -443,8 +460,10 @@ cudaError_t evict_prepare() {
   const void* kernels[] = {
       reinterpret_cast<const void*>(evict_cluster_kernel<1, true>),
       reinterpret_cast<const void*>(evict_cluster_kernel<1, false>),
-      reinterpret_cast<const void*>(evict_cluster_kernel<kCluster, true>),
-      reinterpret_cast<const void*>(evict_cluster_kernel<kCluster, false>)};
+      reinterpret_cast<const void*>(evict_cluster_kernel<6, true>),
+      reinterpret_cast<const void*>(evict_cluster_kernel<6, false>),
+      reinterpret_cast<const void*>(evict_cluster_kernel<8, true>),
+      reinterpret_cast<const void*>(evict_cluster_kernel<8, false>)};
   for (const void* k : kernels) {
     const cudaError_t e =
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
@@ -454,7 +473,7 @@ cudaError_t evict_prepare() {
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
-  const int cs = a.S <= kOneCta ? 1 : kCluster;
+  const int cs = a.S <= kOneCta ? 1 : (a.B > kClusters8 && share_of(a.S, 6) * 8 <= (int64_t)kMaxSmem ? 6 : 8);
   const size_t smem = (size_t)share_of(a.S, cs) * 8;
   const bool staged = smem <= kMaxSmem;
   const bool fused = staged && a.B > 0 && a.B <= kFused && a.out_len != a.kv_len;
@@ -470,7 +489,8 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
     return launch_pdl_cluster(kernel, dim3(a.B * cs), dim3(kThreads), cs, smem, st, a);
   };
   if (cs == 1) return fused ? go(evict_cluster_kernel<1, true>) : go(evict_cluster_kernel<1, false>);
-  return fused ? go(evict_cluster_kernel<kCluster, true>) : go(evict_cluster_kernel<kCluster, false>);
+  if (cs == 6) return fused ? go(evict_cluster_kernel<6, true>) : go(evict_cluster_kernel<6, false>);
+  return fused ? go(evict_cluster_kernel<8, true>) : go(evict_cluster_kernel<8, false>);
 }
 
 }  // namespace sda

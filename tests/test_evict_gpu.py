@@ -61,3 +61,13 @@ def test_bad_length_counts_as_zero():
     r = sda.evict_slots(s, t, n, 20)
     torch.cuda.synchronize()
     same(r, evict(s, t, n.tolist(), 20, 0, 0, 20), 20)
+
+
+@pytest.mark.parametrize("B,S,budget", [(20, 5000, 900), (20, 160000, 4096)])
+def test_many_sequences(B, S, budget):
+    """More sequences than clusters of 8 that run at once."""
+    s, t = inputs(B, B, S)
+    lens = np.random.default_rng(B).integers(0, S + 1, B).tolist()
+    r = sda.evict_slots(s, t, torch.tensor(lens, dtype=torch.int32).cuda(), budget, first=4, recent=9)
+    torch.cuda.synchronize()
+    same(r, evict(s, t, lens, budget, 4, 9, budget), budget)
