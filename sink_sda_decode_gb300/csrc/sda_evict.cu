@@ -232,10 +232,17 @@ __global__ void __launch_bounds__(kThreads) evict_cluster_kernel(const EvictArgs
       const int shift = pass == 0 ? 23 : (pass == 1 ? 12 : 0);
       const int bins = pass == 0 ? 512 : (pass == 1 ? 2048 : 4096);
       const uint32_t copy = pass == 0 ? (uint32_t)(lane & 3) * 512u : 0u;
-      for (int x = c0 + tid; x < c1; x += kThreads) {
-        const uint32_t key = weight_key(sc[x]);
-        if (pass == 0) nan_seen |= key == 0u;
-        if ((key & mask) == prefix) atomicAdd(&hist[copy + ((key >> shift) & (bins - 1))], 1u);
+      for (int x = c0 + tid; x < c1; x += 8 * kThreads) {
+        uint32_t key[8];  // all eight loads before the first of the atomics
+#pragma unroll
+        for (int e = 0; e < 8; ++e) key[e] = weight_key(sc[min(x + e * kThreads, c1 - 1)]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (x + e * kThreads < c1) {
+            if (pass == 0) nan_seen |= key[e] == 0u;
+            if ((key[e] & mask) == prefix) atomicAdd(&hist[copy + ((key[e] >> shift) & (bins - 1))], 1u);
+          }
+        }
       }
       if (pass == 0) {
         __syncthreads();
@@ -287,10 +294,10 @@ __global__ void __launch_bounds__(kThreads) evict_cluster_kernel(const EvictArgs
   const int w0 = warp * rows * 32;
   uint2* bits = reinterpret_cast<uint2*>(hist) + warp * rows;
   uint32_t gt = 0, eq = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int r = 0; r < rows; ++r) {
     const int x = w0 + r * 32 + lane;
-    const uint32_t m = x < cnt ? weight_key(sc[x]) & mask : 0u;
+    const uint32_t m = weight_key(sc[min(x, max(cnt - 1, 0))]) & mask;
     const bool race = x >= c0 && x < c1;
     const uint32_t gb = __ballot_sync(0xffffffffu, x < cnt && (!race || m > prefix));
     const uint32_t eb = __ballot_sync(0xffffffffu, race && m == prefix);
@@ -300,19 +307,20 @@ __global__ void __launch_bounds__(kThreads) evict_cluster_kernel(const EvictArgs
   }
   if (lane == 0) s_warp[warp] = make_uint2(gt, eq);
   __syncthreads();
-  uint2 pre = make_uint2(0, 0), tot = make_uint2(0, 0);
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const uint2 v = s_warp[w];
-    if (w < warp) pre.x += v.x, pre.y += v.y;
-    tot.x += v.x, tot.y += v.y;
-  }
+  const uint2 of = s_warp[lane];  // lane w: warp w's
+  uint2 pre;
+  pre.x = __reduce_add_sync(0xffffffffu, lane < warp ? of.x : 0u);
+  pre.y = __reduce_add_sync(0xffffffffu, lane < warp ? of.y : 0u);
   if constexpr (CS > 1) {
-    if (tid == 0) s_tot = tot;
+    if (tid == kThreads - 1) s_tot = make_uint2(pre.x + of.x, pre.y + of.y);  // lane 31 of warp 31
     all_sync<CS>();
-    for (int c = 0; c < rank; ++c) {
-      pre.x += load_cta(map_cta(&s_tot.x, c));
-      pre.y += load_cta(map_cta(&s_tot.y, c));
+    uint2 v = make_uint2(0, 0);
+    if (lane < rank) {  // lane c: CTA c's
+      v.x = load_cta(map_cta(&s_tot.x, lane));
+      v.y = load_cta(map_cta(&s_tot.y, lane));
     }
+    pre.x += __reduce_add_sync(0xffffffffu, v.x);
+    pre.y += __reduce_add_sync(0xffffffffu, v.y);
   }
   // in place: every CTA of the sequence holds its positions by now, so writes may begin
   float* orow = a.out_scores + (int64_t)b * a.out_S;
