@@ -75,11 +75,11 @@ struct Cursor {
 
 // Pool row of position j of sequence b; -1 for a table entry outside the pool
 // (which raises the error word).
-__device__ __forceinline__ int pool_row(const ChunkParams& p, int b, int j) {
-  const int blk = __ldg(p.g.block_table + (size_t)b * p.g.max_blocks + j / p.g.k_per_block);
-  const long long s = p.g.base + (long long)blk * p.g.k_per_block + j % p.g.k_per_block;
-  if (blk < 0 || s >= p.g.total_pages) {
-    atomicExch(&p.hdr->error, 3);
+__device__ __forceinline__ int pool_row_of(const ChunkGeom& g, int* error, int b, int j) {
+  const int blk = __ldg(g.block_table + (size_t)b * g.max_blocks + j / g.k_per_block);
+  const long long s = g.base + (long long)blk * g.k_per_block + j % g.k_per_block;
+  if (blk < 0 || s >= g.total_pages) {
+    atomicExch(error, 3);
     return -1;
   }
   return (int)s;
@@ -88,7 +88,7 @@ __device__ __forceinline__ int pool_row(const ChunkParams& p, int b, int j) {
 // (it is not read: zeros).
 __device__ __forceinline__ int seen_row(const ChunkParams& p, const Cursor& c, int j) {
   if (j >= c.hi || (j < c.lo && j >= p.g.first)) return -1;
-  return pool_row(p, c.b, j);
+  return pool_row_of(p.g, &p.hdr->error, c.b, j);
 }
 // The box of 16 positions from j on, in groups of 8 pool rows from `base` on:
 // 16 positions lie in one block (tiles and blocks start at multiples of 16) and

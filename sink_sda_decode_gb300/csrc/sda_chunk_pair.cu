@@ -108,62 +108,6 @@ struct Cfg {
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-// ---------------------------------------------------------------- pair PTX
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// Arrive on `bar` of both CTAs once this thread's earlier pair MMAs are done.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t cta) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
-  return r;
-}
-// (A release at cluster scope costs its thread about 1000 cycles, an acquire in a wait
-// about 400.  What goes to the other CTA on every tile is an arrival alone, after reads
-// of TMEM or after stores to the CTA's own shared memory that the MMAs read; stores to
-// the other CTA are rare and have a fence_cluster() of their own on both sides.)
-__device__ __forceinline__ void arrive_cluster(uint32_t mapped) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
-}
-__device__ __forceinline__ void store_cluster(uint32_t mapped, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapped), "r"(v) : "memory");
-}
-// Stores to the other CTA's shared memory, and counts the 4 bytes on its barrier.
-__device__ __forceinline__ void store_async(uint32_t mapped, uint32_t v, uint32_t mapped_bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(mapped),
-               "r"(v), "r"(mapped_bar)
-               : "memory");
-}
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-// Tiled loads into this CTA that complete on a barrier of the pair's CTA 0.
-__device__ __forceinline__ void tma_pair_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w,
-                                            uint32_t bar0) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar0)
-      : "memory");
-}
-__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar0) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar0)
-      : "memory");
-}
-
 template <int D, bool TMA>
 __global__ void __launch_bounds__(TMA ? kTmaThreads : kGatherThreads, 1)
 chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -211,11 +155,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (TMA) tma_prefetch_desc(&tmap_kv);
   }
   if (warp == kQkWarp) {  // both CTAs' warps together
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(tmem_slot)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tmem_alloc_pair(smem_addr(tmem_slot), 512);
   }
   tc_fence_before();
   __syncwarp();
@@ -852,7 +792,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
   cluster_sync();  // neither CTA leaves while the other may still reach its memory
   tc_fence_after();
   if (warp == kQkWarp)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    tmem_dealloc_pair(tmem, 512);
 }
 
 template <typename F>
