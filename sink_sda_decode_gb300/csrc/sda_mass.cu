@@ -18,9 +18,11 @@
 // tile) pairs form one sequence, cut into equal ranges, one per pair; a unit that a
 // range boundary cuts leaves its partial sums per piece, which a last kernel adds up
 // in order.
-//   warps 0..7    epilogue: warp w reads TMEM lane quadrant w % 4 (positions)
-//                 and half w / 4 of the row tile's columns
-//   warps 8..23   the unit's cached rows, 16-byte cp.async
+//   warps 0..15   epilogue: warp w reads TMEM lane quadrant w % 4 (positions)
+//                 and quarter w / 4 of the row tile's columns (with 8 warps the
+//                 weights, not the MMAs, set the pace: 488 us for 2 x 550 tokens over
+//                 7000 positions, 64 heads, where the MMAs alone take 271)
+//   warps 16..23  the unit's cached rows, 16-byte cp.async
 //   warp 24       q panels by TMA;  warp 25: the MMAs (CTA 0, for both)
 // mass_step_kernel, for steps of few rows: see there.
 #include <cuda_bf16.h>
@@ -38,8 +40,9 @@ using namespace ptx;
 constexpr int kKeys = 256;                // positions per unit, 128 a CTA
 constexpr int kRowsQ = 256;               // q rows per tile, 128 loaded by each CTA
 constexpr int kPanelB = 128 * 128;        // bytes of a panel: 128 rows x 64 columns
-constexpr int kEpWarps = 8, kEpThreads = 256;
-constexpr int kLoadWarp0 = 8, kLoadWarps = 16;
+constexpr int kEpWarps = 16, kEpThreads = 512;
+constexpr int kLoadWarp0 = 16, kLoadWarps = 8;
+constexpr int kStepThreads = 256;         // of mass_step_kernel's sums
 constexpr int kQWarp = 24, kMmaWarp = 25;
 constexpr int kThreads = 832;
 constexpr int kPlanThreads = 1024;
@@ -66,8 +69,8 @@ struct Cfg {
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = kPanels * kPanelB;
   static constexpr int kOffCol = kOffQ + kRing * kPanelB;  // per row tile: lse2 float[256], pos int[256]; two of them
-  static constexpr int kOffHalf = kOffCol + 2 * 2048;      // float [128]: the second column half's sums
-  static constexpr int kOffBar = kOffHalf + 512;
+  static constexpr int kOffPart = kOffCol + 2 * 2048;      // float [3][128]: the other column quarters' sums
+  static constexpr int kOffBar = kOffPart + 1536;
   static constexpr int kOffMisc = kOffBar + 256;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
   static constexpr uint32_t kIdesc = idesc_bf16_f32(kKeys, kRowsQ, false, false);
@@ -277,7 +280,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
 
   if (warp >= kLoadWarp0 && warp < kLoadWarp0 + kLoadWarps) {
     // ===================================================== the unit's cached rows
-    constexpr int kRows = 128 / kLoadWarps;  // 8 rows per warp: one swizzle atom
+    constexpr int kRows = 128 / kLoadWarps;  // 16 rows per warp: two swizzle atoms
     constexpr int kCh = D / 8 < 32 ? D / 8 : 32;
     constexpr int kRowsPer = 32 / kCh;
     const int v = warp - kLoadWarp0;
@@ -305,8 +308,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
         for (int c0 = 0; c0 < D / 8; c0 += kCh) {
           const int ch = c0 + lane % kCh;
           const uint4* src = slot >= 0 ? kv4 + (size_t)slot * (D / 8) + ch : kv4;
-          cp_async16(sK + (ch >> 3) * kPanelB + v * 1024 + r * 128 + (((ch & 7) ^ r) << 4), src,
-                     slot >= 0 ? 16u : 0u);
+          cp_async16(sK + (ch >> 3) * kPanelB + (2 * v + (r >> 3)) * 1024 + (r & 7) * 128 +
+                         (((ch & 7) ^ (r & 7)) << 4),
+                     src, slot >= 0 ? 16u : 0u);
         }
       }
       cp_async_commit();
@@ -377,7 +381,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
     // ===================================================== weights and sums
     const int q4 = warp & 3, hc = warp >> 2, st = threadIdx.x;
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    float* s_half = reinterpret_cast<float*>(smem + C::kOffHalf);
+    float* s_part = reinterpret_cast<float*>(smem + C::kOffPart);
     const float sc = p.qk_scale_log2;
     const int H = p.g.H, window = p.g.window, nfirst = p.g.first;
     int g = 0;
@@ -386,6 +390,11 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
       const int j = un.k0 + rank * 128 + q4 * 32 + lane;  // this thread's position
       const int k_last = min(un.k0 + kKeys, un.n) - 1;
       float sum = 0.f, comp = 0.f;
+      auto lse_of = [&](int i) {  // of this thread's column of row tile i
+        const int r = i * kRowsQ + st;
+        return st < kRowsQ && r < un.nrows ? __ldg(p.lse + un.row0 + r) * kLog2e : 0.f;
+      };
+      float lse_next = lse_of(pc.i0);
       for (int i = pc.i0; i < pc.i1; ++i, ++g) {
         const int s = g & 1;
         float* lse2 = reinterpret_cast<float*>(smem + C::kOffCol + s * 2048);
@@ -393,9 +402,10 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
         const int r0 = i * kRowsQ, nr = min(kRowsQ, un.nrows - r0);
         if (st < kRowsQ) {
           const bool in = st < nr;
-          lse2[st] = in ? __ldg(p.lse + un.row0 + r0 + st) * kLog2e : 0.f;
+          lse2[st] = lse_next;
           cpos[st] = in ? un.pos0 + (r0 + st) / H : INT_MIN;
         }
+        if (i + 1 < pc.i1) lse_next = lse_of(i + 1);
         named_bar_sync(1, kEpThreads);  // (also: everyone is past the tile that used these arrays)
         const int p_lo = un.pos0 + r0 / H, p_hi = un.pos0 + (r0 + nr - 1) / H;
         const bool full = nr == kRowsQ && k_last <= p_lo &&
@@ -404,7 +414,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
         tc_fence_after();
         float part = 0.f;
 #pragma unroll 1
-        for (int c0 = hc * 128; c0 < hc * 128 + 128 && c0 < nr; c0 += 16) {
+        for (int c0 = hc * 64; c0 < hc * 64 + 64 && c0 < nr; c0 += 16) {
           uint32_t v[16];
           tmem_ld16(tmem + lane_base + s * 256 + c0, v);
           tmem_wait_ld();
@@ -432,17 +442,18 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
         comp = (t - sum) - y;
         sum = t;
       }
-      if (hc == 1) s_half[q4 * 32 + lane] = sum;
+      if (hc > 0) s_part[(hc - 1) * 128 + q4 * 32 + lane] = sum;
       named_bar_sync(1, kEpThreads);
       if (hc == 0) {
-        sum += s_half[q4 * 32 + lane];
+        const float* o = s_part + q4 * 32 + lane;
+        sum = (sum + o[0]) + (o[128] + o[256]);
         if (pc.i0 == 0 && pc.i1 == un.nq) {
           if (j < un.n) p.out[(int64_t)un.b * p.S + j] += sum;
         } else {
           p.part[(size_t)(2 * worker + (pc.i0 == 0 ? 1 : 0)) * kKeys + rank * 128 + q4 * 32 + lane] = sum;
         }
       }
-      named_bar_sync(1, kEpThreads);  // s_half may be rewritten
+      named_bar_sync(1, kEpThreads);  // s_part may be rewritten
     }
   }
   __syncwarp();
@@ -772,13 +783,13 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (tl.row0 + r0 != have || nr != have_n) {  // these rows' lse and positions
           have = tl.row0 + r0;
           have_n = nr;
-          named_bar_sync(1, kEpThreads);
+          named_bar_sync(1, kStepThreads);
           if (tid < R) {
             const bool in = tid < nr;
             lse2[tid] = in ? __ldg(p.lse + have + tid) * kLog2e : 0.f;
             cpos[tid] = in ? tl.pos0 + (r0 + tid) / H : INT_MIN;
           }
-          named_bar_sync(1, kEpThreads);
+          named_bar_sync(1, kStepThreads);
         }
         const int p_lo = tl.pos0 + r0 / H, p_hi = tl.pos0 + (r0 + nr - 1) / H;
         const bool full = nr == R && last <= p_lo &&
@@ -829,7 +840,7 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
           half[hA] = sumA;
           half[hB] = sumB;
         }
-        named_bar_sync(1, kEpThreads);
+        named_bar_sync(1, kStepThreads);
       }
       if (hc == 0 && tq == 0) {
         if constexpr (R > 16) {
