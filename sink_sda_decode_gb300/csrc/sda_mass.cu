@@ -27,8 +27,6 @@
 // mass_step_kernel, for steps of few rows: see there.
 #include <cuda_bf16.h>
 
-#include <climits>
-
 #include "sda_chunk_dev.cuh"
 
 namespace sda {
@@ -60,6 +58,22 @@ struct alignas(16) MassUnit {
 };
 static_assert(sizeof(MassUnit) == 32, "two 16-byte words");
 
+// Rows (token, head) stand in the order of their tokens' positions, so those that see
+// position j are a range.  Of the rows [0, nr) of a tile whose row 0 is row r0 of a
+// stretch that starts at position pos0: [lo, hi).
+struct RowRange {
+  int lo, hi;
+};
+__device__ __forceinline__ RowRange rows_that_see(int j, int n, int pos0, int r0, int nr, int H,
+                                                  int window, int first) {
+  const long long a = ((long long)j - pos0) * H - r0;           // first row at j or behind
+  const long long z = ((long long)j - pos0 + window) * H - r0;  // first row that j has left behind
+  RowRange r;
+  r.lo = (int)max(0ll, min(a, (long long)nr));
+  r.hi = j >= n ? 0 : (window == 0 || j < first ? nr : (int)max(0ll, min(z, (long long)nr)));
+  return r;
+}
+
 enum Bar : int { kKFull = 0, kKEmpty, kAccFull0, kAccEmpty0 = kAccFull0 + 2, kQFull0 = kAccEmpty0 + 2 };
 
 template <int D>
@@ -68,8 +82,8 @@ struct Cfg {
   static constexpr int kRing = D == 512 ? 5 : 8;  // q panels in flight
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = kPanels * kPanelB;
-  static constexpr int kOffCol = kOffQ + kRing * kPanelB;  // per row tile: lse2 float[256], pos int[256]; two of them
-  static constexpr int kOffPart = kOffCol + 2 * 2048;      // float [3][128]: the other column quarters' sums
+  static constexpr int kOffCol = kOffQ + kRing * kPanelB;  // per row tile: lse2 float[256]; two of them
+  static constexpr int kOffPart = kOffCol + 2 * 1024;      // float [3][128]: the other column quarters' sums
   static constexpr int kOffBar = kOffPart + 1536;
   static constexpr int kOffMisc = kOffBar + 256;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
@@ -388,7 +402,6 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
     while (walk.next(&pc)) {
       const MassUnit& un = pc.un;
       const int j = un.k0 + rank * 128 + q4 * 32 + lane;  // this thread's position
-      const int k_last = min(un.k0 + kKeys, un.n) - 1;
       float sum = 0.f, comp = 0.f;
       auto lse_of = [&](int i) {  // of this thread's column of row tile i
         const int r = i * kRowsQ + st;
@@ -397,39 +410,32 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
       float lse_next = lse_of(pc.i0);
       for (int i = pc.i0; i < pc.i1; ++i, ++g) {
         const int s = g & 1;
-        float* lse2 = reinterpret_cast<float*>(smem + C::kOffCol + s * 2048);
-        int* cpos = reinterpret_cast<int*>(smem + C::kOffCol + s * 2048 + 1024);
+        float* lse2 = reinterpret_cast<float*>(smem + C::kOffCol + s * 1024);
         const int r0 = i * kRowsQ, nr = min(kRowsQ, un.nrows - r0);
-        if (st < kRowsQ) {
-          const bool in = st < nr;
-          lse2[st] = lse_next;
-          cpos[st] = in ? un.pos0 + (r0 + st) / H : INT_MIN;
-        }
+        if (st < kRowsQ) lse2[st] = lse_next;
         if (i + 1 < pc.i1) lse_next = lse_of(i + 1);
-        named_bar_sync(1, kEpThreads);  // (also: everyone is past the tile that used these arrays)
-        const int p_lo = un.pos0 + r0 / H, p_hi = un.pos0 + (r0 + nr - 1) / H;
-        const bool full = nr == kRowsQ && k_last <= p_lo &&
-                          (window == 0 || un.k0 > p_hi - window || k_last < nfirst);
+        const RowRange rr = rows_that_see(j, un.n, un.pos0, r0, nr, H, window, nfirst);
+        named_bar_sync(1, kEpThreads);  // (also: everyone is past the tile that used this array)
         warp_wait(bar(kAccFull0 + s), (g >> 1) & 1, wc);
         tc_fence_after();
         float part = 0.f;
+        // 16 rows at a time; masks only where a lane needs them
 #pragma unroll 1
-        for (int c0 = hc * 64; c0 < hc * 64 + 64 && c0 < nr; c0 += 16) {
+        for (int c0 = hc * 64; c0 < hc * 64 + 64; c0 += 16) {
+          if (!__any_sync(0xffffffffu, rr.lo < c0 + 16 && rr.hi > c0 && rr.lo < rr.hi)) continue;
           uint32_t v[16];
           tmem_ld16(tmem + lane_base + s * 256 + c0, v);
           tmem_wait_ld();
           float a[4] = {0.f, 0.f, 0.f, 0.f};
-          if (full) {
+          if (__all_sync(0xffffffffu, rr.lo <= c0 && rr.hi >= c0 + 16)) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               a[e & 3] += ex2_approx(fmaf(__uint_as_float(v[e]), sc, -lse2[c0 + e]));
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int pos = cpos[c0 + e];
-              const bool see = j <= pos && (window == 0 || j > pos - window || j < nfirst);
               const float w = ex2_approx(fmaf(__uint_as_float(v[e]), sc, -lse2[c0 + e]));
-              a[e & 3] += see ? w : 0.f;
+              a[e & 3] += c0 + e >= rr.lo && c0 + e < rr.hi ? w : 0.f;
             }
           }
           part += (a[0] + a[1]) + (a[2] + a[3]);
@@ -519,8 +525,8 @@ struct StepCfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kPanels * R * 128;
   static constexpr int kOffTiles = kOffK + kStages * kStage;       // int [kStepSeqs + 1]: tiles before sequence b
-  static constexpr int kOffCol = kOffTiles + 4 * kStepSeqs + 16;   // lse2 float[64], pos int[64]
-  static constexpr int kOffSum = kOffCol + 512;                    // float [2 tiles][64]
+  static constexpr int kOffCol = kOffTiles + 4 * kStepSeqs + 16;   // lse2 float[64]
+  static constexpr int kOffSum = kOffCol + 256;                    // float [2 tiles][64]
   static constexpr int kOffBar = kOffSum + 512;
   static constexpr int kOffMisc = kOffBar + 256;
   static constexpr int kSmem = kOffMisc + 160 + 1024;
@@ -763,7 +769,6 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const int q4 = warp & 3, hc = warp >> 2, tq = lane & 3;
     const int hA = q4 * 16 + (lane >> 2), hB = hA + 8;
     float* lse2 = reinterpret_cast<float*>(smem + C::kOffCol);
-    int* cpos = reinterpret_cast<int*>(smem + C::kOffCol + 256);
     float* s_sum = reinterpret_cast<float*>(smem + C::kOffSum);
     const float sc = p.qk_scale_log2;
     const int window = p.g.window, nfirst = p.g.first;
@@ -771,7 +776,7 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
     int a = 0, have = -1, have_n = 0, x = 0;
     walk(true, [&](const StepTile& tl) {
       const int64_t at = (int64_t)tl.b * p.S + tl.k0;
-      const int jA = tl.k0 + hA, jB = tl.k0 + hB, last = min(tl.k0 + kTileS, tl.n) - 1;
+      const int jA = tl.k0 + hA, jB = tl.k0 + hB;
       float before[2] = {0.f, 0.f};
       if (hc == 0 && tq == 0 && p.prev) {
         if (jA < tl.n) before[0] = p.prev[at + hA];
@@ -780,20 +785,16 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
       float sumA = 0.f, sumB = 0.f, compA = 0.f, compB = 0.f;
       for (int r0 = 0; r0 < tl.nrows; r0 += R, ++a) {
         const int s = a & 1, nr = min(R, tl.nrows - r0);
-        if (tl.row0 + r0 != have || nr != have_n) {  // these rows' lse and positions
+        if (tl.row0 + r0 != have || nr > have_n) {  // these rows' lse
           have = tl.row0 + r0;
           have_n = nr;
           named_bar_sync(1, kStepThreads);
-          if (tid < R) {
-            const bool in = tid < nr;
-            lse2[tid] = in ? __ldg(p.lse + have + tid) * kLog2e : 0.f;
-            cpos[tid] = in ? tl.pos0 + (r0 + tid) / H : INT_MIN;
-          }
+          if (tid < R) lse2[tid] = tid < nr ? __ldg(p.lse + have + tid) * kLog2e : 0.f;
           named_bar_sync(1, kStepThreads);
         }
-        const int p_lo = tl.pos0 + r0 / H, p_hi = tl.pos0 + (r0 + nr - 1) / H;
-        const bool full = nr == R && last <= p_lo &&
-                          (window == 0 || tl.k0 > p_hi - window || last < nfirst);
+        const RowRange ra = rows_that_see(jA, tl.n, tl.pos0, r0, nr, H, window, nfirst);
+        const RowRange rb = rows_that_see(jB, tl.n, tl.pos0, r0, nr, H, window, nfirst);
+        const bool full = __all_sync(0xffffffffu, ra.lo == 0 && ra.hi == R && rb.lo == 0 && rb.hi == R);
         warp_wait(bar(kSAccFull0 + s), (a >> 1) & 1, wc);
         tc_fence_after();
         if (work) {
@@ -807,13 +808,9 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
           for (int rep = 0; rep < kReps; ++rep) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int c = 32 * hc + 8 * rep + 2 * tq + (k & 1), j = k < 2 ? jA : jB;
+              const int c = 32 * hc + 8 * rep + 2 * tq + (k & 1);
               const float w = ex2_approx(fmaf(__uint_as_float(v[4 * rep + k]), sc, -lse2[c]));
-              bool see = true;
-              if (!full) {
-                const int pos = cpos[c];
-                see = j <= pos && (window == 0 || j > pos - window || j < nfirst);
-              }
+              const bool see = full || (k < 2 ? c >= ra.lo && c < ra.hi : c >= rb.lo && c < rb.hi);
               (k < 2 ? pA : pB) += see ? w : 0.f;
             }
           }
