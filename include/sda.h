@@ -465,14 +465,21 @@ sda_status sda_qk_norm_rope_swa_store_fp8(const void* q, const void* kv, const v
  *   attn_sink   [H] fp32 sink logits (-inf: no sink)
  *   out         [T, H, D] bf16, 16-byte aligned, overlapping neither q nor the
  *               pool; lse [T, H] fp32
- * The device error word (sda_decode_error_flag on the workspace): 2 = q_indptr
+ * The device error word (sda_paged_error_flag on the workspace): 2 = q_indptr
  * or kv_len broke the contract (nothing computed); 3 = a table entry pointed
  * outside the pool (that row counts as zeros, outputs that see it are
- * unspecified); 1 = a pipeline wait timed out.  Three launches, no
- * allocation, graph-capturable; calls that may run at the same time need a
- * workspace each.
+ * unspecified); 1 = a pipeline wait timed out.  One to three launches (short
+ * tables and windows, few units, many), no allocation, graph-capturable; calls
+ * that may run at the same time need a workspace each.
  */
 sda_status sda_chunk_attention_workspace_size(int B, int T, int H, int D, size_t* bytes);
+
+/*
+ * Device-side error word of the last sda_chunk_attention or sda_attention_mass
+ * that used `workspace`: writes one int32 (0 = fine) to *device_flag (device
+ * memory), ordered on `stream`.
+ */
+sda_status sda_paged_error_flag(const void* workspace, int32_t* device_flag, void* stream);
 
 sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t total_pages,
                                const int32_t* block_table, int max_blocks, int k_per_block,

@@ -20,14 +20,14 @@ import torch
 
 from . import _lib
 from .paged import (Evicted, attention_mass, attention_mass_workspace_size, chunk_attention,
-                    chunk_attention_workspace_size, evict_slots)
+                    chunk_attention_workspace_size, evict_slots, paged_error_flag)
 
 __all__ = ["decode", "workspace_size", "build_indices", "validate_indices", "decode_error_flag",
            "decode_kernel", "decode_fp8", "workspace_size_fp8", "qk_norm_rope_swa_store", "topk_slots", "build_decode",
            "build_decode_host", "build_decode_host_workspace_size",
            "decode_host", "set_timing_events", "decode_noalloc", "library_path",
            "chunk_attention", "chunk_attention_workspace_size", "attention_mass",
-           "attention_mass_workspace_size", "evict_slots", "Evicted"]
+           "attention_mass_workspace_size", "evict_slots", "Evicted", "paged_error_flag"]
 
 library_path = _lib.LIB_PATH
 

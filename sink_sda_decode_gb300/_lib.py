@@ -65,6 +65,7 @@ SIGNATURES = {
     "sda_chunk_attention": (_i32, [_vp, _vp, _i64, _vp, _i32, _i32, _i64, _vp, _vp, _vp, _f32, _i32,
                                    _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_size_t,
                                    _vp]),
+    "sda_paged_error_flag": (_i32, [_vp, _vp, _vp]),
     "sda_attention_mass_workspace_size": (_i32, [_i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]),
     "sda_attention_mass": (_i32, [_vp, _vp, _i64, _vp, _i32, _i32, _i64, _vp, _vp, _vp, _f32, _i32,
                                   _i32, _vp, _f32, _i32, _i32, _i32, _i32, _vp, _vp,

@@ -954,6 +954,17 @@ static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+sda_status sda_paged_error_flag(const void* workspace, int32_t* device_flag, void* stream) {
+  if (!workspace || !device_flag || !aligned(workspace, 256) || !aligned(device_flag, 4))
+    return SDA_ERR_INVALID_ARG;
+  const cudaError_t e = launch_paged_error(workspace, device_flag, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) {
+    note_cuda_error(e, "sda_paged_error_flag");
+    return SDA_ERR_CUDA;
+  }
+  return SDA_OK;
+}
+
 sda_status sda_chunk_attention_workspace_size(int B, int T, int H, int D, size_t* bytes) {
   if (!bytes) return SDA_ERR_INVALID_ARG;
   ChunkGeom g = {};
@@ -966,7 +977,7 @@ sda_status sda_chunk_attention_workspace_size(int B, int T, int H, int D, size_t
     note_cuda_error(e, "sda_chunk_attention_workspace_size");
     return SDA_ERR_CUDA;
   }
-  *bytes = chunk_layout(B, T, H, D, caps.num_sms).total;
+  *bytes = chunk_layout(g, caps.num_sms).total;
   return SDA_OK;
 }
 
@@ -1002,7 +1013,7 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
     note_cuda_error(e, "sda_chunk_attention");
     return SDA_ERR_CUDA;
   }
-  const ChunkLayout L = chunk_layout(B, T, H, D, caps.num_sms);
+  const ChunkLayout L = chunk_layout(g, caps.num_sms);
   if (workspace_bytes < L.total) return SDA_ERR_WORKSPACE;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   e = launch_chunk_plan(g, L, workspace, st);

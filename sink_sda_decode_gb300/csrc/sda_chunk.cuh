@@ -50,23 +50,38 @@ __host__ __device__ inline int chunk_tile_start(int i, int nf, int lo, int tile)
   return (i < nf ? i : lo / tile + i - nf) * tile;
 }
 
-// Header of the workspace.
+// Header of the workspace (256 bytes), and behind it one error word per CTA.
 struct ChunkHeader {
   int n_units;
   int n_tiles;  // KV tiles of all units
-  int per;      // tiles per CTA: CTA k owns tiles [k * per, min((k + 1) * per, n_tiles))
-  int ctas;     // CTAs with tiles
-  int error;    // 1 = a wait timed out, 2 = bad lengths (nothing computed), 3 = bad table entry
-  int pad[59];
+  int per;      // tiles per worker: worker k owns tiles [k * per, min((k + 1) * per, n_tiles))
+  int ctas;     // workers with tiles
+  int error;    // 2 = bad lengths (nothing computed)
+  int words;    // error words of this call (1 = a wait timed out, 3 = bad table entry)
+  int pad[58];
 };
 static_assert(sizeof(ChunkHeader) == 256, "header is 256 bytes");
-static_assert(offsetof(ChunkHeader, error) == offsetof(WsHeader, error),
-              "sda_decode_error_flag reads either header");
+constexpr size_t kErrorWords = 256, kErrorBytes = 4 * kMaxPlanGrid;  // offset and size of the words
+
+// Where a worker (a CTA, or a pair of CTAs) begins, and how far it goes.
+struct alignas(16) ChunkStart {
+  int b, r;  // sequence, and unit of it
+  int off;   // first tile of that unit
+  int nt;    // tiles in all
+};
+
+// How the tiles are shared out.
+//   kPlanned  equal numbers of tiles, by a kernel before
+//   kCut      the same, but every CTA finds its own beginning (few units)
+//   kWhole    whole units, every CTA its share: no merge of pieces is launched
+enum ChunkMode : int { kPlanned = 0, kCut = 1, kWhole = 2 };
+constexpr int kFusedSeqs = 2048, kFusedUnits = 4096;  // most that the CTAs look through themselves
 
 struct ChunkLayout {
-  size_t units_off, seq_off, cta_off, ml_off, o_off, total;
-  int u_max, grid, R, tile;  // R: rows per unit; grid: CTAs, or pairs of CTAs, that share the tiles
-  bool pair;                 // units of 128 rows, 64 for each CTA of a cluster of two
+  size_t start_off, rec_off, seq_off, ml_off, o_off, total;
+  int grid, R, tile;  // R: rows per unit; grid: workers that share the tiles
+  bool pair;          // units of 128 rows, 64 for each CTA of a cluster of two
+  ChunkMode mode;
 };
 // Positions per KV tile (a multiple of 16).  With 64 rows of q at D = 512 two
 // stages of 64 positions fit beside q, or three of 48: the tensor pipe needs
@@ -81,8 +96,11 @@ inline bool chunk_boxes(const ChunkGeom& g) {
   const int64_t rows = g.total_pages - g.base;
   return g.k_per_block % 16 == 0 && rows > 0 && rows % 8 == 0;
 }
-// The layout for B sequences of T tokens in all.
-ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms);
+// The layout of a call (the sizes depend on B, T, H and D alone).
+ChunkLayout chunk_layout(const ChunkGeom& g, int num_sms);
+
+// error = the largest of a workspace's error words.
+cudaError_t launch_paged_error(const void* ws, int32_t* error, cudaStream_t st);
 
 cudaError_t chunk_prepare();  // one-time kernel attributes on the current device
 cudaError_t launch_chunk_plan(const ChunkGeom& g, const ChunkLayout& L, void* ws, cudaStream_t st);
@@ -109,6 +127,37 @@ cudaError_t launch_mass(const void* q, const void* kv, const ChunkGeom& g, const
 void note_cuda_error(cudaError_t e, const char* where);
 
 #ifdef __CUDACC__
+__device__ __forceinline__ int units_of(const ChunkGeom& g, int R, int b) {
+  const int m = __ldg(g.q_indptr + b + 1) - __ldg(g.q_indptr + b);
+  return (int)(((long long)m * g.H + R - 1) / R);
+}
+__device__ __forceinline__ bool lengths_bad(const ChunkGeom& g, int b) {
+  const int q0 = __ldg(g.q_indptr + b), q1 = __ldg(g.q_indptr + b + 1), n = __ldg(g.kv_len + b);
+  return q0 < 0 || q1 < q0 || q1 > g.T || n < 0 || n > (long long)g.max_blocks * g.k_per_block;
+}
+// Unit r of sequence b (cum is left 0).
+__device__ __forceinline__ ChunkUnit chunk_unit(const ChunkGeom& g, int R, int tile, int b, int r) {
+  const int q0 = __ldg(g.q_indptr + b), m = __ldg(g.q_indptr + b + 1) - q0, n = __ldg(g.kv_len + b);
+  const int r0 = r * R;  // row in the sequence's m * H rows
+  ChunkUnit d;
+  d.row0 = q0 * g.H + r0;
+  d.nrows = min(R, m * g.H - r0);
+  d.b = b;
+  const int tok = r0 / g.H;
+  d.pos0 = n - m + tok;
+  d.h0 = r0 - tok * g.H;
+  const int p_hi = d.pos0 + (d.h0 + d.nrows - 1) / g.H;
+  d.hi = max(p_hi + 1, 0);
+  d.lo = g.window > 0 ? (int)max((long long)d.pos0 - g.window + 1, 0ll) : 0;
+  if (d.hi == 0) d.lo = 0;
+  const int lot = d.lo / tile;
+  d.nf = (min(g.first, lot * tile) + tile - 1) / tile;
+  // rows that see nothing: one tile of masked positions
+  d.ntiles = max(d.nf + (d.hi + tile - 1) / tile - lot, 1);
+  d.cum = d.pad0 = d.pad1 = 0;
+  return d;
+}
+
 // Exclusive scan over a block of 1024 threads; *total (shared) holds the sum.
 __device__ inline long long scan_exclusive(long long v, long long* warp_sums, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

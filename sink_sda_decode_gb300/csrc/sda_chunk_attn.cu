@@ -96,6 +96,7 @@ struct Cfg {
   static_assert((kPanels - 1) * kPanelQ + 64 * 128 <= kOffBar, "padded QK operand inside smem");
   static_assert(D >= 128 || 2 * kPBytes >= 1024, "padded PV operand inside smem");
   static_assert(kTile % 16 == 0 && kTile <= 64, "MMA shapes");
+  static_assert(kStages * kStage >= 4 * (kFusedSeqs + 1), "chunk_begin's words");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -150,12 +151,22 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // everything above overlaps the plan; global memory only below
   pdl_trigger();
-  const int per = __ldcg(&p.hdr->per), n_tiles = __ldcg(&p.hdr->n_tiles);
-  const long long t0l = (long long)blockIdx.x * per;
-  const int t0 = (int)min(t0l, (long long)n_tiles);
-  const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // this CTA's tiles
-  const int u0 = __ldcg(p.cta_unit + blockIdx.x);
-  const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
+  bool bad;
+  const ChunkStart begin = chunk_begin<TMA ? 384 : kGatherThreads, R, kTile>(
+      p, blockIdx.x, reinterpret_cast<int*>(smem + C::kOffKV),
+      reinterpret_cast<int*>(smem + C::kOffP), &bad);
+  const int nt = begin.nt;  // this CTA's tiles
+  int* const error = reinterpret_cast<int*>(reinterpret_cast<char*>(p.hdr) + kErrorWords) + blockIdx.x;
+  if (threadIdx.x == 0) {
+    *error = 0;
+    if (blockIdx.x == 0) {
+      p.hdr->words = gridDim.x;
+      if (p.mode != kPlanned) p.hdr->error = bad ? 2 : 0;
+    }
+  }
+  __syncthreads();
+  const PipeWait wc{abort_flag, error, p.wait_timeout_ns};
+  using Walk = Cursor<R, kTile>;
 
   if (TMA && warp == kTmaWarp) {
     // ===================================================== KV tiles by TMA
@@ -164,27 +175,22 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // prefetches of the tile two ahead into L2, kept this warp busier than the
     // tensor pipe: one TMA instruction costs about 90 cycles of issue.)
     const int behind = (int)((p.g.total_pages - p.g.base) / 8);
-    auto box_of = [&](const Cursor& c) {
+    auto box_of = [&](const Walk& c) {
       return lane < C::kBoxes
-                 ? box_group(p, c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + lane * 16)
+                 ? box_group(p, error, c, c.start() + lane * 16)
                  : behind;
     };
-    Cursor c;  // runs a tile ahead of the copies
-    c.init(p.units, u0, t0, nt);
+    Walk c;  // runs a tile ahead of the copies
+    c.init(p.g, begin);
     int y = behind;
     if (c.left > 0) {
       y = box_of(c);
-      c.next();
+      c.next(p.g);
     }
     bool ok = true;
     int loads = 0;
     for (int g = 0; g < nt && ok; ++g) {
       const int s = g % KS;
-      int y_next = behind;
-      if (c.left > 0) {
-        y_next = box_of(c);
-        c.next();
-      }
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
         if (g >= KS) ok = warp_wait(pv_done(s, h), ((g / KS) - 1) & 1, wc);
@@ -195,7 +201,10 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (lane < C::kBoxes) tma_load_4d(dst, &tmap_kv, 0, 0, h * C::kPanelsH, y, kv_full(s, h));
         ++loads;
       }
-      y = y_next;
+      if (c.left > 0) {  // (after this tile's copies: the table entry is a while coming)
+        y = box_of(c);
+        c.next(p.g);
+      }
     }
     // copies in flight land before the CTA's memory goes away (the last KS stages)
     for (int x = max(0, loads - KS * HV); x < loads; ++x)
@@ -208,34 +217,28 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     constexpr int kRowsPer = 32 / kCh;                 // rows per warp-wide copy
     const int v = warp - kLoadWarp0;
     const uint4* kv4 = reinterpret_cast<const uint4*>(p.kv);
-    auto slot_of = [&](const Cursor& c) {  // lanes 0 .. kRows - 1: rows kRows v + lane
+    auto slot_of = [&](const Walk& c) {  // lanes 0 .. kRows - 1: rows kRows v + lane
       return lane < kRows
-                 ? seen_row(p, c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + v * kRows + lane)
+                 ? seen_row(p, error, c, c.start() + v * kRows + lane)
                  : -1;
     };
     auto prefetch = [&](int slot) {
       if (slot >= 0) bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(p.kv) + (size_t)slot * D * 2, D * 2);
     };
-    Cursor c;  // runs two tiles ahead of the copies
-    c.init(p.units, u0, t0, nt);
+    Walk c;  // runs two tiles ahead of the copies
+    c.init(p.g, begin);
     int sl0 = -1, sl1 = -1;
     if (c.left > 0) {
       sl0 = slot_of(c);
-      c.next();
+      c.next(p.g);
     }
     if (c.left > 0) {
       sl1 = slot_of(c);
-      prefetch(sl1);
-      c.next();
+      c.next(p.g);
     }
     bool ok = true;
     for (int g = 0; g < nt && ok; ++g) {
       const int s = g % KS;
-      int sl2 = -1;
-      if (c.left > 0) {
-        sl2 = slot_of(c);
-        c.next();
-      }
       const uint32_t stage = sKV + s * C::kStage;
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
@@ -257,19 +260,23 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // on to the next stage meanwhile (the reader fences to the async proxy)
         cp_async_arrive(kv_full(s, h));
       }
-      prefetch(sl2);
+      prefetch(sl1);
       sl0 = sl1;
-      sl1 = sl2;
+      sl1 = -1;
+      if (c.left > 0) {
+        sl1 = slot_of(c);
+        c.next(p.g);
+      }
     }
     cp_async_wait_all();
   } else if (warp == kQkWarp) {
     // ===================================================== QK MMAs
-    Cursor c;
-    c.init(p.units, u0, t0, nt);
+    Walk c;
+    c.init(p.g, begin);
     int pieces = 0, q_loads = 0;
     bool ok = true;
     auto load_q = [&]() {
-      const int row = __ldcg(&p.units[c.u].row0);
+      const int row = c.row0;
       if (elect_one()) {
         mbar_arrive_expect_tx(bar(kQFull), C::kPanels * C::kPanelQ);
 #pragma unroll
@@ -310,7 +317,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         __syncwarp();
       }
       if (!ok) break;
-      c.next();
+      c.next(p.g);
       if (last) {
         if (c.left > 0) {  // q of the next unit, once this unit's MMAs have read q
           ok = warp_wait(bar(kQEmpty), pieces & 1, wc);
@@ -328,8 +335,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     __syncwarp();
   } else if (warp == kPvWarp) {
     // ===================================================== PV MMAs
-    Cursor c;
-    c.init(p.units, u0, t0, nt);
+    Walk c;
+    c.init(p.g, begin);
     for (int g = 0; g < nt; ++g) {
       const int s = g & 1, ks = g % KS;
       if (!warp_wait(bar(kPReady0 + s), (g >> 1) & 1, wc)) break;
@@ -351,7 +358,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       }
       __syncwarp();
-      c.next();
+      c.next(p.g);
     }
     if (elect_one()) {
       mma_commit(bar(kDrainPv));
@@ -379,9 +386,12 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // on block-wide votes), so every named barrier is reached by all of them
     // even after a wait timed out.
     int g = 0;
-    for (int u = u0; g < nt; ++u) {
-      const ChunkUnit un = load_unit(p.units + u);
-      const int i0 = g == 0 ? t0 - un.cum : 0;
+    UnitWalk uw;
+    uw.init(p.g, R, begin);
+    for (int pieces = 0; g < nt; ++pieces) {
+      if (pieces > 0) uw.next(p.g, R);
+      const ChunkUnit un = chunk_unit(p.g, R, kTile, uw.b, uw.r);
+      const int i0 = g == 0 ? begin.off : 0;
       const int i1 = min(un.ntiles, i0 + nt - g);
       const bool whole = i0 == 0 && i1 == un.ntiles;
       const bool vA = hA < un.nrows, vB = hB < un.nrows;
@@ -806,8 +816,10 @@ ChunkParams chunk_params(const void* kv, const ChunkGeom& g, const float* attn_s
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.hdr = reinterpret_cast<ChunkHeader*>(base);
-  p.units = reinterpret_cast<const ChunkUnit*>(base + L.units_off);
-  p.cta_unit = reinterpret_cast<const int*>(base + L.cta_off);
+  p.starts = reinterpret_cast<ChunkStart*>(base + L.start_off);
+  p.recs = reinterpret_cast<ChunkUnit*>(base + L.rec_off);
+  p.mode = L.mode;
+  p.workers = L.grid;
   p.part_ml = reinterpret_cast<float2*>(base + L.ml_off);
   p.part_o = reinterpret_cast<float*>(base + L.o_off);
   p.g = g;

@@ -17,8 +17,9 @@ struct ChunkParams {
   __nv_bfloat16* out;
   float* lse;
   ChunkHeader* hdr;
-  const ChunkUnit* units;
-  const int* cta_unit;
+  ChunkStart* starts;
+  ChunkUnit* recs;  // recs[k]: the unit that holds tile k * per, for the combine
+  int mode, workers;
   float2* part_ml;
   float* part_o;
   ChunkGeom g;
@@ -26,52 +27,183 @@ struct ChunkParams {
   uint64_t wait_timeout_ns;
 };
 
-__device__ __forceinline__ ChunkUnit load_unit(const ChunkUnit* u) {
-  ChunkUnit d;
-  int4* w = reinterpret_cast<int4*>(&d);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) w[i] = __ldcg(reinterpret_cast<const int4*>(u) + i);
-  return d;
-}
-
-// Walks the CTA's tiles in order; every role walks the same ones.
-struct Cursor {
-  const ChunkUnit* units;
-  int u;           // unit
-  int i;           // logical tile within the unit
-  int left;        // tiles left to this CTA, this one included
-  bool first;      // first tile of this CTA's piece of the unit
-  int b, lo, hi, nf, ntiles;
-  __device__ __forceinline__ void load() {
-    const int4 a = __ldcg(reinterpret_cast<const int4*>(units + u) + 1);
-    ntiles = __ldcg(&units[u].ntiles);
-    b = __ldcg(&units[u].b);
-    lo = a.y;
-    hi = a.z;
-    nf = a.w;
+// Walks units from one on.
+struct UnitWalk {
+  int b, r, nu;  // unit r of sequence b, which has nu
+  __device__ __forceinline__ void init(const ChunkGeom& g, int R, const ChunkStart& s) {
+    b = s.b;
+    r = s.r;
+    nu = s.nt > 0 ? units_of(g, R, b) : 0;
   }
-  __device__ __forceinline__ void init(const ChunkUnit* us, int u0, int t0, int n) {
-    units = us;
-    u = u0;
-    left = n;
-    first = true;
-    if (left > 0) {
-      load();
-      i = t0 - __ldcg(&units[u].cum);
-    }
-  }
-  __device__ __forceinline__ bool last() const { return left == 1 || i == ntiles - 1; }
-  __device__ __forceinline__ void next() {
-    first = false;
-    --left;
-    if (++i == ntiles && left > 0) {
-      ++u;
-      i = 0;
-      first = true;
-      load();
+  __device__ __forceinline__ void next(const ChunkGeom& g, int R) {
+    ++r;
+    while (r >= nu) {
+      r = 0;
+      nu = units_of(g, R, ++b);
     }
   }
 };
+
+// Walks a worker's tiles in order; every role walks the same ones.  R: rows of
+// a unit.
+template <int R, int TILE>
+struct Cursor {
+  UnitWalk w;
+  int i;       // logical tile within the unit
+  int left;    // tiles left, this one included
+  bool first;  // first tile of this worker's piece of the unit
+  int b, lo, hi, nf, ntiles, row0;
+  __device__ __forceinline__ void load(const ChunkGeom& g) {
+    const ChunkUnit d = chunk_unit(g, R, TILE, w.b, w.r);
+    b = w.b;
+    lo = d.lo;
+    hi = d.hi;
+    nf = d.nf;
+    ntiles = d.ntiles;
+    row0 = d.row0;
+  }
+  __device__ __forceinline__ void init(const ChunkGeom& g, const ChunkStart& s) {
+    w.init(g, R, s);
+    left = s.nt;
+    first = true;
+    i = s.off;
+    if (left > 0) load(g);
+  }
+  __device__ __forceinline__ bool last() const { return left == 1 || i == ntiles - 1; }
+  __device__ __forceinline__ int start() const { return chunk_tile_start(i, nf, lo, TILE); }
+  __device__ __forceinline__ void next(const ChunkGeom& g) {
+    first = false;
+    --left;
+    if (++i == ntiles && left > 0) {
+      w.next(g, R);
+      i = 0;
+      first = true;
+      load(g);
+    }
+  }
+};
+
+// Where worker `worker` begins; called by all THREADS threads of the CTA, which
+// then are past a barrier.  `s_seq` (kFusedSeqs + 1 words) and `scratch` (64 words)
+// are shared memory that is free until then.  *bad: the lengths broke the contract.
+template <int THREADS, int R, int TILE>
+__device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker, int* s_seq,
+                                                  int* scratch, bool* bad) {
+  const ChunkGeom& g = p.g;
+  ChunkStart st = {0, 0, 0, 0};
+  *bad = false;
+  if (p.mode == kPlanned) {
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(p.starts + worker));
+    return ChunkStart{v.x, v.y, v.z, v.w};
+  }
+  constexpr int kW = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long* sums = reinterpret_cast<long long*>(scratch);  // [kW]
+  int* found = scratch + 2 * kW;                             // [4]
+  // exclusive prefix of one value per thread, and the total
+  auto scan = [&](long long v, long long* total) {
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();  // (sums may be rewritten)
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long before = 0, all = 0;
+    for (int w = 0; w < kW; ++w) {
+      const long long s = sums[w];
+      if (w < warp) before += s;
+      all += s;
+    }
+    *total = all;
+    return before + x - v;
+  };
+  // s_seq[b] = units of the sequences before b
+  const int each = (g.B + THREADS - 1) / THREADS;
+  const int b0 = min(tid * each, g.B), b1 = min(b0 + each, g.B);
+  int wrong = 0;
+  long long mine = 0, U;
+  for (int b = b0; b < b1; ++b) {
+    if (lengths_bad(g, b)) wrong = 1;
+    else mine += units_of(g, R, b);
+  }
+  long long at = scan(mine, &U);
+  *bad = __syncthreads_or(wrong);
+  if (*bad) return st;
+  for (int b = b0; b < b1; ++b) {
+    s_seq[b] = (int)at;
+    at += units_of(g, R, b);
+  }
+  if (tid == 0) s_seq[g.B] = (int)U;
+  __syncthreads();
+  if (p.mode == kWhole) {
+    const int lo = (int)(U * worker / p.workers), hi = (int)(U * (worker + 1) / p.workers);
+    long long nt = 0, tot;
+    for (int u = lo + tid; u < hi; u += THREADS) {
+      const int b = last_le(s_seq, g.B, u);
+      nt += chunk_unit(g, R, TILE, b, u - s_seq[b]).ntiles;
+    }
+    scan(nt, &tot);
+    if (lo < hi) {
+      st.b = last_le(s_seq, g.B, lo);
+      st.r = lo - s_seq[st.b];
+      st.nt = (int)tot;
+    }
+  } else {
+    // each thread a stretch of units
+    const int eu = ((int)U + THREADS - 1) / THREADS;
+    const int u0 = min(tid * eu, (int)U), u1 = min(u0 + eu, (int)U);
+    long long nt = 0, tt;
+    UnitWalk w = {};
+    auto from = [&]() {
+      w.b = last_le(s_seq, g.B, u0);
+      w.r = u0 - s_seq[w.b];
+      w.nu = units_of(g, R, w.b);
+    };
+    if (u0 < u1) {
+      from();
+      for (int u = u0; u < u1; ++u) {
+        nt += chunk_unit(g, R, TILE, w.b, w.r).ntiles;
+        if (u + 1 < u1) w.next(g, R);
+      }
+    }
+    long long cum = scan(nt, &tt);
+    if (tt > 0x7fffffffll) {
+      *bad = true;
+      return st;
+    }
+    const int per = tt > 0 ? (int)((tt + p.workers - 1) / p.workers) : 1;
+    const long long t0 = (long long)worker * per;
+    if (t0 >= cum && t0 < cum + nt) {  // this thread's stretch holds the first tile
+      from();
+      for (;;) {
+        ChunkUnit d = chunk_unit(g, R, TILE, w.b, w.r);
+        if (t0 < cum + d.ntiles) {
+          found[0] = w.b;
+          found[1] = w.r;
+          found[2] = (int)(t0 - cum);
+          d.cum = (int)cum;
+          p.recs[worker] = d;
+          break;
+        }
+        cum += d.ntiles;
+        w.next(g, R);
+      }
+    }
+    if (worker == 0 && tid == 0) {
+      p.hdr->n_tiles = (int)tt;
+      p.hdr->per = per;
+      p.hdr->ctas = (int)((tt + per - 1) / per);
+    }
+    __syncthreads();
+    if (t0 < tt) st = ChunkStart{found[0], found[1], found[2], (int)min((long long)per, tt - t0)};
+  }
+  ptx::fence_proxy_async_smem();  // the tiles will be written here through the async proxy
+  __syncthreads();
+  return st;
+}
 
 // Pool row of position j of sequence b; -1 for a table entry outside the pool
 // (which raises the error word).
@@ -86,20 +218,22 @@ __device__ __forceinline__ int pool_row_of(const ChunkGeom& g, int* error, int b
 }
 // Pool row of position j of the cursor's unit; -1: no row of the unit sees it
 // (it is not read: zeros).
-__device__ __forceinline__ int seen_row(const ChunkParams& p, const Cursor& c, int j) {
+template <typename C>
+__device__ __forceinline__ int seen_row(const ChunkParams& p, int* error, const C& c, int j) {
   if (j >= c.hi || (j < c.lo && j >= p.g.first)) return -1;
-  return pool_row_of(p.g, &p.hdr->error, c.b, j);
+  return pool_row_of(p.g, error, c.b, j);
 }
 // The box of 16 positions from j on, in groups of 8 pool rows from `base` on:
 // 16 positions lie in one block (tiles and blocks start at multiples of 16) and
 // so in 16 pool rows in a row.  A box that no row sees is read from behind the
 // pool, which fills it with zeros.
-__device__ __forceinline__ int box_group(const ChunkParams& p, const Cursor& c, int j) {
+template <typename C>
+__device__ __forceinline__ int box_group(const ChunkParams& p, int* error, const C& c, int j) {
   const int behind = (int)((p.g.total_pages - p.g.base) / 8);
   int x = j;  // the box's first position that is seen, if any, tells its block
   if (x < c.lo && x >= p.g.first) x = c.lo;
   if (x >= j + 16) return behind;
-  const int r = seen_row(p, c, x);
+  const int r = seen_row(p, error, c, x);
   return r < 0 ? behind : (int)((r - (x - j) - p.g.base) / 8);
 }
 

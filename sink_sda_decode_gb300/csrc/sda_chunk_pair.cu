@@ -105,6 +105,7 @@ struct Cfg {
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(256, 128, true, false);
   static_assert(kOCol + 128 * kBlocks <= 512, "TMEM columns");
   static_assert(kOffStage % 16 == 0, "16-byte staging accesses");
+  static_assert(kStages * kKBytes >= 4 * (kFusedSeqs + 1), "chunk_begin's words");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -164,12 +165,22 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // everything above overlaps the plan; global memory only below
   pdl_trigger();
-  const int per = __ldcg(&p.hdr->per), n_tiles = __ldcg(&p.hdr->n_tiles);
-  const long long t0l = (long long)worker * per;
-  const int t0 = (int)min(t0l, (long long)n_tiles);
-  const int nt = (int)min(t0l + per, (long long)n_tiles) - t0;  // the pair's tiles
-  const int u0 = __ldcg(p.cta_unit + worker);
-  const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
+  bool bad;
+  const ChunkStart begin = chunk_begin<TMA ? kTmaThreads : kGatherThreads, 2 * kR, kTile>(
+      p, worker, reinterpret_cast<int*>(smem + C::kOffK), reinterpret_cast<int*>(smem + C::kOffP),
+      &bad);
+  const int nt = begin.nt;  // the pair's tiles
+  int* const error = reinterpret_cast<int*>(reinterpret_cast<char*>(p.hdr) + kErrorWords) + blockIdx.x;
+  if (threadIdx.x == 0) {
+    *error = 0;
+    if (blockIdx.x == 0) {
+      p.hdr->words = gridDim.x;
+      if (p.mode != kPlanned) p.hdr->error = bad ? 2 : 0;
+    }
+  }
+  __syncthreads();
+  const PipeWait wc{abort_flag, error, p.wait_timeout_ns};
+  using Walk = Cursor<2 * kR, kTile>;
 
   if constexpr (!TMA) {
     if (warp >= kQkWarp && warp < kLoadWarp0) setmaxnreg_dec<72>();
@@ -188,23 +199,18 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const uint32_t dst0 = keys ? sK + half * C::kKHalf + (lane & 1) * C::kBox : sV + lane * C::kBox;
       const uint32_t bytes = keys ? C::kKBytes : C::kVBytes;
       const int behind = (int)((p.g.total_pages - p.g.base) / 8);
-      auto box_of = [&](const Cursor& c) {
-        return lane < 4 ? box_group(p, c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + off) : behind;
+      auto box_of = [&](const Walk& c) {
+        return lane < 4 ? box_group(p, error, c, c.start() + off) : behind;
       };
-      Cursor c;  // runs a tile ahead of the copies
-      c.init(p.units, u0, t0, nt);
+      Walk c;  // runs a tile ahead of the copies
+      c.init(p.g, begin);
       int y = behind;
       if (c.left > 0) {
         y = box_of(c);
-        c.next();
+        c.next(p.g);
       }
       for (; g < nt; ++g) {
         const int s = g % KS;
-        int y_next = behind;
-        if (c.left > 0) {
-          y_next = box_of(c);
-          c.next();
-        }
         if (g >= KS) ok = warp_wait(bar(free0 + s), ((g / KS) - 1) & 1, wc);
         if (!ok) break;
         // (CTA 1's bytes may land before CTA 0 has said how many to expect: the
@@ -213,7 +219,10 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         __syncwarp();
         if (lane < 4)
           tma_pair_4d(dst0 + s * bytes, &tmap_kv, 0, 0, half * C::kPanelsH, y, bar0(full0 + s));
-        y = y_next;
+        if (c.left > 0) {  // (after this tile's copies: the table entry is a while coming)
+          y = box_of(c);
+          c.next(p.g);
+        }
       }
     } else {
       // ===================================================== passing on landed stages
@@ -240,28 +249,23 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const int rows = keys ? kKeys / kLoadWarps : kTile / kLoadWarps;
     const int off = keys ? rank * kKeys + v * rows : v * rows;
     const uint4* kv4 = reinterpret_cast<const uint4*>(p.kv);
-    auto slot_of = [&](const Cursor& c) {
-      return lane < rows ? seen_row(p, c, chunk_tile_start(c.i, c.nf, c.lo, kTile) + off + lane) : -1;
+    auto slot_of = [&](const Walk& c) {
+      return lane < rows ? seen_row(p, error, c, c.start() + off + lane) : -1;
     };
-    Cursor c;  // runs two tiles ahead of the copies
-    c.init(p.units, u0, t0, nt);
+    Walk c;  // runs two tiles ahead of the copies
+    c.init(p.g, begin);
     int sl0 = -1, sl1 = -1;
     if (c.left > 0) {
       sl0 = slot_of(c);
-      c.next();
+      c.next(p.g);
     }
     if (c.left > 0) {
       sl1 = slot_of(c);
-      c.next();
+      c.next(p.g);
     }
     bool ok = true;
     for (int g = 0; g < nt; ++g) {
       const int s = g % KS;
-      int sl2 = -1;
-      if (c.left > 0) {
-        sl2 = slot_of(c);
-        c.next();
-      }
       if (g >= KS) ok = warp_wait(bar(free0 + s), ((g / KS) - 1) & 1, wc);
       if (!ok) break;
       auto copy = [&](uint32_t dst, int slot, int ch) {
@@ -293,18 +297,22 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       cp_async_arrive(bar(landed0 + s));  // once this thread's copies have landed
       sl0 = sl1;
-      sl1 = sl2;
+      sl1 = -1;
+      if (c.left > 0) {
+        sl1 = slot_of(c);
+        c.next(p.g);
+      }
     }
     cp_async_wait_all();
   } else if (warp == kQkWarp) {
     // ===================================================== q loads (both), QK MMAs (CTA 0)
-    Cursor c;
-    c.init(p.units, u0, t0, nt);
+    Walk c;
+    c.init(p.g, begin);
     constexpr uint32_t kQBytes = C::kPanels * kR * 128;
     int pieces = 0;
     bool ok = true;
     auto load_q = [&]() {
-      const int row = __ldcg(&p.units[c.u].row0) + rank * kR;
+      const int row = c.row0 + rank * kR;
       if (elect_one()) {
         if (rank == 0) mbar_arrive_expect_tx(bar(kQFull), 2 * kQBytes);
 #pragma unroll
@@ -345,7 +353,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         __syncwarp();
       }
-      c.next();
+      c.next(p.g);
       if (last) {  // q of the next unit, once this unit's MMAs have read q
         ok = warp_wait(bar(kQEmpty), pieces & 1, wc);
         loaded = false;
@@ -362,8 +370,8 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
   } else if (warp == kPvWarp) {
     // ===================================================== decision, PV MMAs (CTA 0)
     if (rank == 0) {
-      Cursor c;
-      c.init(p.units, u0, t0, nt);
+      Walk c;
+      c.init(p.g, begin);
       volatile int* flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag);
       int scaled = 0, pieces = 0, said[2] = {0, 0};
       for (int g = 0; g < nt; ++g) {
@@ -409,7 +417,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
           commit_pair(bar(kVFree0 + ks));
         }
         __syncwarp();
-        c.next();
+        c.next(p.g);
       }
     }
   } else if (warp < kSmWarps) {
@@ -488,9 +496,12 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (lane == 0) arrive_cluster(bar0(kScaled));
     };
 
-    for (int u = u0; g < nt; ++u) {
-      const ChunkUnit un = load_unit(p.units + u);
-      const int i0 = g == 0 ? t0 - un.cum : 0;
+    UnitWalk uw;
+    uw.init(p.g, 2 * kR, begin);
+    while (g < nt) {
+      if (pieces > 0) uw.next(p.g, 2 * kR);
+      const ChunkUnit un = chunk_unit(p.g, 2 * kR, kTile, uw.b, uw.r);
+      const int i0 = g == 0 ? begin.off : 0;
       const int i1 = min(un.ntiles, i0 + nt - g);
       const bool whole = i0 == 0 && i1 == un.ntiles;
       const int h0 = un.h0 + rank * kR, nrows = max(0, min(kR, un.nrows - rank * kR));
@@ -701,9 +712,12 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const float* s_fac = reinterpret_cast<const float*>(smem + C::kOffFac);
     uint8_t* stg = smem + C::kOffStage + q4 * 2048;
     int g = 0, pieces = 0;
-    for (int u = u0; g < nt; ++u) {
-      const ChunkUnit un = load_unit(p.units + u);
-      const int i0 = g == 0 ? t0 - un.cum : 0;
+    UnitWalk uw;
+    uw.init(p.g, 2 * kR, begin);
+    while (g < nt) {
+      if (pieces > 0) uw.next(p.g, 2 * kR);
+      const ChunkUnit un = chunk_unit(p.g, 2 * kR, kTile, uw.b, uw.r);
+      const int i0 = g == 0 ? begin.off : 0;
       const int i1 = min(un.ntiles, i0 + nt - g);
       const bool whole = i0 == 0 && i1 == un.ntiles;
       g += i1 - i0;

@@ -1,12 +1,12 @@
 // sda_chunk_plan.cu -- work plan of the chunk attention, and the merge of
 // units that the plan cut.
 //
-// The plan runs on the device because the lengths live there and the call
-// must stay capturable.  The units' KV tiles form one sequence, which is cut
-// into equal ranges, one per CTA ("split-L"): CTA k owns the tiles
-// [k * per, (k + 1) * per).  A unit that a range boundary cuts becomes
-// pieces, each of which leaves an unnormalised (m, l, acc); the combine
-// kernel merges them.
+// Everything runs on the device because the lengths live there and the call must
+// stay capturable.  The units' KV tiles form one sequence, which is cut into equal
+// ranges, one per worker ("split-L").  A unit that a range boundary cuts becomes
+// pieces, each of which leaves an unnormalised (m, l, acc); the combine kernel
+// merges them.  With few units every CTA of the attention kernel finds its own
+// range (sda_chunk_dev.cuh); this file's plan kernel does it for many.
 #include <cuda_bf16.h>
 
 #include "sda_chunk.cuh"
@@ -16,108 +16,83 @@ namespace sda {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kSmemUnits = 8192;  // units whose tile offsets are also kept in shared memory
-constexpr int kSmemSeqs = 2048;   // sequences whose unit offsets are kept in shared memory
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
-    const ChunkGeom g, int R, int tile, int grid, int u_max, ChunkHeader* __restrict__ hdr,
-    ChunkUnit* __restrict__ units, int* __restrict__ seq_unit, int* __restrict__ cta_unit) {
+    const ChunkGeom g, int R, int tile, int grid, ChunkHeader* __restrict__ hdr,
+    ChunkStart* __restrict__ starts, ChunkUnit* __restrict__ recs, int* __restrict__ seq_unit) {
   __shared__ long long warp_sums[32];
   __shared__ long long s_total;
-  __shared__ int s_cum[kSmemUnits];
-  __shared__ int s_seq[kSmemSeqs + 1];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  // units of every sequence; lengths that make no sense stop the plan
+  // seq_unit[b] = units of the sequences before b; lengths that make no sense stop the plan
   int bad = 0;
   long long U = 0;
-  const long long cap = (long long)g.max_blocks * g.k_per_block;
   for (int b0 = 0; b0 < g.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    long long nu = 0;
+    int nu = 0;
     if (b < g.B) {
-      const int q0 = g.q_indptr[b], q1 = g.q_indptr[b + 1], n = g.kv_len[b];
-      if (q0 < 0 || q1 < q0 || q1 > g.T || n < 0 || n > cap) bad = 1;
-      else nu = ((long long)(q1 - q0) * g.H + R - 1) / R;
+      if (lengths_bad(g, b)) bad = 1;
+      else nu = units_of(g, R, b);
     }
-    long long tot;
     const long long ex = scan_exclusive(nu, warp_sums, &s_total);
-    tot = s_total;
-    if (b < g.B) {
-      const int v = (int)min(U + ex, (long long)u_max);
-      if (b <= kSmemSeqs) s_seq[b] = v;
-      seq_unit[b] = v;
-    }
+    const long long tot = s_total;
+    if (b < g.B) seq_unit[b] = (int)min(U + ex, 0x7fffffffll);
     U += tot;
     __syncthreads();
   }
-  if (U > u_max) bad = 1;
   bad = __syncthreads_or(bad);
   const int nu = bad ? 0 : (int)U;
-  const int* seq = g.B <= kSmemSeqs ? s_seq : seq_unit;
   long long tt = 0;
-  for (int u0 = 0; u0 < nu; u0 += kPlanThreads) {
-    const int u = u0 + tid;
-    ChunkUnit d = {};
-    if (u < nu) {
-      // the last sequence that starts at or before u (sequences without tokens share a start)
-      const int b = last_le(seq, g.B, u);
-      const int q0 = g.q_indptr[b], m = g.q_indptr[b + 1] - q0, n = g.kv_len[b];
-      const long long r0 = (long long)(u - seq[b]) * R;  // row in the sequence's m * H rows
-      const long long rows = (long long)m * g.H - r0;
-      d.row0 = (int)((long long)q0 * g.H + r0);
-      d.nrows = (int)min((long long)R, rows);
-      d.b = b;
-      d.pos0 = n - m + (int)(r0 / g.H);
-      d.h0 = (int)(r0 % g.H);
-      const int p_hi = d.pos0 + (d.h0 + d.nrows - 1) / g.H;
-      d.hi = max(p_hi + 1, 0);
-      d.lo = g.window > 0 ? max(0, (int)max((long long)d.pos0 - g.window + 1, 0ll)) : 0;
-      if (d.hi == 0) d.lo = 0;
-      const int lot = d.lo / tile;
-      d.nf = (min(g.first, lot * tile) + tile - 1) / tile;
-      d.ntiles = d.nf + (d.hi + tile - 1) / tile - lot;
-      if (d.ntiles < 1) d.ntiles = 1;  // rows that see nothing: one tile of masked positions
-    }
-    const long long ex = scan_exclusive(d.ntiles, warp_sums, &s_total);
-    const long long tot = s_total;
-    if (u < nu) {
-      d.cum = (int)min(tt + ex, 0x7fffffffll);
-      units[u] = d;
-      if (u < kSmemUnits) s_cum[u] = d.cum;
-    }
-    tt += tot;
-    __syncthreads();
-  }
-  if (tt > 0x7fffffffll) bad = 1, tt = 0;  // uniform: every thread has the same sum
-  const int TT = bad ? 0 : (int)tt;
-  const int per = TT > 0 ? (int)((TT + (long long)grid - 1) / grid) : 1;
-  for (int k = tid; k <= grid; k += kPlanThreads) {
-    const long long t = (long long)k * per;
-    int u = nu;
-    if (t < TT) {
-      if (nu <= kSmemUnits) {
-        u = last_le(s_cum, nu, (int)t);
-      } else {
-        int lo = 0, hi = nu;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (units[mid].cum <= t) lo = mid;
-          else hi = mid;
-        }
-        u = lo;
+  int per = 1;
+  // first the number of tiles, then the units that hold the range boundaries
+  for (int pass = 0; pass < 2; ++pass) {
+    long long run = 0;
+    for (int u0 = 0; u0 < nu; u0 += kPlanThreads) {
+      const int u = u0 + tid;
+      ChunkUnit d = {};
+      int b = 0;
+      if (u < nu) {
+        b = last_le(seq_unit, g.B, u);  // (sequences without tokens share a start)
+        d = chunk_unit(g, R, tile, b, u - seq_unit[b]);
       }
+      const long long cum = run + scan_exclusive(d.ntiles, warp_sums, &s_total);
+      if (pass == 1 && u < nu) {
+        for (long long k = (cum + per - 1) / per; k * per < cum + d.ntiles; ++k) {
+          starts[k] = ChunkStart{b, u - seq_unit[b], (int)(k * per - cum),
+                                 (int)min((long long)per, tt - k * per)};
+          d.cum = (int)cum;
+          recs[k] = d;
+        }
+      }
+      run += s_total;
+      __syncthreads();
     }
-    cta_unit[k] = u;
+    if (pass == 0) {
+      if (run > 0x7fffffffll) bad = 1;  // uniform: every thread has the same sum
+      tt = bad ? 0 : run;
+      per = tt > 0 ? (int)((tt + grid - 1) / grid) : 1;
+      if (tt == 0) break;
+    }
   }
+  for (int k = tid; k < grid; k += kPlanThreads)
+    if ((long long)k * per >= tt) starts[k] = ChunkStart{0, 0, 0, 0};
   if (tid == 0) {
     hdr->n_units = nu;
-    hdr->n_tiles = TT;
+    hdr->n_tiles = (int)tt;
     hdr->per = per;
-    hdr->ctas = (TT + per - 1) / per;
+    hdr->ctas = (int)((tt + per - 1) / per);
     hdr->error = bad ? 2 : 0;
   }
+}
+
+// The largest of a workspace's error words.
+__global__ void paged_error_kernel(const ChunkHeader* __restrict__ hdr, int32_t* __restrict__ error) {
+  const int* words = reinterpret_cast<const int*>(reinterpret_cast<const char*>(hdr) + kErrorWords);
+  int e = threadIdx.x == 0 ? hdr->error : 0;
+  for (int i = threadIdx.x; i < min(hdr->words, kMaxPlanGrid); i += 32) e = max(e, words[i]);
+  e = __reduce_max_sync(0xffffffffu, e);
+  if (threadIdx.x == 0) *error = e;
 }
 
 // Merge of the pieces of cut units.  Block (x = k - 1, y): boundary k of the
@@ -140,16 +115,15 @@ template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
     const float* __restrict__ attn_sink, int H, int R, __nv_bfloat16* __restrict__ out,
     float* __restrict__ lse, const ChunkHeader* __restrict__ hdr,
-    const ChunkUnit* __restrict__ units, const int* __restrict__ cta_unit,
-    const float2* __restrict__ part_ml, const float* __restrict__ part_o) {
+    const ChunkUnit* __restrict__ recs, const float2* __restrict__ part_ml,
+    const float* __restrict__ part_o) {
   using C = CombineCfg<D>;
   pdl_wait();
   pdl_trigger();
   const int k = blockIdx.x + 1;
-  const int u = cta_unit[k];
-  const int ctas = hdr->ctas, per = hdr->per, n_units = hdr->n_units;
-  if (k >= ctas || u >= n_units) return;
-  const ChunkUnit un = units[u];
+  const int ctas = hdr->ctas, per = hdr->per;
+  const ChunkUnit un = recs[k];  // the unit that holds boundary k
+  if (k >= ctas) return;
   const long long t0 = (long long)k * per;
   if (un.cum >= t0 || un.cum < t0 - per) return;  // not cut here, or cut by an earlier boundary already
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,56 +190,75 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
 
 }  // namespace
 
-ChunkLayout chunk_layout(int B, int T, int H, int D, int num_sms) {
+ChunkLayout chunk_layout(const ChunkGeom& g, int num_sms) {
   ChunkLayout L;
-  const int64_t rows = (int64_t)T * H;
+  const int64_t rows = (int64_t)g.T * g.H;
   // 16-row units where a sequence has at most 16 rows on average (a step of
   // few heads): q then takes a quarter of the shared memory and three KV stages
   // of 64 positions fit, and the rows' masks and stores are not padded to 64.
-  L.R = rows <= (int64_t)16 * B ? 16 : 64;
+  L.R = rows <= (int64_t)16 * g.B ? 16 : 64;
   L.grid = num_sms < kMaxPlanGrid ? num_sms : kMaxPlanGrid;
   // With more than 128 rows a sequence on average, pairs of CTAs take units of 128 rows.
-  L.pair = D >= 256 && rows > (int64_t)128 * B;
+  L.pair = g.D >= 256 && rows > (int64_t)128 * g.B;
   if (L.pair) {
     L.R = 128;
     L.grid /= 2;
   }
-  L.tile = chunk_tile(L.R, D);
-  L.u_max = (int)((rows + L.R - 1) / L.R + B);
-  size_t off = sizeof(ChunkHeader);
-  L.units_off = off;
-  off = align256(off + (size_t)L.u_max * sizeof(ChunkUnit));
+  L.tile = chunk_tile(L.R, g.D);
+  // Where no unit can have more than kWholeTiles tiles (short tables, or a window)
+  // units are not cut: a merge takes as long as about four tiles.
+  constexpr int64_t kWholeTiles = 8;
+  const int64_t S = (int64_t)g.max_blocks * g.k_per_block;
+  int64_t most = (S + L.tile - 1) / L.tile;
+  if (g.window > 0) {
+    const int64_t span = (int64_t)g.window + (L.R - 1) / g.H + 1;
+    const int64_t w = span / L.tile + 2 + ((int64_t)g.first + L.tile - 1) / L.tile;
+    if (w < most) most = w;
+  }
+  L.mode = kPlanned;
+  if (g.B <= kFusedSeqs) {
+    if (most <= kWholeTiles) L.mode = kWhole;
+    else if (rows / L.R + g.B <= kFusedUnits) L.mode = kCut;
+  }
+  size_t off = kErrorWords + kErrorBytes;
+  L.start_off = off;
+  off = align256(off + (size_t)L.grid * sizeof(ChunkStart));
+  L.rec_off = off;
+  off = align256(off + (size_t)L.grid * sizeof(ChunkUnit));
   L.seq_off = off;
-  off = align256(off + (size_t)(B + 1) * 4);
-  L.cta_off = off;
-  off = align256(off + (size_t)(L.grid + 1) * 4);
+  off = align256(off + (size_t)(g.B + 1) * 4);
   L.ml_off = off;
   off = align256(off + (size_t)2 * L.grid * L.R * 8);
   L.o_off = off;
-  off = align256(off + (size_t)2 * L.grid * L.R * D * 4);
+  off = align256(off + (size_t)2 * L.grid * L.R * g.D * 4);
   L.total = off;
   return L;
 }
 
 cudaError_t launch_chunk_plan(const ChunkGeom& g, const ChunkLayout& L, void* ws, cudaStream_t st) {
+  if (L.mode != kPlanned) return cudaSuccess;
   char* base = static_cast<char*>(ws);
-  return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, g, L.R, L.tile, L.grid, L.u_max,
+  return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, g, L.R, L.tile, L.grid,
                     reinterpret_cast<ChunkHeader*>(base),
-                    reinterpret_cast<ChunkUnit*>(base + L.units_off),
-                    reinterpret_cast<int*>(base + L.seq_off),
-                    reinterpret_cast<int*>(base + L.cta_off));
+                    reinterpret_cast<ChunkStart*>(base + L.start_off),
+                    reinterpret_cast<ChunkUnit*>(base + L.rec_off),
+                    reinterpret_cast<int*>(base + L.seq_off));
+}
+
+cudaError_t launch_paged_error(const void* ws, int32_t* error, cudaStream_t st) {
+  paged_error_kernel<<<1, 32, 0, st>>>(static_cast<const ChunkHeader*>(ws), error);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_chunk_combine(const float* attn_sink, const ChunkGeom& g, void* out, float* lse,
                                  const ChunkLayout& L, void* ws, cudaStream_t st) {
   char* base = static_cast<char*>(ws);
-  if (L.grid < 2) return cudaSuccess;
+  if (L.grid < 2 || L.mode == kWhole) return cudaSuccess;
   auto go = [&](auto kernel, int rows) {
     return launch_pdl(kernel, dim3(L.grid - 1, L.R / rows), dim3(kCombineWarps * 32), 0,
                       st, attn_sink, g.H, L.R, static_cast<__nv_bfloat16*>(out), lse,
                       reinterpret_cast<const ChunkHeader*>(base),
-                      reinterpret_cast<const ChunkUnit*>(base + L.units_off),
-                      reinterpret_cast<const int*>(base + L.cta_off),
+                      reinterpret_cast<const ChunkUnit*>(base + L.rec_off),
                       reinterpret_cast<const float2*>(base + L.ml_off),
                       reinterpret_cast<const float*>(base + L.o_off));
   };

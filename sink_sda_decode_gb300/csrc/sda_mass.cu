@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(
     hdr->per = per;
     hdr->ctas = (TT + per - 1) / per;
     hdr->error = bad ? 2 : 0;
+    hdr->words = 0;  // (the next kernel's)
   }
 }
 
@@ -289,7 +290,13 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
   const int t0 = (int)min((long long)worker * per, (long long)n_tiles);
   const int t1 = (int)min((long long)(worker + 1) * per, (long long)n_tiles);
   PieceWalk walk{p.units, t0 < t1 ? __ldcg(p.cta_unit + worker) : 0, t0, t1};
-  const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
+  int* const error = reinterpret_cast<int*>(reinterpret_cast<char*>(p.hdr) + kErrorWords) + blockIdx.x;
+  if (threadIdx.x == 0) {
+    *error = 0;
+    if (blockIdx.x == 0) p.hdr->words = gridDim.x;
+  }
+  __syncthreads();
+  const PipeWait wc{abort_flag, error, p.wait_timeout_ns};
   Piece pc;
 
   if (warp >= kLoadWarp0 && warp < kLoadWarp0 + kLoadWarps) {
@@ -307,7 +314,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tmap_q, const Params p) {
       if (lane < kRows && j < pc.un.n) {
         const int blk = __ldg(p.g.block_table + (size_t)pc.un.b * p.g.max_blocks + j / p.g.k_per_block);
         const long long s = p.g.base + (long long)blk * p.g.k_per_block + j % p.g.k_per_block;
-        if (blk < 0 || s >= p.g.total_pages) atomicExch(&p.hdr->error, 3);
+        if (blk < 0 || s >= p.g.total_pages) atomicExch(error, 3);
         else sl = (int)s;
       }
       if (x > 0) {
@@ -637,14 +644,21 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     if (b1 == B && (b0 < B || tid == 0)) s_tiles[B] = bad ? 0 : run;
   }
-  if (tid == 0 && bad) atomicExch(&p.hdr->error, 2);  // (the call has cleared it)
+  int* const error = reinterpret_cast<int*>(reinterpret_cast<char*>(p.hdr) + kErrorWords) + blockIdx.x;
+  if (tid == 0) {
+    *error = 0;
+    if (blockIdx.x == 0) {
+      p.hdr->words = gridDim.x;
+      p.hdr->error = bad ? 2 : 0;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = s_tiles[B], per = (total + gridDim.x - 1) / (int)gridDim.x;
   const int t0 = min((int)blockIdx.x * per, total), t1 = min(t0 + per, total);
-  const PipeWait wc{abort_flag, &p.hdr->error, p.wait_timeout_ns};
+  const PipeWait wc{abort_flag, error, p.wait_timeout_ns};
   const int b_first = t0 < t1 ? last_le(s_tiles, B, t0) : 0;
   // Calls f on every tile of this CTA that has rows or (all) on every tile.
   auto walk = [&](bool all, auto f) {
@@ -667,7 +681,7 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
       int y = behind;
       const int j = tl.k0 + lane * 16;
       if (lane < 4 && j < tl.n) {
-        const int r = pool_row_of(p.g, &p.hdr->error, tl.b, j);
+        const int r = pool_row_of(p.g, error, tl.b, j);
         if (r >= 0) y = (int)((r - p.g.base) / 8);
       }
       if (g >= KS && !warp_wait(bar(kSkFree0 + s), ((g / KS) - 1) & 1, wc)) return false;
@@ -692,7 +706,7 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
     walk(false, [&](const StepTile& tl) {
       const int s = g % KS;
       const int j = tl.k0 + v * kRows + lane;
-      const int sl = lane < kRows && j < tl.n ? pool_row_of(p.g, &p.hdr->error, tl.b, j) : -1;
+      const int sl = lane < kRows && j < tl.n ? pool_row_of(p.g, error, tl.b, j) : -1;
       if (g >= KS && !warp_wait(bar(kSkFree0 + s), ((g / KS) - 1) & 1, wc)) return false;
 #pragma unroll
       for (int r0 = 0; r0 < kRows; r0 += kRowsPer) {
@@ -900,7 +914,7 @@ MassLayout mass_layout(int B, int64_t S, int num_sms) {
   MassLayout L;
   L.u_max = (int)((S + kKeys - 1) / kKeys * B);
   L.grid = (num_sms < kMaxPlanGrid ? num_sms : kMaxPlanGrid) / 2;  // pairs
-  size_t off = sizeof(ChunkHeader);
+  size_t off = kErrorWords + kErrorBytes;
   L.units_off = off;
   off = align256(off + (size_t)L.u_max * sizeof(MassUnit));
   L.seq_off = off;
@@ -953,8 +967,6 @@ static cudaError_t launch_mass_step(const void* q, const void* kv, const ChunkGe
       (tma && !pipe_map_pool(&tkv, p.kv + g.base * g.D, g.D, (uint64_t)(g.total_pages - g.base) / 8,
                              g.D >= 256 ? g.D / 128 : g.D / 64, 2)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaMemsetAsync(&p.hdr->error, 0, sizeof(int), st);
-  if (e != cudaSuccess) return e;
   return for_step(R, g.D, tma, [&](auto kernel, size_t smem, dim3 threads) {
     return launch_pdl(kernel, dim3(num_sms), threads, smem, st, tq, tkv, p);
   });

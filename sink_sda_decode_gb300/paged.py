@@ -115,7 +115,7 @@ def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torc
     Asynchronous on `stream`.  With out, lse and `workspace` (uint8, at least
     chunk_attention_workspace_size(...) bytes) given the call allocates nothing
     and can be captured into a CUDA graph; calls that may overlap on the GPU
-    need a workspace each.  decode_error_flag(workspace) reads its error word
+    need a workspace each.  paged_error_flag(workspace) reads its error word
     (2: lengths outside the contract, nothing computed; 3: a table entry
     outside the pool).
     """
@@ -151,6 +151,24 @@ def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torc
             lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(dev, stream))
     _lib.check(rc, "sda_chunk_attention")
     return out, lse
+
+
+def paged_error_flag(workspace: torch.Tensor, stream: torch.cuda.Stream | None = None) -> int:
+    """Device error word of the last chunk_attention() or attention_mass() on
+    `workspace` (synchronises): 0 = fine; 1 = a pipeline wait timed out; 2 =
+    q_indptr or kv_len outside their contract (nothing was computed); 3 = a table
+    entry outside the pool (its rows counted as zeros)."""
+    lib = _lib.load()
+    dev = workspace.device
+    with _on(dev):
+        flag = torch.zeros(1, dtype=torch.int32, device=dev)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream(dev))
+        _lib.check(lib.sda_paged_error_flag(workspace.data_ptr(), flag.data_ptr(),
+                                            _stream_of(dev, stream)), "sda_paged_error_flag")
+        if stream is not None:
+            stream.synchronize()
+        return int(flag.item())
 
 
 def attention_mass_workspace_size(B: int, max_blocks: int, k_per_block: int) -> int:
