@@ -632,7 +632,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 f = a / den;
                 lse = (M + log2f(den)) * kLn2;
               }
-              p.lse[un.row0 + r] = lse;
+              // (the sink alone: as it is; a NaN that was seen: NaN)
+              p.lse[un.row0 + r] = l != l ? l : (m == -INFINITY ? (w2 ? sinkB : sinkA) : lse);
             }
           } else {
             p.part_ml[(size_t)slot * R + r] = make_float2(m, l);

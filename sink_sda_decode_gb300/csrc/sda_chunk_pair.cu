@@ -689,7 +689,8 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
               f = a / den;
               lse = (M + log2f(den)) * kLn2;
             }
-            p.lse[un.row0 + rank * kR + st] = lse;
+            // (the sink alone: as it is; a NaN that was seen: NaN)
+            p.lse[un.row0 + rank * kR + st] = lr != lr ? lr : (mr == -INFINITY ? sink : lse);
           }
         } else {
           const int slot = 2 * worker + (i0 == 0 ? 1 : 0);

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
   auto ml_of = [&](int i) {
     return i < np ? part_ml[slot(i) * R + row] : make_float2(-INFINITY, 0.f);
   };
-  const float ms = attn_sink[(un.h0 + row) % H] * kLog2e;
+  const float sink = attn_sink[(un.h0 + row) % H], ms = sink * kLog2e;
   const float2 ml0 = ml_of(lane);  // of the first 32 pieces
   float mk = ml0.x;
   for (int i = lane + 32; i < np; i += 32) mk = fmaxf(mk, ml_of(i).x);
@@ -185,7 +185,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
     const __nv_bfloat162 v = __floats2bfloat162_rn(acc[x] * inv + 0.f, acc[x + 1] * inv + 0.f);
     *reinterpret_cast<__nv_bfloat162*>(out + orow * D + col + x) = v;
   }
-  if (col == 0) lse[orow] = dead ? M * kLn2 : (M + log2f(den)) * kLn2;
+  // (the sink alone: as it is; a NaN that was seen: NaN)
+  if (col == 0)
+    lse[orow] = den != den ? den : mk == -INFINITY ? sink : (dead ? M * kLn2 : (M + log2f(den)) * kLn2);
 }
 
 }  // namespace

@@ -74,13 +74,13 @@ class Case:
     """One random input: pool, block table (distinct blocks in random order), q."""
 
     def __init__(self, seed, m, n, H, D, K, window=0, first=0, base=0, spare=2, device="cuda",
-                 scale=None, lead=0, trail=0, sink=None):
+                 scale=None, lead=0, trail=0, sink=None, columns=0, loud=()):
         g = torch.Generator().manual_seed(seed)
         self.m, self.n, self.K, self.base = list(m), list(n), K, base
         self.B, self.window, self.first = len(m), window, first
         self.scale = scale if scale is not None else D ** -0.5
         blocks = [-(-x // K) for x in n]
-        mb = max(blocks + [1])
+        mb = max(blocks + [1, columns])
         total = sum(blocks) + spare
         perm = torch.randperm(total, generator=g).to(torch.int32)
         table = torch.full((self.B, mb), -7, dtype=torch.int32)  # never read behind kv_len
@@ -89,6 +89,8 @@ class Case:
             table[b, :blocks[b]] = perm[at:at + blocks[b]]
             at += blocks[b]
         self.pool = torch.randn(base + total * K, D, generator=g).to(torch.bfloat16)
+        for b, j, factor in loud:  # rows whose scores stand out
+            self.pool[rows_of(table.numpy()[b], n[b], K, base)[j]] *= factor
         self.q_indptr_l = [lead + x for x in np.cumsum([0] + list(m)).tolist()]
         T = self.q_indptr_l[-1] + trail
         self.q = torch.randn(T, H, D, generator=g).to(torch.bfloat16)
