@@ -38,7 +38,7 @@ struct alignas(16) ChunkUnit {
   int hi;       // positions from hi on are visible to no row
   int nf;       // KV tiles of the first positions (those below lo's tile)
   int ntiles;   // KV tiles: tiles 0..nf-1, then from the one that holds lo on (>= 1)
-  int cum;      // KV tiles of all earlier units
+  int off;      // in a worker's record: its first tile of this unit
   int pad0, pad1;
 };
 static_assert(sizeof(ChunkUnit) == 48, "three 16-byte words");
@@ -54,8 +54,8 @@ __host__ __device__ inline int chunk_tile_start(int i, int nf, int lo, int tile)
 struct ChunkHeader {
   int n_units;
   int n_tiles;  // KV tiles of all units
-  int per;      // tiles per worker: worker k owns tiles [k * per, min((k + 1) * per, n_tiles))
-  int ctas;     // workers with tiles
+  int per;      // attention mass: row tiles per worker
+  int ctas;     // attention mass: workers with row tiles
   int error;    // 2 = bad lengths (nothing computed)
   int words;    // error words of this call (1 = a wait timed out, 3 = bad table entry)
   int pad[58];
@@ -67,11 +67,17 @@ constexpr size_t kErrorWords = 256, kErrorBytes = 4 * kMaxPlanGrid;  // offset a
 struct alignas(16) ChunkStart {
   int b, r;  // sequence, and unit of it
   int off;   // first tile of that unit
-  int nt;    // tiles in all
+  int nt;    // tiles in all (in the plan's list: tiles before it)
 };
 
+// The workers' ranges are equal in cost: a unit costs its tiles and this much for
+// its beginning and end (about 5500 cycles on a pair, tiles of 1650).  Equal numbers
+// of tiles left the workers that had many short units far behind (12 sequences of 1
+// to 300 tokens: the median worker was done after 340 us, the last after 487).
+constexpr int kUnitCost = 3;
+
 // How the tiles are shared out.
-//   kPlanned  equal numbers of tiles, by a kernel before
+//   kPlanned  ranges of equal cost, by a kernel before
 //   kCut      the same, but every CTA finds its own beginning (few units)
 //   kWhole    whole units, every CTA its share: no merge of pieces is launched
 enum ChunkMode : int { kPlanned = 0, kCut = 1, kWhole = 2 };
@@ -135,7 +141,7 @@ __device__ __forceinline__ bool lengths_bad(const ChunkGeom& g, int b) {
   const int q0 = __ldg(g.q_indptr + b), q1 = __ldg(g.q_indptr + b + 1), n = __ldg(g.kv_len + b);
   return q0 < 0 || q1 < q0 || q1 > g.T || n < 0 || n > (long long)g.max_blocks * g.k_per_block;
 }
-// Unit r of sequence b (cum is left 0).
+// Unit r of sequence b (off is left 0).
 __device__ __forceinline__ ChunkUnit chunk_unit(const ChunkGeom& g, int R, int tile, int b, int r) {
   const int q0 = __ldg(g.q_indptr + b), m = __ldg(g.q_indptr + b + 1) - q0, n = __ldg(g.kv_len + b);
   const int r0 = r * R;  // row in the sequence's m * H rows
@@ -154,7 +160,7 @@ __device__ __forceinline__ ChunkUnit chunk_unit(const ChunkGeom& g, int R, int t
   d.nf = (min(g.first, lot * tile) + tile - 1) / tile;
   // rows that see nothing: one tile of masked positions
   d.ntiles = max(d.nf + (d.hi + tile - 1) / tile - lot, 1);
-  d.cum = d.pad0 = d.pad1 = 0;
+  d.off = d.pad0 = d.pad1 = 0;
   return d;
 }
 

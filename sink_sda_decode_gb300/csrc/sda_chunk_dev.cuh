@@ -18,7 +18,7 @@ struct ChunkParams {
   float* lse;
   ChunkHeader* hdr;
   ChunkStart* starts;
-  ChunkUnit* recs;  // recs[k]: the unit that holds tile k * per, for the combine
+  ChunkUnit* recs;  // recs[k]: the unit that worker k begins in, for the combine
   int mode, workers;
   float2* part_ml;
   float* part_o;
@@ -94,12 +94,12 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
   *bad = false;
   if (p.mode == kPlanned) {
     const int4 v = __ldcg(reinterpret_cast<const int4*>(p.starts + worker));
-    return ChunkStart{v.x, v.y, v.z, v.w};
+    return ChunkStart{v.x, v.y, v.z, __ldcg(&p.starts[worker + 1].nt) - v.w};
   }
   constexpr int kW = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long* sums = reinterpret_cast<long long*>(scratch);  // [kW]
-  int* found = scratch + 2 * kW;                             // [4]
+  int* found = scratch + 2 * kW;                             // [5]
   // exclusive prefix of one value per thread, and the total
   auto scan = [&](long long v, long long* total) {
     long long x = v;
@@ -169,36 +169,45 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
         if (u + 1 < u1) w.next(g, R);
       }
     }
-    long long cum = scan(nt, &tt);
+    const long long tiles = scan(nt, &tt);  // of the units before this stretch
     if (tt > 0x7fffffffll) {
       *bad = true;
       return st;
     }
-    const int per = tt > 0 ? (int)((tt + p.workers - 1) / p.workers) : 1;
-    const long long t0 = (long long)worker * per;
-    if (t0 >= cum && t0 < cum + nt) {  // this thread's stretch holds the first tile
+    const long long cost = tt + U * kUnitCost;
+    const long long per = cost > 0 ? (cost + p.workers - 1) / p.workers : 1;
+    const long long mine0 = tiles + (long long)u0 * kUnitCost;
+    const long long mine1 = mine0 + nt + (long long)(u1 - u0) * kUnitCost;
+    // this worker's beginning and the next one's, where they lie in this stretch
+    for (int e = 0; e < 2; ++e) {
+      const long long at_c = (worker + e) * per;
+      if (at_c < mine0 || at_c >= mine1) continue;
       from();
+      long long t = tiles, c = mine0;
       for (;;) {
         ChunkUnit d = chunk_unit(g, R, TILE, w.b, w.r);
-        if (t0 < cum + d.ntiles) {
-          found[0] = w.b;
-          found[1] = w.r;
-          found[2] = (int)(t0 - cum);
-          d.cum = (int)cum;
-          p.recs[worker] = d;
+        if (at_c < c + d.ntiles + kUnitCost) {
+          d.off = (int)max(at_c - c - kUnitCost, 0ll);
+          if (e == 0) {
+            found[0] = w.b;
+            found[1] = w.r;
+            found[2] = d.off;
+            p.recs[worker] = d;
+          }
+          found[3 + e] = (int)(t + d.off);
           break;
         }
-        cum += d.ntiles;
+        t += d.ntiles;
+        c += d.ntiles + kUnitCost;
         w.next(g, R);
       }
     }
-    if (worker == 0 && tid == 0) {
-      p.hdr->n_tiles = (int)tt;
-      p.hdr->per = per;
-      p.hdr->ctas = (int)((tt + per - 1) / per);
-    }
+    if (tid == 0 && worker * per >= cost) p.recs[worker] = ChunkUnit{-1};
     __syncthreads();
-    if (t0 < tt) st = ChunkStart{found[0], found[1], found[2], (int)min((long long)per, tt - t0)};
+    if (worker * per < cost) {
+      const int end = (worker + 1) * per < cost ? found[4] : (int)tt;
+      st = ChunkStart{found[0], found[1], found[2], end - found[3]};
+    }
   }
   ptx::fence_proxy_async_smem();  // the tiles will be written here through the async proxy
   __syncthreads();

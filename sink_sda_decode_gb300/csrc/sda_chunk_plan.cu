@@ -2,8 +2,8 @@
 // units that the plan cut.
 //
 // Everything runs on the device because the lengths live there and the call must
-// stay capturable.  The units' KV tiles form one sequence, which is cut into equal
-// ranges, one per worker ("split-L").  A unit that a range boundary cuts becomes
+// stay capturable.  The units' KV tiles form one sequence, which is cut into ranges
+// of equal cost, one per worker ("split-L").  A unit that a range boundary cuts becomes
 // pieces, each of which leaves an unnormalised (m, l, acc); the combine kernel
 // merges them.  With few units every CTA of the attention kernel finds its own
 // range (sda_chunk_dev.cuh); this file's plan kernel does it for many.
@@ -43,11 +43,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
   }
   bad = __syncthreads_or(bad);
   const int nu = bad ? 0 : (int)U;
-  long long tt = 0;
-  int per = 1;
-  // first the number of tiles, then the units that hold the range boundaries
+  long long tt = 0, cost = 0;  // tiles, and cost, of all units
+  long long per = 1;
+  // first the sums, then the units that hold the range boundaries
   for (int pass = 0; pass < 2; ++pass) {
-    long long run = 0;
+    long long run_t = 0, run_c = 0;
     for (int u0 = 0; u0 < nu; u0 += kPlanThreads) {
       const int u = u0 + tid;
       ChunkUnit d = {};
@@ -56,32 +56,37 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
         b = last_le(seq_unit, g.B, u);  // (sequences without tokens share a start)
         d = chunk_unit(g, R, tile, b, u - seq_unit[b]);
       }
-      const long long cum = run + scan_exclusive(d.ntiles, warp_sums, &s_total);
+      const long long before = run_t + scan_exclusive(d.ntiles, warp_sums, &s_total);
+      const long long units = min(kPlanThreads, nu - u0);
       if (pass == 1 && u < nu) {
-        for (long long k = (cum + per - 1) / per; k * per < cum + d.ntiles; ++k) {
-          starts[k] = ChunkStart{b, u - seq_unit[b], (int)(k * per - cum),
-                                 (int)min((long long)per, tt - k * per)};
-          d.cum = (int)cum;
+        const long long c0 = before + (long long)u * kUnitCost, c1 = c0 + d.ntiles + kUnitCost;
+        for (long long k = (c0 + per - 1) / per; k * per < c1 && k < grid; ++k) {
+          d.off = (int)max(k * per - c0 - kUnitCost, 0ll);
+          starts[k] = ChunkStart{b, u - seq_unit[b], d.off, (int)(before + d.off)};
           recs[k] = d;
         }
       }
-      run += s_total;
+      run_t += s_total;
+      run_c += s_total + units * kUnitCost;
       __syncthreads();
     }
     if (pass == 0) {
-      if (run > 0x7fffffffll) bad = 1;  // uniform: every thread has the same sum
-      tt = bad ? 0 : run;
-      per = tt > 0 ? (int)((tt + grid - 1) / grid) : 1;
+      if (run_t > 0x7fffffffll) bad = 1;  // uniform: every thread has the same sum
+      tt = bad ? 0 : run_t;
+      cost = bad ? 0 : run_c;
+      per = cost > 0 ? (cost + grid - 1) / grid : 1;
       if (tt == 0) break;
     }
   }
-  for (int k = tid; k < grid; k += kPlanThreads)
-    if ((long long)k * per >= tt) starts[k] = ChunkStart{0, 0, 0, 0};
+  for (int k = tid; k <= grid; k += kPlanThreads) {
+    if (k == grid || k * per >= cost) {
+      starts[k] = ChunkStart{0, 0, 0, (int)tt};
+      if (k < grid) recs[k] = ChunkUnit{-1};
+    }
+  }
   if (tid == 0) {
     hdr->n_units = nu;
     hdr->n_tiles = (int)tt;
-    hdr->per = per;
-    hdr->ctas = (int)((tt + per - 1) / per);
     hdr->error = bad ? 2 : 0;
   }
 }
@@ -95,13 +100,13 @@ __global__ void paged_error_kernel(const ChunkHeader* __restrict__ hdr, int32_t*
   if (threadIdx.x == 0) *error = e;
 }
 
-// Merge of the pieces of cut units.  Block (x = k - 1, y): boundary k of the
-// tile ranges; it acts if boundary k is the first to cut its unit.  A warp takes
-// 128 columns (all of D below that) of one row; its lanes hold the pieces' (m, l)
-// and weights, 32 at a time, and eight pieces' partials are in flight together:
-// a unit cut into 19 pieces (8 sequences of 65536 positions) is bound by the
-// latency of those loads.  Piece 0 lies in slot 2 (k - 1) + 1 (the unit starts in
-// CTA k - 1's range), piece i in slot 2 (k - 1 + i).
+// Merge of the pieces of cut units.  Block (x = k - 1, y): the beginning of worker
+// k's range; it acts if that is the first to cut its unit.  A warp takes 128 columns
+// (all of D below that) of one row; its lanes hold the pieces' (m, l) and weights,
+// 32 at a time, and eight pieces' partials are in flight together: a unit cut into 19
+// pieces (8 sequences of 65536 positions) is bound by the latency of those loads.
+// Piece 0 lies in slot 2 (k - 1) + 1 (the unit starts in worker k - 1's range), piece
+// i in slot 2 (k - 1 + i).
 constexpr int kCombineWarps = 8;
 
 template <int D>
@@ -114,23 +119,29 @@ struct CombineCfg {
 template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
     const float* __restrict__ attn_sink, int H, int R, __nv_bfloat16* __restrict__ out,
-    float* __restrict__ lse, const ChunkHeader* __restrict__ hdr,
-    const ChunkUnit* __restrict__ recs, const float2* __restrict__ part_ml,
+    float* __restrict__ lse, int workers, const ChunkUnit* __restrict__ recs, const float2* __restrict__ part_ml,
     const float* __restrict__ part_o) {
   using C = CombineCfg<D>;
   pdl_wait();
   pdl_trigger();
   const int k = blockIdx.x + 1;
-  const int ctas = hdr->ctas, per = hdr->per;
-  const ChunkUnit un = recs[k];  // the unit that holds boundary k
-  if (k >= ctas) return;
-  const long long t0 = (long long)k * per;
-  if (un.cum >= t0 || un.cum < t0 - per) return;  // not cut here, or cut by an earlier boundary already
+  const ChunkUnit un = recs[k];  // the unit that worker k begins in
+  const int row_before = recs[k - 1].row0, off_before = recs[k - 1].off;
+  // not cut here, or cut by an earlier beginning already
+  if (un.off == 0 || un.row0 < 0 || (row_before == un.row0 && off_before > 0)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y * C::kRows + warp / C::kWarpsRow;
   const int col = (warp % C::kWarpsRow) * 128 + lane * C::kPer;
   if (row >= un.nrows) return;
-  const int np = 1 + (int)(((long long)un.cum + un.ntiles - t0 + per - 1) / per);
+  // the pieces: piece 0, and those of the workers from k on that begin in this unit
+  int np = 1;
+  for (int k0 = k;; k0 += 32) {
+    const int x = k0 + lane;
+    const bool in = x < workers && recs[x].row0 == un.row0 && recs[x].off > 0;
+    const uint32_t not_in = ~__ballot_sync(0xffffffffu, in);
+    np += not_in ? __ffs(not_in) - 1 : 32;
+    if (not_in) break;
+  }
   auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + i)); };
   auto ml_of = [&](int i) {
     return i < np ? part_ml[slot(i) * R + row] : make_float2(-INFINITY, 0.f);
@@ -224,7 +235,7 @@ ChunkLayout chunk_layout(const ChunkGeom& g, int num_sms) {
   }
   size_t off = kErrorWords + kErrorBytes;
   L.start_off = off;
-  off = align256(off + (size_t)L.grid * sizeof(ChunkStart));
+  off = align256(off + (size_t)(L.grid + 1) * sizeof(ChunkStart));
   L.rec_off = off;
   off = align256(off + (size_t)L.grid * sizeof(ChunkUnit));
   L.seq_off = off;
@@ -259,8 +270,7 @@ cudaError_t launch_chunk_combine(const float* attn_sink, const ChunkGeom& g, voi
   auto go = [&](auto kernel, int rows) {
     return launch_pdl(kernel, dim3(L.grid - 1, L.R / rows), dim3(kCombineWarps * 32), 0,
                       st, attn_sink, g.H, L.R, static_cast<__nv_bfloat16*>(out), lse,
-                      reinterpret_cast<const ChunkHeader*>(base),
-                      reinterpret_cast<const ChunkUnit*>(base + L.rec_off),
+                      L.grid, reinterpret_cast<const ChunkUnit*>(base + L.rec_off),
                       reinterpret_cast<const float2*>(base + L.ml_off),
                       reinterpret_cast<const float*>(base + L.o_off));
   };
