@@ -70,11 +70,12 @@ struct alignas(16) ChunkStart {
   int nt;    // tiles in all (in the plan's list: tiles before it)
 };
 
-// The workers' ranges are equal in cost: a unit costs its tiles and this much for
-// its beginning and end (about 5500 cycles on a pair, tiles of 1650).  Equal numbers
-// of tiles left the workers that had many short units far behind (12 sequences of 1
-// to 300 tokens: the median worker was done after 340 us, the last after 487).
-constexpr int kUnitCost = 3;
+// The workers' ranges are equal in cost: a unit of R rows costs its tiles and this
+// many more for its beginning and end (on a pair about 5500 cycles, at 1650 a tile).
+// Equal numbers of tiles left the workers that had many short units far behind: 12
+// sequences of 1 to 300 tokens over 300 to 6000 positions took 521 us (the median
+// worker was done after 340), and take 420.
+constexpr int unit_cost(int R) { return R == 128 ? 3 : 1; }
 
 // How the tiles are shared out.
 //   kPlanned  ranges of equal cost, by a kernel before
@@ -90,10 +91,10 @@ struct ChunkLayout {
   ChunkMode mode;
 };
 // Positions per KV tile (a multiple of 16).  With 64 rows of q at D = 512 two
-// stages of 64 positions fit beside q, or three of 48: the tensor pipe needs
-// 7 % more cycles a position with 48 (it reads q more often), but a tile's load,
-// scores, softmax and PV take longer than two tiles' MMAs, and three in flight
-// keep the pipe busier (attend of a 2048-token chunk over 8192 positions).
+// stages of 64 positions fit beside q in one CTA, or three of 48.  A step is bound by
+// the time from a stage's load to its release (load, scores, softmax, PV), so three
+// in flight win although their MMAs take 7 % more cycles a position: one token of 64
+// heads over 8 caches of up to 65536 positions, 87 against 91 us.
 constexpr int chunk_tile(int R, int D) { return R == 64 && D == 512 ? 48 : 64; }
 // Whether KV tiles can be loaded as boxes of 16 rows: blocks hold a multiple of
 // 16 rows, and the pool from `base` on whole groups of 8 (the tensor map counts

@@ -174,10 +174,10 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
       *bad = true;
       return st;
     }
-    const long long cost = tt + U * kUnitCost;
+    const long long cost = tt + U * unit_cost(R);
     const long long per = cost > 0 ? (cost + p.workers - 1) / p.workers : 1;
-    const long long mine0 = tiles + (long long)u0 * kUnitCost;
-    const long long mine1 = mine0 + nt + (long long)(u1 - u0) * kUnitCost;
+    const long long mine0 = tiles + (long long)u0 * unit_cost(R);
+    const long long mine1 = mine0 + nt + (long long)(u1 - u0) * unit_cost(R);
     // this worker's beginning and the next one's, where they lie in this stretch
     for (int e = 0; e < 2; ++e) {
       const long long at_c = (worker + e) * per;
@@ -186,8 +186,8 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
       long long t = tiles, c = mine0;
       for (;;) {
         ChunkUnit d = chunk_unit(g, R, TILE, w.b, w.r);
-        if (at_c < c + d.ntiles + kUnitCost) {
-          d.off = (int)max(at_c - c - kUnitCost, 0ll);
+        if (at_c < c + d.ntiles + unit_cost(R)) {
+          d.off = (int)max(at_c - c - unit_cost(R), 0ll);
           if (e == 0) {
             found[0] = w.b;
             found[1] = w.r;
@@ -198,7 +198,7 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
           break;
         }
         t += d.ntiles;
-        c += d.ntiles + kUnitCost;
+        c += d.ntiles + unit_cost(R);
         w.next(g, R);
       }
     }

@@ -59,15 +59,15 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(
       const long long before = run_t + scan_exclusive(d.ntiles, warp_sums, &s_total);
       const long long units = min(kPlanThreads, nu - u0);
       if (pass == 1 && u < nu) {
-        const long long c0 = before + (long long)u * kUnitCost, c1 = c0 + d.ntiles + kUnitCost;
+        const long long c0 = before + (long long)u * unit_cost(R), c1 = c0 + d.ntiles + unit_cost(R);
         for (long long k = (c0 + per - 1) / per; k * per < c1 && k < grid; ++k) {
-          d.off = (int)max(k * per - c0 - kUnitCost, 0ll);
+          d.off = (int)max(k * per - c0 - unit_cost(R), 0ll);
           starts[k] = ChunkStart{b, u - seq_unit[b], d.off, (int)(before + d.off)};
           recs[k] = d;
         }
       }
       run_t += s_total;
-      run_c += s_total + units * kUnitCost;
+      run_c += s_total + units * unit_cost(R);
       __syncthreads();
     }
     if (pass == 0) {
