@@ -6,18 +6,21 @@
 // last `recent` positions and, of those between, the k - first - recent with
 // the largest weight (-0 equal to +0, NaN below -inf, equal weights by
 // increasing position).  Weights map to 32-bit keys that preserve that order,
-// so the k-th key is found by an exact radix select (digits of 11, 11 and 10
-// bits, stopping once the digit's bin is kept whole); one ordered pass then
-// gives every position its rank among the kept or the freed ones.
+// so the k-th key is found by an exact radix select (stopping once the digit's
+// bin is kept whole); one ordered pass then gives every position its rank among
+// the kept or the freed ones.
 //
 // evict_cluster_kernel: one CTA (tables of up to 4096 columns) or a cluster of 8
 // or 6 a sequence, each CTA with its share of the positions in shared memory, so that
 // scores and slots are read once; the digits' histograms and the kept counts of
 // the CTAs are put together through distributed shared memory, and each warp
 // writes the kept and the freed of 32 positions in a row at a time.  16 sequences
-// of up to 131072 positions cut to 4096: 21 us, against 179 with one CTA a
+// of 10482 to 131072 positions cut to 4096 take 35 us, against 176 with one CTA a
 // sequence that reads its row again for every digit (evict_stream_kernel, left for
-// tables whose share does not fit).
+// tables whose share does not fit).  The bytes would take 2 us; what bounds it is the
+// chain of the longest sequence: about 3 us to load its share, then 5 us for each of
+// three digits (histogram, two cluster barriers with the sums between them) and 8 us
+// to count and to write.
 //
 // In-place calls are safe: everything is read before anything is written (the
 // cluster kernel), or a position before anything at or before it (the stream
@@ -105,8 +108,8 @@ __global__ void __launch_bounds__(kThreads) evict_indptr_kernel(const EvictArgs 
 
 // Rows of up to kOneCta columns take one CTA, longer ones a cluster of 8 or 6: 14
 // clusters of 8 run at once on a GB300, or 24 of 6, so that more than 14 sequences
-// take clusters of 6 where their share fits (16 sequences of up to 131072: 31 us in
-// clusters of 6, 42 us in two waves of clusters of 8).
+// take clusters of 6 where their share fits (16 sequences of up to 131072: 39 us in
+// clusters of 6, 42 us in two waves of clusters of 8, before the last steps).
 constexpr int kOneCta = 4096, kFused = 4096, kClusters8 = 14;
 constexpr size_t kMaxSmem = 200 * 1024;
 static_assert(kMaxSmem / 8 / 32 <= kBins / 2, "the bits of a share's rows of 32 fit the histogram");
