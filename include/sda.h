@@ -463,8 +463,8 @@ sda_status sda_qk_norm_rope_swa_store_fp8(const void* q, const void* kv, const v
  *               and lse outside [q_indptr[0], q_indptr[B]) are not written
  *   kv_len      [B] int32 in [0, max_blocks * k_per_block]
  *   attn_sink   [H] fp32 sink logits (-inf: no sink)
- *   out         [T, H, D] bf16, 16-byte aligned, overlapping neither q nor the
- *               pool; lse [T, H] fp32
+ *   out         [T, H, D] bf16, 16-byte aligned; lse [T, H] fp32; they overlap
+ *               neither each other nor anything that is read
  * The device error word (sda_paged_error_flag on the workspace): 2 = q_indptr
  * or kv_len broke the contract (nothing computed); 3 = a table entry pointed
  * outside the pool (that row counts as zeros, outputs that see it are
@@ -499,7 +499,8 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
  * bits.
  *   lse   [T, H] fp32
  *   prev  [B, S] fp32, S = max_blocks * k_per_block, or NULL for zeros
- *   out   [B, S] fp32; may be prev itself, must not partly overlap it
+ *   out   [B, S] fp32; may be prev itself, must not otherwise overlap what is
+ *         read
  * T may be 0 (q and lse may then be NULL): out = decay * prev.  Error word and
  * workspace as sda_chunk_attention (word 2: lengths outside the contract, out
  * without any weight added).  The timing hook brackets all of its launches.
@@ -531,7 +532,7 @@ sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t tot
  * out_stride >= min(stride, budget); freed_capacity >= B * max(stride -
  * budget, 0), at most 2^31 - 1.  out_scores / out_table / out_len may be
  * scores / slot_table / kv_len themselves (with out_stride = stride) and must
- * not otherwise overlap what is read.  *status (device int32, overwritten):
+ * not otherwise overlap what is read; no two outputs overlap.  *status (device int32, overwritten):
  * bits 1 (bad length), 8 (a NaN competed).  Graph-capturable, no workspace.
  */
 sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64_t stride,

@@ -951,7 +951,7 @@ static sda_status chunk_geometry_ok(const ChunkGeom& g) {
 
 static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
+  return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
 sda_status sda_paged_error_flag(const void* workspace, int32_t* device_flag, void* stream) {
@@ -1001,10 +1001,11 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
                           static_cast<const void*>(block_table), static_cast<const void*>(attn_sink),
                           static_cast<const void*>(lse)})
     if (!aligned(ptr, 4)) return SDA_ERR_INVALID_ARG;
-  // a unit's out is written while other units still read q and the pool
-  const size_t rows = static_cast<size_t>(T) * H;
-  if (overlaps(q, rows * D * 2, out, rows * D * 2) ||
-      overlaps(unified_kv, static_cast<size_t>(total_pages) * D * 2, out, rows * D * 2))
+  // a unit's out and lse are written while other units still read q and the pool
+  const size_t rows = static_cast<size_t>(T) * H, on = rows * D * 2, ln = rows * 4;
+  const size_t pn = static_cast<size_t>(total_pages) * D * 2;
+  if (overlaps(q, on, out, on) || overlaps(unified_kv, pn, out, on) || overlaps(q, on, lse, ln) ||
+      overlaps(unified_kv, pn, lse, ln) || overlaps(out, on, lse, ln))
     return SDA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return SDA_ERR_WORKSPACE;
   DeviceCaps caps;
@@ -1075,9 +1076,13 @@ sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t tot
                           static_cast<const void*>(block_table), static_cast<const void*>(lse),
                           static_cast<const void*>(prev), static_cast<const void*>(out)})
     if (!aligned(ptr, 4)) return SDA_ERR_INVALID_ARG;
-  // out is prev itself or apart from everything that is read
-  const size_t nb = static_cast<size_t>(B) * S * 4;
+  // out is prev itself or apart from it, and apart from what all CTAs read
+  const size_t nb = static_cast<size_t>(B) * S * 4, rows = static_cast<size_t>(T) * H;
   if (prev && prev != out && overlaps(prev, nb, out, nb)) return SDA_ERR_INVALID_ARG;
+  if (overlaps(q, rows * D * 2, out, nb) || overlaps(lse, rows * 4, out, nb) ||
+      overlaps(unified_kv, static_cast<size_t>(total_pages) * D * 2, out, nb) ||
+      overlaps(block_table, static_cast<size_t>(B) * max_blocks * 4, out, nb))
+    return SDA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return SDA_ERR_WORKSPACE;
   DeviceCaps caps;
   cudaError_t e = device_caps(&caps);
@@ -1119,15 +1124,29 @@ sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64
                          freed_indptr, status};
   for (const void* ptr : words)
     if (!aligned(ptr, 4)) return SDA_ERR_INVALID_ARG;
-  // in place (same array, same row length) or apart
+  // what is written is in place (the same array with the same row length) or apart from
+  // what is read, and apart from what else is written
+  struct Span {
+    const void* p;
+    size_t n;
+    const void* place;  // the input that it may be
+  };
   const size_t in = static_cast<size_t>(B) * stride * 4, on = static_cast<size_t>(B) * out_stride * 4;
-  const bool same = stride == out_stride;
-  if (!(same && scores == out_scores) && overlaps(scores, in, out_scores, on))
-    return SDA_ERR_INVALID_ARG;
-  if (!(same && slot_table == out_table) && overlaps(slot_table, in, out_table, on))
-    return SDA_ERR_INVALID_ARG;
   const size_t bn = static_cast<size_t>(B) * 4;
-  if (out_len != kv_len && overlaps(kv_len, bn, out_len, bn)) return SDA_ERR_INVALID_ARG;
+  const bool same = stride == out_stride;
+  const Span reads[] = {{scores, in, nullptr}, {slot_table, in, nullptr}, {kv_len, bn, nullptr}};
+  const Span writes[] = {{out_scores, on, same ? scores : nullptr},
+                         {out_table, on, same ? slot_table : nullptr},
+                         {out_len, bn, kv_len},
+                         {freed_slots, static_cast<size_t>(freed_capacity) * 4, nullptr},
+                         {freed_indptr, bn + 4, nullptr},
+                         {status, 4, nullptr}};
+  for (const Span& w : writes) {
+    for (const Span& r : reads)
+      if (!(w.p == r.p && w.place == r.p) && overlaps(w.p, w.n, r.p, r.n)) return SDA_ERR_INVALID_ARG;
+    for (const Span& o : writes)
+      if (&o != &w && overlaps(w.p, w.n, o.p, o.n)) return SDA_ERR_INVALID_ARG;
+  }
   const EvictArgs a{scores,  slot_table,  stride,         kv_len,       B,     budget, first, recent,
                     out_scores, out_table, out_stride, out_len, freed_slots, freed_capacity,
                     freed_indptr, status};

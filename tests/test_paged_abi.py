@@ -106,6 +106,29 @@ def test_evict_slots_refuses(lib, bad):
     assert evict(lib, **bad) == INVALID
 
 
+@pytest.mark.parametrize("lse", [1 << 20, (1 << 20) + 3 * 16 * 1024 - 4, 1 << 24, 1 << 22, (1 << 22) - 188])
+def test_lse_of_chunk_attention_is_apart(lib, lse):
+    """From q, the pool and out (3 x 16 rows)."""
+    assert attend(lib, lse=lse) == INVALID
+    assert attend(lib, lse=(1 << 22) - 192, ws=128) == WORKSPACE  # ends where out begins
+
+
+@pytest.mark.parametrize("bad", [dict(out=1 << 20), dict(out=(1 << 20) - 508), dict(out=(1 << 24) + 16),
+                                 dict(lse=(1 << 22) + 64), dict(table=(1 << 22) - 28)])
+def test_out_of_attention_mass_is_apart(lib, bad):
+    assert mass(lib, **bad) == INVALID
+    assert mass(lib, prev=1 << 22, ws=64) == WORKSPACE  # in place
+
+
+@pytest.mark.parametrize("bad", [
+    dict(freed=1 << 20), dict(freed=(1 << 21) + 64), dict(freed=(1 << 22) + 4), dict(out_table=1 << 20),
+    dict(out_scores=1 << 21), dict(out_table=1 << 22), dict(out_len=(1 << 20) + 8), dict(indptr=12),
+    dict(status=20), dict(status=64), dict(status=256 + 16), dict(indptr=60), dict(out_stride=700, out_table=1 << 20),
+    dict(out_stride=700, out_scores=1 << 21)])
+def test_results_of_evict_slots_are_apart(lib, bad):
+    assert evict(lib, **bad) == INVALID
+
+
 def test_python_refuses_sizes_that_do_not_fit():
     with pytest.raises(ValueError):
         sda.chunk_attention_workspace_size(2 ** 31, 1, 1, 64)
