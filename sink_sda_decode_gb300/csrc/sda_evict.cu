@@ -490,7 +490,11 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   const bool fused = staged && a.B > 0 && a.B <= kFused && a.out_len != a.kv_len;
   if (!fused) {
     const cudaError_t e = launch_pdl(evict_indptr_kernel, dim3(1), dim3(kThreads), 0, st, a);
-    if (e != cudaSuccess || a.B == 0) return e;
+    if (e != cudaSuccess) return e;
+    if (a.B == 0)  // nothing was freed: the whole list is its unused tail (-1 is all ones)
+      return a.freed_capacity > 0
+                 ? cudaMemsetAsync(a.freed, 0xff, (size_t)a.freed_capacity * sizeof(int32_t), st)
+                 : cudaSuccess;
   } else {
     const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), st);
     if (e != cudaSuccess) return e;

@@ -71,3 +71,13 @@ def test_many_sequences(B, S, budget):
     r = sda.evict_slots(s, t, torch.tensor(lens, dtype=torch.int32).cuda(), budget, first=4, recent=9)
     torch.cuda.synchronize()
     same(r, evict(s, t, lens, budget, 4, 9, budget), budget)
+
+
+def test_no_sequences():
+    """The freed list holds -1 behind its end, also when that is all of it."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = sda.Evicted(torch.empty(0, 7, device="cuda"), torch.empty(0, 7, **i32), torch.empty(0, **i32),
+                      torch.full((5,), 9, **i32), torch.full((1,), 9, **i32), torch.full((1,), 9, **i32))
+    r = sda.evict_slots(torch.empty(0, 9, device="cuda"), torch.empty(0, 9, **i32), torch.empty(0, **i32), 7, out=out)
+    torch.cuda.synchronize()
+    assert r.freed_slots.tolist() == [-1] * 5 and r.freed_indptr.tolist() == [0] and r.status.tolist() == [0]
