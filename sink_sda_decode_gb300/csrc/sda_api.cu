@@ -1035,7 +1035,7 @@ static sda_status mass_geometry_ok(const ChunkGeom& g) {
   const sda_status s = chunk_geometry_ok(g);
   if (s != SDA_OK) return s;
   const int64_t S = static_cast<int64_t>(g.max_blocks) * g.k_per_block;
-  if (S > 0x7fffffffll || (S / 128 + 1) * g.B > (1 << 26)) return SDA_ERR_INVALID_ARG;
+  if (S > kMaxLen || (S / 128 + 1) * g.B > (1 << 26)) return SDA_ERR_INVALID_ARG;
   return SDA_OK;
 }
 

@@ -45,6 +45,10 @@ static_assert(sizeof(ChunkUnit) == 48, "three 16-byte words");
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Most cached positions of a sequence: a tile (up to 256) that holds the last of them
+// ends within 32 bits.
+constexpr int kMaxLen = 0x7fffffff - 511;
+
 // The position that logical tile i of a unit starts at, with tiles of `tile` positions.
 __host__ __device__ inline int chunk_tile_start(int i, int nf, int lo, int tile) {
   return (i < nf ? i : lo / tile + i - nf) * tile;
@@ -140,7 +144,8 @@ __device__ __forceinline__ int units_of(const ChunkGeom& g, int R, int b) {
 }
 __device__ __forceinline__ bool lengths_bad(const ChunkGeom& g, int b) {
   const int q0 = __ldg(g.q_indptr + b), q1 = __ldg(g.q_indptr + b + 1), n = __ldg(g.kv_len + b);
-  return q0 < 0 || q1 < q0 || q1 > g.T || n < 0 || n > (long long)g.max_blocks * g.k_per_block;
+  return q0 < 0 || q1 < q0 || q1 > g.T || n < 0 || n > kMaxLen ||
+         n > (long long)g.max_blocks * g.k_per_block;
 }
 // Unit r of sequence b (off is left 0).
 __device__ __forceinline__ ChunkUnit chunk_unit(const ChunkGeom& g, int R, int tile, int b, int r) {

@@ -244,3 +244,22 @@ def test_nan_that_is_seen(H, m, K):
     c.pool[torch_rows(c, 1)[500].cuda(), 3] = float("nan")
     out, lse = check(c)
     assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("H,B", [(4, 1), (64, 1), (64, 2049)])
+def test_lengths_near_two_billion_are_refused(H, B):
+    """Positions are counted in 32 bits, tiles' ends too.  (H = 64, one sequence of 5
+    tokens: two CTAs a tile; 2049 sequences: the plan.)"""
+    m = 5 if B == 1 else 1
+    q = torch.zeros(m * B, H, 512, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(64, 512, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+    ptr = torch.arange(0, m * B + 1, m, dtype=torch.int32, device="cuda")
+    n = torch.full((B,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    n[1:] = 1
+    ws = torch.empty(sda.chunk_attention_workspace_size(B, m * B, H, 512), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 3.0)
+    sda.chunk_attention(q, pool, table, ptr, n, torch.zeros(H, device="cuda"), 0.1, k_per_block=2 ** 30, out=out,
+                        workspace=ws)
+    assert sda.paged_error_flag(ws) == 2
+    assert bool((out == 3.0).all())

@@ -129,6 +129,15 @@ def test_results_of_evict_slots_are_apart(lib, bad):
     assert evict(lib, **bad) == INVALID
 
 
+@pytest.mark.parametrize("K,refused", [(1, True), (511, True), (512, False)])
+def test_attention_mass_rows_end_within_32_bits(lib, K, refused):
+    """Rows of 2^31 - K positions."""
+    n = ctypes.c_size_t(0)
+    a = (1, 1, 2 ** 31 - K, ctypes.byref(n))
+    got = lib.sda_attention_mass_workspace_size(*a)
+    assert (got == INVALID) if refused else (got != INVALID)  # (without a GPU no size is known)
+
+
 def test_python_refuses_sizes_that_do_not_fit():
     with pytest.raises(ValueError):
         sda.chunk_attention_workspace_size(2 ** 31, 1, 1, 64)
