@@ -478,7 +478,8 @@ sda_status sda_chunk_attention_workspace_size(int B, int T, int H, int D, size_t
 /*
  * Device-side error word of the last sda_chunk_attention or sda_attention_mass
  * that used `workspace`: writes one int32 (0 = fine) to *device_flag (device
- * memory), ordered on `stream`.
+ * memory), ordered on `stream`.  Calls without work (B = 0, T = 0 for the
+ * attention, an empty table for the mass) do not use theirs.
  */
 sda_status sda_paged_error_flag(const void* workspace, int32_t* device_flag, void* stream);
 

@@ -54,6 +54,15 @@ def _workspace(nbytes, dev, stream) -> torch.Tensor:
     return ws
 
 
+_HEADER = 256  # bytes of a workspace that say how the last call went
+
+
+def _nothing_to_do(workspace, stream) -> None:
+    """A call without work leaves its workspace alone; its error word is 0 all the same."""
+    with torch.cuda.stream(stream) if stream is not None else _HERE:
+        workspace[:_HEADER].zero_()
+
+
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(device: int, size, *args) -> int:
     """A workspace size depends on the device's SM count and these sizes only."""
@@ -149,6 +158,8 @@ def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torc
             q_indptr.data_ptr(), kv_len.data_ptr(), attn_sink.data_ptr(), float(softmax_scale),
             _int32(window, "window"), _int32(first, "first"), B, T, H, D, out.data_ptr(),
             lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(dev, stream))
+        if B == 0 or T == 0:
+            _nothing_to_do(workspace, stream)
     _lib.check(rc, "sda_chunk_attention")
     return out, lse
 
@@ -159,8 +170,11 @@ def paged_error_flag(workspace: torch.Tensor, stream: torch.cuda.Stream | None =
     q_indptr or kv_len outside their contract (nothing was computed); 3 = a table
     entry outside the pool (its rows counted as zeros)."""
     lib = _lib.load()
+    _need(workspace, "workspace", torch.uint8, 1)
     dev = workspace.device
     with _on(dev):
+        if workspace.numel() < _workspace_bytes(dev.index, attention_mass_workspace_size, 0, 0, 1):
+            raise ValueError("workspace is smaller than any that a call can have used")
         flag = torch.zeros(1, dtype=torch.int32, device=dev)
         if stream is not None:
             stream.wait_stream(torch.cuda.current_stream(dev))
@@ -229,6 +243,8 @@ def attention_mass(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torch
             kv_len.data_ptr(), lse.data_ptr(), float(softmax_scale), _int32(window, "window"),
             _int32(first, "first"), None if scores is None else scores.data_ptr(), float(decay), B,
             T, H, D, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(dev, stream))
+        if B == 0 or S == 0:
+            _nothing_to_do(workspace, stream)
     _lib.check(rc, "sda_attention_mass")
     return out
 

@@ -87,3 +87,29 @@ def test_prompts_then_eviction_then_steps():
     a, _ = sda.chunk_attention(q.cuda(), pool, table, one, lens, sink.cuda(), scale, k_per_block=1)
     d = sda.decode(q.cuda(), pool, idx, ptr, sink.cuda(), scale)
     assert float((a.double() - d.double()).abs().max()) <= 4 * 2.0 ** -8 * 6
+
+
+@pytest.mark.parametrize("B,T", [(0, 0), (2, 0)])
+def test_error_word_of_calls_without_work(B, T):
+    """0, whatever the workspace held before."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros(T, 16, 64, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(64, 64, dtype=torch.bfloat16, device="cuda")
+    ptr, n = torch.zeros(B + 1, **i32), torch.zeros(B, **i32)
+    ws = torch.full((max(sda.chunk_attention_workspace_size(B, T, 16, 64),
+                         sda.attention_mass_workspace_size(B, 0, 16)),), 0x7f, dtype=torch.uint8, device="cuda")
+    _, lse = sda.chunk_attention(q, pool, torch.zeros(B, 1, **i32), ptr, n, torch.zeros(16, device="cuda"), 0.1,
+                                 k_per_block=16, workspace=ws)
+    assert sda.paged_error_flag(ws) == 0
+    ws.fill_(0x7f)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    sda.attention_mass(q, pool, torch.zeros(B, 0, **i32), ptr, n, lse, 0.1, k_per_block=16, workspace=ws, stream=side)
+    assert sda.paged_error_flag(ws, side) == 0
+
+
+def test_error_word_needs_a_workspace():
+    with pytest.raises(ValueError):
+        sda.paged_error_flag(torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises((ValueError, TypeError)):
+        sda.paged_error_flag(torch.zeros(1 << 20, device="cuda"))
