@@ -46,11 +46,17 @@ def _stream_of(dev, stream) -> int:
             else torch._C._cuda_getCurrentRawStream(dev.index))
 
 
-def _workspace(nbytes, dev, stream) -> torch.Tensor:
-    """A workspace that torch's allocator knows is in use on `stream`."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+def _used_on(stream, *tensors) -> None:
+    """Tells torch's allocator that these, made on the current stream, are in use on `stream`,
+    so that their memory is not given away while the call runs."""
     if isinstance(stream, torch.cuda.Stream):
-        ws.record_stream(stream)
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _workspace(nbytes, dev, stream) -> torch.Tensor:
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _used_on(stream, ws)
     return ws
 
 
@@ -136,12 +142,14 @@ def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torc
         raise ValueError("attn_sink must have H entries")
     if out is None:
         out = torch.empty_like(q)
+        _used_on(stream, out)
     else:
         _need(out, "out", torch.bfloat16, 3, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if lse is None:
         lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+        _used_on(stream, lse)
     else:
         _need(lse, "lse", torch.float32, 2, dev)
         if lse.shape != (T, H):
@@ -230,6 +238,7 @@ def attention_mass(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torch
                 raise ValueError(f"{name} must be [B, max_blocks * k_per_block]")
     if out is None:
         out = torch.empty(B, S, dtype=torch.float32, device=dev)
+        _used_on(stream, out)
     with _on(dev):
         if workspace is None:
             workspace = _workspace(
@@ -292,6 +301,7 @@ def evict_slots(scores: torch.Tensor, slot_table: torch.Tensor, kv_len: torch.Te
                       torch.empty(freed, dtype=i32, device=dev),
                       torch.empty(B + 1, dtype=i32, device=dev),
                       torch.empty(1, dtype=i32, device=dev))
+        _used_on(stream, *out)
     else:
         _need(out.scores, "out.scores", torch.float32, 2, dev)
         for name in ("slot_table", "kv_len", "freed_slots", "freed_indptr", "status"):

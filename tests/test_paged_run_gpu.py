@@ -113,3 +113,38 @@ def test_error_word_needs_a_workspace():
         sda.paged_error_flag(torch.zeros(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises((ValueError, TypeError)):
         sda.paged_error_flag(torch.zeros(1 << 20, device="cuda"))
+
+
+@pytest.mark.parametrize("op", ["attend", "mass", "evict"])
+def test_results_on_another_stream_are_not_given_away(op):
+    """Results that are dropped while their call still waits on its stream."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros(64, 16, 512, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(4096, 512, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(4096, **i32).view(1, 4096)
+    ptr, n = torch.tensor([0, 64], **i32), torch.tensor([4096], **i32)
+    lse, scores = torch.zeros(64, 16, device="cuda"), torch.zeros(1, 4096, device="cuda")
+    sink = torch.zeros(16, device="cuda")
+    side = torch.cuda.Stream()
+
+    def call():
+        if op == "attend":
+            return sda.chunk_attention(q, pool, table, ptr, n, sink, 0.1, k_per_block=1, stream=side)
+        if op == "mass":
+            return (sda.attention_mass(q, pool, table, ptr, n, lse, 0.1, k_per_block=1, stream=side),)
+        return tuple(sda.evict_slots(scores, table, n, 1000, stream=side))
+
+    call()  # (what is made once)
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    gate = torch.cuda.Event()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # 0.1 s: the call waits behind it
+    r = call()
+    gate.record(side)
+    like = [(t.shape, t.dtype, t.data_ptr()) for t in r]
+    del r
+    again = [torch.empty(s, dtype=d, device="cuda") for s, d, _ in like]
+    assert not gate.query()  # still waiting
+    assert not {t.data_ptr() for t in again} & {p for _, _, p in like}
+    torch.cuda.synchronize()
