@@ -83,8 +83,12 @@ constexpr int unit_cost(int R) { return R == 128 ? 3 : 1; }
 
 // How the tiles are shared out.
 //   kPlanned  ranges of equal cost, by a kernel before
-//   kCut      the same, but every CTA finds its own beginning (few units)
-//   kWhole    whole units, every CTA its share: no merge of pieces is launched
+//   kCut      the same, but every CTA finds its own beginning (few units): one launch
+//             less (replayed from a graph, against kPlanned: one token of 16 heads over 64
+//             caches 28.7 against 29.7 us, of 64 heads over 8 long caches 92.0 against 94.0,
+//             drafted tokens 131.1 against 130.0, ragged prompts 421.5 against 420.5)
+//   kWhole    whole units, every CTA its share: no merge of pieces is launched (prompts
+//             with a window of 128: 188 us, 209 with a plan and a merge)
 enum ChunkMode : int { kPlanned = 0, kCut = 1, kWhole = 2 };
 constexpr int kFusedSeqs = 2048, kFusedUnits = 4096;  // most that the CTAs look through themselves
 

@@ -15,12 +15,11 @@
 // scores and slots are read once; the digits' histograms and the kept counts of
 // the CTAs are put together through distributed shared memory, and each warp
 // writes the kept and the freed of 32 positions in a row at a time.  16 sequences
-// of 10482 to 131072 positions cut to 4096 take 35 us, against 176 with one CTA a
+// of up to 131072 positions cut to 4096 take 37 us, against 179 with one CTA a
 // sequence that reads its row again for every digit (evict_stream_kernel, left for
 // tables whose share does not fit).  The bytes would take 2 us; what bounds it is the
-// chain of the longest sequence: about 3 us to load its share, then 5 us for each of
-// three digits (histogram, two cluster barriers with the sums between them) and 8 us
-// to count and to write.
+// chain of the longest sequence: its share's load, three digits (each a histogram and
+// two cluster barriers with the sums between them), the counts, the writes.
 //
 // In-place calls are safe: everything is read before anything is written (the
 // cluster kernel), or a position before anything at or before it (the stream
@@ -108,8 +107,8 @@ __global__ void __launch_bounds__(kThreads) evict_indptr_kernel(const EvictArgs 
 
 // Rows of up to kOneCta columns take one CTA, longer ones a cluster of 8 or 6: 14
 // clusters of 8 run at once on a GB300, or 24 of 6, so that more than 14 sequences
-// take clusters of 6 where their share fits (16 sequences of up to 131072: 39 us in
-// clusters of 6, 42 us in two waves of clusters of 8, before the last steps).
+// take clusters of 6 where their share fits (16 sequences of up to 131072, replayed
+// from a graph: 36.6 us in clusters of 6, 39.2 us in two waves of clusters of 8).
 constexpr int kOneCta = 4096, kFused = 4096, kClusters8 = 14;
 constexpr size_t kMaxSmem = 200 * 1024;
 static_assert(kMaxSmem / 8 / 32 <= kBins / 2, "the bits of a share's rows of 32 fit the histogram");

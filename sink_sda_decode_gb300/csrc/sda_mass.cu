@@ -12,8 +12,8 @@
 // Two kernels.  mass_kernel, for chunks: pairs of CTAs (cta_group::2) take units of
 // 256 positions, 128 in the shared memory of each CTA, and the q rows that see any
 // of them, cut into tiles of 256 rows and streamed as 64-column panels, of which
-// each CTA loads 128 rows.  (M256 N256 K16 runs at the tensor pipe's full rate, 129
-// cycles, and a CTA's panels come in at 32 bytes a cycle; with one CTA to 128
+// each CTA loads 128 rows.  (M256 N256 K16 runs at the tensor pipe's full rate,
+// and a CTA's panels come in at 32 bytes a cycle; with one CTA to 128
 // positions and 128 rows they came at 64, the limit of a SM's loads.)  All (unit, row
 // tile) pairs form one sequence, cut into equal ranges, one per pair; a unit that a
 // range boundary cuts leaves its partial sums per piece, which a last kernel adds up
@@ -25,10 +25,10 @@
 // mass_step_kernel, for steps of few rows: see there.
 //
 // Measured, 2 sequences of 500 to 600 tokens over 6000 to 8192 positions, 64 heads,
-// D = 512 (542 GFLOP): 287 us of device time, 1890 TFLOP/s, the tensor pipe active
-// 94 % of the cycles.  One CTA to 128 positions took 744 us; with 8 epilogue warps the
-// weights set the pace (488 us), and with masks tested per weight the CTAs at the
-// chunk's own positions came in last (396 us; a row range per position: 287).
+// D = 512 (542 GFLOP): 287 to 325 us, 1890 to 1670 TFLOP/s between runs, the tensor
+// pipe active 94 % of the cycles.  One CTA to 128 positions took 744 us; pairs
+// with 8 epilogue warps 488 (the weights set the pace), with 16 warps 396, and with a
+// range of rows per position in place of masks tested per weight 287.
 #include <cuda_bf16.h>
 
 #include "sda_chunk_dev.cuh"
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kKeys) mass_combine_kernel(
 // in shared memory from tile to tile of a sequence; S^T = K Q^T with M = 64
 // positions, N = R rows; the sums over the rows are final, so out is written at once.
 // Measured: one token of 64 heads over 8 caches of 16384 to 65536 positions, D = 512
-// (368 MB): 61 us, 89 % of the measured copy rate; the kernel for chunks took 131.
+// (368 MB): 61 us, where a copy of as many bytes takes 55; the kernel for chunks took 131.
 //   warps 0..7   weights and sums: warp w reads TMEM lane quadrant w % 4 (16
 //                positions) and half w / 4 of the rows' columns
 //   warp 8       MMAs, q loads      warp 9   cached rows by TMA (boxes of 16)
