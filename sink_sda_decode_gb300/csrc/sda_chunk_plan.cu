@@ -102,12 +102,17 @@ __global__ void paged_error_kernel(const ChunkHeader* __restrict__ hdr, int32_t*
 
 // Merge of the pieces of cut units.  Block (x = k - 1, y): the beginning of worker
 // k's range; it acts if that is the first to cut its unit.  A warp takes 128 columns
-// (all of D below that) of one row; its lanes hold the pieces' (m, l) and weights,
-// 32 at a time, and eight pieces' partials are in flight together: a unit cut into 19
-// pieces (8 sequences of 65536 positions) is bound by the latency of those loads.
-// Piece 0 lies in slot 2 (k - 1) + 1 (the unit starts in worker k - 1's range), piece
-// i in slot 2 (k - 1 + i).
+// (all of D below that) of one row.  Piece 0 lies in slot 2 (k - 1) + 1 (the unit starts
+// in worker k - 1's range), piece i in slot 2 (k - 1 + i).
+// What bounds it is the chain of dependent loads: after the two records that tell
+// whether a block acts, those of the workers behind k and the (m, l) of all pieces that
+// there may be are loaded together, then the partials of P pieces at a time.
 constexpr int kCombineWarps = 8;
+// A pair's units are seldom cut more than once, and with few registers more rows are
+// under way (drafted tokens, replayed from a graph: 123.9 us with P = 2, 125.9 with 3,
+// 126.7 with 1, 131.3 with 8); a step's few rows are cut into up to 19 pieces (one token
+// over 8 long caches: 92.0 us with P = 8, 92.2 with 4, 93.7 with 2).
+constexpr int kPiecesPair = 2, kPiecesOne = 8;
 
 template <int D>
 struct CombineCfg {
@@ -116,7 +121,18 @@ struct CombineCfg {
   static constexpr int kPer = D < 128 ? 2 : 4;             // columns of a lane
 };
 
-template <int D>
+// Loads that stay where they are written: the compiler else puts them one by one
+// before their uses.
+__device__ __forceinline__ void load_here(const float* p, float (&v)[4]) {
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "l"(p));
+}
+__device__ __forceinline__ void load_here(const float* p, float (&v)[2]) {
+  asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p));
+}
+
+template <int D, int P>
 __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
     const float* __restrict__ attn_sink, int H, int R, __nv_bfloat16* __restrict__ out,
     float* __restrict__ lse, int workers, const ChunkUnit* __restrict__ recs, const float2* __restrict__ part_ml,
@@ -133,21 +149,22 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
   const int row = blockIdx.y * C::kRows + warp / C::kWarpsRow;
   const int col = (warp % C::kWarpsRow) * 128 + lane * C::kPer;
   if (row >= un.nrows) return;
-  // the pieces: piece 0, and those of the workers from k on that begin in this unit
-  int np = 1;
-  for (int k0 = k;; k0 += 32) {
-    const int x = k0 + lane;
-    const bool in = x < workers && recs[x].row0 == un.row0 && recs[x].off > 0;
-    const uint32_t not_in = ~__ballot_sync(0xffffffffu, in);
-    np += not_in ? __ffs(not_in) - 1 : 32;
-    if (not_in) break;
-  }
   auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + i)); };
+  auto begins_here = [&](int x) { return x < workers && recs[x].row0 == un.row0 && recs[x].off > 0; };
+  // lane i: worker k - 1 + i, whose range begins in the unit's piece i if that exists
+  float2 ml0 = make_float2(-INFINITY, 0.f);
+  if (k - 1 + lane < workers) ml0 = part_ml[slot(lane) * R + row];
+  const float sink = attn_sink[(un.h0 + row) % H], ms = sink * kLog2e;
+  uint32_t not_in = __ballot_sync(0xffffffffu, lane > 0 && !begins_here(k - 1 + lane));
+  int np = not_in ? __ffs(not_in) - 1 : 32;
+  for (int x0 = k + 31; not_in == 0; x0 += 32) {
+    not_in = ~__ballot_sync(0xffffffffu, begins_here(x0 + lane));
+    np += not_in ? __ffs(not_in) - 1 : 32;
+  }
+  if (lane >= np) ml0 = make_float2(-INFINITY, 0.f);
   auto ml_of = [&](int i) {
     return i < np ? part_ml[slot(i) * R + row] : make_float2(-INFINITY, 0.f);
   };
-  const float sink = attn_sink[(un.h0 + row) % H], ms = sink * kLog2e;
-  const float2 ml0 = ml_of(lane);  // of the first 32 pieces
   float mk = ml0.x;
   for (int i = lane + 32; i < np; i += 32) mk = fmaxf(mk, ml_of(i).x);
 #pragma unroll
@@ -162,21 +179,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
     const float w = i0 + lane < np ? ex2_approx(ml.x - M) : 0.f;
     den += ml.x == -INFINITY ? ml.y : ml.y * w;
     const int n = min(32, np - i0);
-    for (int j0 = 0; j0 < n; j0 += 8) {
-      float v[8][C::kPer];
+    for (int j0 = 0; j0 < n; j0 += P) {
+      float v[P][C::kPer];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float* o = part_o + (slot(i0 + min(j0 + j, n - 1)) * R + row) * D + col;
-        if constexpr (C::kPer == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(o);
-          v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(o);
-          v[j][0] = x.x, v[j][1] = x.y;
-        }
-      }
+      for (int j = 0; j < P; ++j)
+        load_here(part_o + (slot(i0 + min(j0 + j, n - 1)) * R + row) * D + col, v[j]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < P; ++j) {
         const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
         if (j0 + j < n) {
 #pragma unroll
@@ -275,10 +284,14 @@ cudaError_t launch_chunk_combine(const float* attn_sink, const ChunkGeom& g, voi
                       reinterpret_cast<const float*>(base + L.o_off));
   };
   switch (g.D) {
-    case 64: return go(chunk_combine_kernel<64>, CombineCfg<64>::kRows);
-    case 128: return go(chunk_combine_kernel<128>, CombineCfg<128>::kRows);
-    case 256: return go(chunk_combine_kernel<256>, CombineCfg<256>::kRows);
-    case 512: return go(chunk_combine_kernel<512>, CombineCfg<512>::kRows);
+    case 64: return go(chunk_combine_kernel<64, kPiecesOne>, CombineCfg<64>::kRows);
+    case 128: return go(chunk_combine_kernel<128, kPiecesOne>, CombineCfg<128>::kRows);
+    case 256:
+      return L.pair ? go(chunk_combine_kernel<256, kPiecesPair>, CombineCfg<256>::kRows)
+                    : go(chunk_combine_kernel<256, kPiecesOne>, CombineCfg<256>::kRows);
+    case 512:
+      return L.pair ? go(chunk_combine_kernel<512, kPiecesPair>, CombineCfg<512>::kRows)
+                    : go(chunk_combine_kernel<512, kPiecesOne>, CombineCfg<512>::kRows);
     default: return cudaErrorInvalidValue;
   }
 }
