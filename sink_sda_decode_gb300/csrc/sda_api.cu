@@ -937,7 +937,7 @@ sda_status sda_qk_norm_rope_swa_store_fp8(const void* q, const void* kv, const v
 }
 
 // The checks that the paged-cache operators share; what the kernels trust.
-static sda_status chunk_geometry_ok(const ChunkGeom& g) {
+static sda_status chunk_geometry_ok(ChunkGeom& g) {
   if (g.B < 0 || g.T < 0 || g.k_per_block <= 0 || g.max_blocks < 0 || g.window < 0 || g.first < 0)
     return SDA_ERR_INVALID_ARG;
   if (g.total_pages <= 0 || g.total_pages > 0x7fffffffll || g.base < 0 || g.base > g.total_pages)
@@ -946,6 +946,7 @@ static sda_status chunk_geometry_ok(const ChunkGeom& g) {
   // rows are counted in 32 bits, 64 of them past the end being addressable
   if (static_cast<int64_t>(g.T) * g.H > 0x7fffffffll - 64 || g.B > (1 << 24))
     return SDA_ERR_INVALID_ARG;
+  g.set_h();
   return SDA_OK;
 }
 
@@ -987,8 +988,8 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
                                const float* attn_sink, float softmax_scale, int window, int first,
                                int B, int T, int H, int D, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, void* stream) {
-  const ChunkGeom g{q_indptr, kv_len,      block_table, B,      T,    H, D, max_blocks,
-                    k_per_block, base, total_pages, window, first};
+  ChunkGeom g{q_indptr, kv_len,      block_table, B,      T,    H, D, max_blocks,
+                    k_per_block, base, total_pages, window, first, 0, 0};
   const sda_status s = chunk_geometry_ok(g);
   if (s != SDA_OK) return s;
   if (B == 0 || T == 0) return SDA_OK;
@@ -1031,7 +1032,7 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
 }
 
 // The mass's score rows span the whole table: S = max_blocks * k_per_block.
-static sda_status mass_geometry_ok(const ChunkGeom& g) {
+static sda_status mass_geometry_ok(ChunkGeom& g) {
   const sda_status s = chunk_geometry_ok(g);
   if (s != SDA_OK) return s;
   const int64_t S = static_cast<int64_t>(g.max_blocks) * g.k_per_block;
@@ -1062,8 +1063,8 @@ sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t tot
                               const float* lse, float softmax_scale, int window, int first,
                               const float* prev, float decay, int B, int T, int H, int D,
                               float* out, void* workspace, size_t workspace_bytes, void* stream) {
-  const ChunkGeom g{q_indptr, kv_len,      block_table, B,      T,    H, D, max_blocks,
-                    k_per_block, base, total_pages, window, first};
+  ChunkGeom g{q_indptr, kv_len,      block_table, B,      T,    H, D, max_blocks,
+                    k_per_block, base, total_pages, window, first, 0, 0};
   const sda_status s = mass_geometry_ok(g);
   if (s != SDA_OK) return s;
   const int64_t S = static_cast<int64_t>(max_blocks) * k_per_block;

@@ -23,6 +23,14 @@ struct ChunkGeom {
   int max_blocks, k_per_block;
   int64_t base, total_pages;
   int window, first;
+  uint32_t h_mul;  // n / H = n h_mul >> h_shift for 0 <= n < 2^31 (div_h)
+  int h_shift;
+  void set_h() {
+    int b = 0;
+    while ((1 << b) < H) ++b;
+    h_shift = 31 + b;
+    h_mul = (uint32_t)(((1ull << h_shift) + H - 1) / H);
+  }
 };
 
 // All heads share the cached rows, so the (token, head) rows of a sequence
@@ -142,6 +150,11 @@ cudaError_t launch_mass(const void* q, const void* kv, const ChunkGeom& g, const
 void note_cuda_error(cudaError_t e, const char* where);
 
 #ifdef __CUDACC__
+// n / H.  With b = ceil(log2 H), h_mul = (2^(31 + b) + e) / H for some 0 <= e < H, so
+// n h_mul / 2^(31 + b) = n / H + (n / 2^31) (e / 2^b) / H exceeds n / H by less than 1 / H.
+__device__ __forceinline__ int div_h(const ChunkGeom& g, int n) {
+  return (int)(((unsigned long long)(unsigned)n * g.h_mul) >> g.h_shift);
+}
 __device__ __forceinline__ int units_of(const ChunkGeom& g, int R, int b) {
   const int m = __ldg(g.q_indptr + b + 1) - __ldg(g.q_indptr + b);
   return (int)(((long long)m * g.H + R - 1) / R);
@@ -159,10 +172,10 @@ __device__ __forceinline__ ChunkUnit chunk_unit(const ChunkGeom& g, int R, int t
   d.row0 = q0 * g.H + r0;
   d.nrows = min(R, m * g.H - r0);
   d.b = b;
-  const int tok = r0 / g.H;
+  const int tok = div_h(g, r0);
   d.pos0 = n - m + tok;
   d.h0 = r0 - tok * g.H;
-  const int p_hi = d.pos0 + (d.h0 + d.nrows - 1) / g.H;
+  const int p_hi = d.pos0 + div_h(g, d.h0 + d.nrows - 1);
   d.hi = max(p_hi + 1, 0);
   d.lo = g.window > 0 ? (int)max((long long)d.pos0 - g.window + 1, 0ll) : 0;
   if (d.hi == 0) d.lo = 0;

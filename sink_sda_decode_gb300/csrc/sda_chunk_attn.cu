@@ -402,10 +402,11 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int i1 = min(un.ntiles, i0 + nt - g);
       const bool whole = i0 == 0 && i1 == un.ntiles;
       const bool vA = hA < un.nrows, vB = hB < un.nrows;
-      const int posA = un.pos0 + (un.h0 + hA) / H, posB = un.pos0 + (un.h0 + hB) / H;
-      const int p_lo = un.pos0, p_hi = un.pos0 + (un.h0 + un.nrows - 1) / H;
-      const float sinkA = whole && vA ? __ldg(p.attn_sink + (un.h0 + hA) % H) : 0.f;
-      const float sinkB = whole && vB ? __ldg(p.attn_sink + (un.h0 + hB) % H) : 0.f;
+      const int tokA = div_h(p.g, un.h0 + hA), tokB = div_h(p.g, un.h0 + hB);
+      const int posA = un.pos0 + tokA, posB = un.pos0 + tokB;
+      const int p_lo = un.pos0, p_hi = un.pos0 + div_h(p.g, un.h0 + un.nrows - 1);
+      const float sinkA = whole && vA ? __ldg(p.attn_sink + un.h0 + hA - tokA * H) : 0.f;
+      const float sinkB = whole && vB ? __ldg(p.attn_sink + un.h0 + hB - tokB * H) : 0.f;
       const float scA = vA ? sc : 0.f, scB = vB ? sc : 0.f;
       float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;  // l: this thread's share
       for (int i = i0; i < i1; ++i, ++g) {
@@ -483,7 +484,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // p = 2^(x scale - m) in bf16 into rows hA, hB of P (K-major, 128-byte
         // swizzle) with two stmatrix.x4.  The MMA multiplies the rounded p, the
         // denominator sums the unrounded ones: each weight is off by at most
-        // 2^-9 of itself, less than the output's own rounding, and lse is exact.
+        // 2^-8 of itself, as the output's own rounding, and lse has none.
         const uint32_t prow = sP + s * C::kPBytes + (2 * q4) * 1024 + (lane & 7) * 128;
         auto pchunk = [&](int c) {  // this lane's address of a matrix of stmatrix: chunk c of its row
           return prow + (uint32_t)(((kReps * hc + c) ^ (lane & 7)) << 4);

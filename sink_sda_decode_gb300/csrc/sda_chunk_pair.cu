@@ -508,8 +508,9 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int i1 = min(un.ntiles, i0 + nt - g);
       const bool whole = i0 == 0 && i1 == un.ntiles;
       const int h0 = un.h0 + rank * kR, nrows = max(0, min(kR, un.nrows - rank * kR));
-      const int p_lo = un.pos0 + h0 / H, p_hi = un.pos0 + (h0 + max(nrows, 1) - 1) / H;
-      const float sink = whole && st < nrows ? __ldg(p.attn_sink + (h0 + st) % H) : 0.f;  // of row st
+      const int p_lo = un.pos0 + div_h(p.g, h0), p_hi = un.pos0 + div_h(p.g, h0 + max(nrows, 1) - 1);
+      const float sink =
+          whole && st < nrows ? __ldg(p.attn_sink + h0 + st - div_h(p.g, h0 + st) * H) : 0.f;  // of row st
       float m[4], l[4], scr[4];  // l: this thread's share
       int pos[4];
 #pragma unroll
@@ -519,7 +520,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // (rows past the unit's end have factor 0: their weights, never used, stay
         // finite and raise nothing)
         scr[i] = row0 + 8 * i < nrows ? sc : 0.f;
-        pos[i] = un.pos0 + (h0 + row0 + 8 * i) / H;
+        pos[i] = un.pos0 + div_h(p.g, h0 + row0 + 8 * i);
       }
       for (int i = i0; i < i1; ++i, ++g) {
         const int s = g & 1;
@@ -552,14 +553,22 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         uint32_t see = 0xffffu;
         int flags = 0;
         if (!full) {
+          // bits 0, 1, 8, 9 of a row's ten positions are its elements 0..3
           see = 0;
-          bool poison = false;  // a score that is masked and not finite
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = j0 + 32 * kh + 16 * hc + 8 * ((e >> 1) & 1) + 2 * tq + (e & 1);
-            const bool ok = j <= pos[e >> 2] && (window == 0 || j > pos[e >> 2] - window || j < nfirst);
-            see |= ok ? 1u << e : 0u;
-            poison |= !ok && !(fabsf(x[e]) < INFINITY);
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const uint32_t m10 = seen_bits(pos[i4], j0 + 32 * kh + 16 * hc + 2 * tq, window, nfirst);
+            see |= ((m10 & 3u) | ((m10 >> 6) & 12u)) << (4 * i4);
+          }
+          bool poison = false;  // a score that is masked and not finite
+          float zero = 0.f;  // NaN if a score is not finite
+#pragma unroll
+          for (int e = 0; e < 16; ++e) zero = fmaf(x[e], 0.f, zero);
+          if (zero != 0.f) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) bad |= fabsf(x[e]) < INFINITY ? 0u : 1u << e;
+            poison = (bad & ~see) != 0;
           }
           if (named_bar_or(1, kSmThreads, poison)) flags = 2;
         }
