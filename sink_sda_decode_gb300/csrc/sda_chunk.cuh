@@ -86,7 +86,7 @@ struct alignas(16) ChunkStart {
 // many more for its beginning and end (on a pair about 5500 cycles, at 1650 a tile).
 // Equal numbers of tiles left the workers that had many short units far behind: 12
 // sequences of 1 to 300 tokens over 300 to 6000 positions took 521 us (the median
-// worker was done after 340), and take 420.
+// worker was done after 340), and 420 with equal costs.
 constexpr int unit_cost(int R) { return R == 128 ? 3 : 1; }
 
 // How the tiles are shared out.

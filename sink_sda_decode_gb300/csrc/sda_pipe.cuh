@@ -56,7 +56,7 @@ __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, const P
 }
 
 // pipe_wait for a converged warp.  All lanes poll: a lane polling alone for its
-// warp was slower (a prompt chunk of attention 2.6 to 3.4 ms).
+// warp was slower (a prompt chunk of attention 1.34 to 1.75 ms).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const PipeWait& w) {
   return __all_sync(0xffffffffu, pipe_wait(bar, parity, w));
 }
