@@ -97,7 +97,9 @@ struct Cursor {
 
 // Where worker `worker` begins; called by all THREADS threads of the CTA, which
 // then are past a barrier.  `s_seq` (kFusedSeqs + 1 words) and `scratch` (64 words)
-// are shared memory that is free until then.  *bad: the lengths broke the contract.
+// are shared memory that is free until then.  *bad: the lengths broke the contract;
+// the merge is launched all the same and goes by the records, so every worker says
+// that it begins in no unit (the workspace may hold an earlier call's, or anything).
 template <int THREADS, int R, int TILE>
 __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker, int* s_seq,
                                                   int* scratch, bool* bad) {
@@ -112,6 +114,11 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long* sums = reinterpret_cast<long long*>(scratch);  // [kW]
   int* found = scratch + 2 * kW;                             // [5]
+  auto refuse = [&]() {
+    *bad = true;
+    if (p.mode == kCut && tid == 0) p.recs[worker] = ChunkUnit{-1};
+    return ChunkStart{0, 0, 0, 0};
+  };
   // exclusive prefix of one value per thread, and the total
   auto scan = [&](long long v, long long* total) {
     long long x = v;
@@ -142,8 +149,7 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
     else mine += units_of(g, R, b);
   }
   long long at = scan(mine, &U);
-  *bad = __syncthreads_or(wrong);
-  if (*bad) return st;
+  if (__syncthreads_or(wrong)) return refuse();
   for (int b = b0; b < b1; ++b) {
     s_seq[b] = (int)at;
     at += units_of(g, R, b);
@@ -182,10 +188,7 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
       }
     }
     const long long tiles = scan(nt, &tt);  // of the units before this stretch
-    if (tt > 0x7fffffffll) {
-      *bad = true;
-      return st;
-    }
+    if (tt > 0x7fffffffll) return refuse();
     const long long cost = tt + U * unit_cost(R);
     const long long per = cost > 0 ? (cost + p.workers - 1) / p.workers : 1;
     const long long mine0 = tiles + (long long)u0 * unit_cost(R);
