@@ -58,15 +58,34 @@ cudaError_t device_caps(DeviceCaps* caps) {
     d.err = cudaDeviceGetAttribute(&d.caps.num_sms, cudaDevAttrMultiProcessorCount, dev);
     for (int nh : {16, 32, 64})
       if (d.err == cudaSuccess) d.err = umma_prepare(nh);
-    if (d.err == cudaSuccess) d.err = chunk_prepare();
-    if (d.err == cudaSuccess) d.err = mass_prepare();
-    if (d.err == cudaSuccess) d.err = evict_prepare();
   });
   *caps = d.caps;
   return d.err;
 }
 
 namespace {
+
+// device_caps(), and the kernel attributes of one of the paged-cache operators, set at
+// that operator's first call on a device: setting them loads the kernels, which is not
+// decode's to wait for (its first call took 3.1 ms in place of 0.7 with all of them).
+enum PagedOp : int { kOpAttention, kOpMass, kOpEvict, kPagedOps };
+struct Prepared {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+Prepared g_paged[kMaxDevices][kPagedOps];
+
+cudaError_t paged_caps(PagedOp op, DeviceCaps* caps) {
+  cudaError_t e = device_caps(caps);
+  int dev = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  Prepared& p = g_paged[dev][op];
+  std::call_once(p.once, [&]() {
+    p.err = op == kOpAttention ? chunk_prepare() : (op == kOpMass ? mass_prepare() : evict_prepare());
+  });
+  return p.err;
+}
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -973,7 +992,7 @@ sda_status sda_chunk_attention_workspace_size(int B, int T, int H, int D, size_t
   const sda_status s = chunk_geometry_ok(g);
   if (s != SDA_OK) return s;
   DeviceCaps caps;
-  const cudaError_t e = device_caps(&caps);
+  const cudaError_t e = paged_caps(kOpAttention, &caps);
   if (e != cudaSuccess) {
     note_cuda_error(e, "sda_chunk_attention_workspace_size");
     return SDA_ERR_CUDA;
@@ -1010,7 +1029,7 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
     return SDA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return SDA_ERR_WORKSPACE;
   DeviceCaps caps;
-  cudaError_t e = device_caps(&caps);
+  cudaError_t e = paged_caps(kOpAttention, &caps);
   if (e != cudaSuccess) {
     note_cuda_error(e, "sda_chunk_attention");
     return SDA_ERR_CUDA;
@@ -1048,7 +1067,7 @@ sda_status sda_attention_mass_workspace_size(int B, int max_blocks, int k_per_bl
   const sda_status s = mass_geometry_ok(g);
   if (s != SDA_OK) return s;
   DeviceCaps caps;
-  const cudaError_t e = device_caps(&caps);
+  const cudaError_t e = paged_caps(kOpMass, &caps);
   if (e != cudaSuccess) {
     note_cuda_error(e, "sda_attention_mass_workspace_size");
     return SDA_ERR_CUDA;
@@ -1086,7 +1105,7 @@ sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t tot
     return SDA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return SDA_ERR_WORKSPACE;
   DeviceCaps caps;
-  cudaError_t e = device_caps(&caps);
+  cudaError_t e = paged_caps(kOpMass, &caps);
   if (e != cudaSuccess) {
     note_cuda_error(e, "sda_attention_mass");
     return SDA_ERR_CUDA;
@@ -1153,7 +1172,7 @@ sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64
                     freed_indptr, status};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   DeviceCaps caps;
-  cudaError_t e = device_caps(&caps);
+  cudaError_t e = paged_caps(kOpEvict, &caps);
   if (e == cudaSuccess && g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_before, st);
   if (e == cudaSuccess) e = launch_evict(a, st);
   if (e == cudaSuccess && g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_after, st);
