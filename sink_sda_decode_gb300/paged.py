@@ -11,6 +11,10 @@ table one of single slots).  With m_b new tokens and n_b = kv_len[b] cached
 positions, the new tokens' own rows the last m_b of them, token i stands at
 p = n_b - m_b + i and sees the positions j <= p with window == 0, or
 j > p - window, or j < first.
+
+A call runs on `stream` (None: the current one).  With another stream than the
+current one, the caller orders the two, as for any kernel: before the call for
+tensors that are written on the current stream, after it for its results.
 """
 from __future__ import annotations
 
@@ -21,7 +25,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _lib
+from . import _lib, _memory
 
 
 def _need(t, name: str, dtype, ndim: int, dev=None):
@@ -44,20 +48,6 @@ def _on(dev):
 def _stream_of(dev, stream) -> int:
     return (stream.cuda_stream if stream is not None
             else torch._C._cuda_getCurrentRawStream(dev.index))
-
-
-def _used_on(stream, *tensors) -> None:
-    """Tells torch's allocator that these, made on the current stream, are in use on `stream`,
-    so that their memory is not given away while the call runs."""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in tensors:
-            t.record_stream(stream)
-
-
-def _workspace(nbytes, dev, stream) -> torch.Tensor:
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _used_on(stream, ws)
-    return ws
 
 
 _HEADER = 256  # bytes of a workspace that say how the last call went
@@ -141,22 +131,20 @@ def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torc
     if attn_sink.numel() != H:
         raise ValueError("attn_sink must have H entries")
     if out is None:
-        out = torch.empty_like(q)
-        _used_on(stream, out)
+        out = _memory.empty(q.shape, q.dtype, dev, stream)
     else:
         _need(out, "out", torch.bfloat16, 3, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
-        _used_on(stream, lse)
+        lse = _memory.empty((T, H), torch.float32, dev, stream)
     else:
         _need(lse, "lse", torch.float32, 2, dev)
         if lse.shape != (T, H):
             raise ValueError("lse must be [T, H]")
     with _on(dev):
         if workspace is None:
-            workspace = _workspace(
+            workspace = _memory.workspace(
                 _workspace_bytes(dev.index, chunk_attention_workspace_size, B, T, H, D), dev, stream)
         else:
             _need(workspace, "workspace", torch.uint8, 1, dev)
@@ -237,11 +225,10 @@ def attention_mass(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torch
             if t.shape != (B, S):
                 raise ValueError(f"{name} must be [B, max_blocks * k_per_block]")
     if out is None:
-        out = torch.empty(B, S, dtype=torch.float32, device=dev)
-        _used_on(stream, out)
+        out = _memory.empty((B, S), torch.float32, dev, stream)
     with _on(dev):
         if workspace is None:
-            workspace = _workspace(
+            workspace = _memory.workspace(
                 _workspace_bytes(dev.index, attention_mass_workspace_size, B, block_table.shape[1],
                                  k_per_block), dev, stream)
         else:
@@ -295,13 +282,8 @@ def evict_slots(scores: torch.Tensor, slot_table: torch.Tensor, kv_len: torch.Te
     if out is None:
         W = min(S, budget)
         i32 = torch.int32
-        out = Evicted(torch.empty(B, W, dtype=torch.float32, device=dev),
-                      torch.empty(B, W, dtype=i32, device=dev),
-                      torch.empty(B, dtype=i32, device=dev),
-                      torch.empty(freed, dtype=i32, device=dev),
-                      torch.empty(B + 1, dtype=i32, device=dev),
-                      torch.empty(1, dtype=i32, device=dev))
-        _used_on(stream, *out)
+        out = Evicted(*_memory.empties(dev, stream, ((B, W), torch.float32), ((B, W), i32), (B, i32),
+                                       (freed, i32), (B + 1, i32), (1, i32)))
     else:
         _need(out.scores, "out.scores", torch.float32, 2, dev)
         for name in ("slot_table", "kv_len", "freed_slots", "freed_indptr", "status"):

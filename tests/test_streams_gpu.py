@@ -1,0 +1,89 @@
+"""Memory that a call on another stream makes for itself: a block that was freed on the
+current stream, where queued work still uses it, is not written by the call."""
+import pytest
+import torch
+
+import sink_sda_decode_gb300 as sda
+
+pytestmark = pytest.mark.gpu
+
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+def paged():
+    q = torch.randn(64, 16, 512, device="cuda").to(torch.bfloat16)
+    pool = torch.randn(4096, 512, device="cuda").to(torch.bfloat16)
+    table = torch.arange(4096, **I32).view(1, 4096)
+    ptr, n = torch.tensor([0, 64], **I32), torch.tensor([4096], **I32)
+    lse, scores = torch.zeros(64, 16, device="cuda"), torch.rand(1, 4096, device="cuda")
+    sink = torch.zeros(16, device="cuda")
+    attend = lambda s: sda.chunk_attention(q, pool, table, ptr, n, sink, 0.04, k_per_block=1, stream=s)
+    return {"attend": attend,
+            "mass": lambda s: (sda.attention_mass(q, pool, table, ptr, n, lse, 0.04, k_per_block=1, stream=s),),
+            "evict": lambda s: tuple(sda.evict_slots(scores, table, n, 1000, stream=s))}
+
+
+def check_untouched(call):
+    """Copies of what lay in the call's own blocks before, made by work that is queued on
+    the current stream when the blocks are freed and the call runs on another."""
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    call(side)  # (what is made once)
+    torch.cuda.synchronize()
+    before = [torch.full_like(t, 3) for t in want]
+    ws = torch.full((64 << 20,), 3, dtype=torch.uint8, device="cuda")  # workspaces are cut from it, if from any
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)  # 0.2 s: the copies wait behind it
+    copies = [t.clone() for t in before + [ws]]
+    del before, ws
+    got = call(side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()  # the copies are still to be made
+    torch.cuda.synchronize()
+    for t in copies:
+        assert bool((t == 3).all())
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def check_not_given_away(call):
+    """A result that is dropped while work on the current stream still reads it."""
+    want = call(None)[0].clone()
+    side = torch.cuda.Stream()
+    call(side)
+    torch.cuda.synchronize()
+    got = call(side)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(400_000_000)
+    copy = got.clone()
+    shape, dtype = got.shape, got.dtype
+    del got
+    with torch.cuda.stream(side):
+        torch.full(shape, 3, dtype=dtype, device="cuda")
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
+
+
+@pytest.mark.parametrize("op", ["attend", "mass", "evict"])
+def test_paged_operators(op):
+    check_untouched(paged()[op])
+    check_not_given_away(paged()[op])
+
+
+def test_two_calls_without_a_workspace_on_two_streams():
+    """The first call's workspace is dropped, its kernels still to run, when the second
+    call makes its own."""
+    call = paged()["attend"]
+    want = call(None)
+    side = torch.cuda.Stream()
+    call(side)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        torch.cuda._sleep(20_000_000)
+        a = call(None)
+        b = call(side)
+        torch.cuda.synchronize()
+        for x in (a, b):
+            assert torch.equal(x[0], want[0]) and torch.equal(x[1], want[1])
