@@ -18,7 +18,7 @@ import ctypes
 
 import torch
 
-from . import _lib
+from . import _lib, _memory
 from .paged import (Evicted, attention_mass, attention_mass_workspace_size, chunk_attention,
                     chunk_attention_workspace_size, evict_slots, paged_error_flag)
 
@@ -38,13 +38,8 @@ def _stream_ptr(stream) -> int:
 
 
 def _workspace_for(nbytes: int, dev, stream) -> torch.Tensor:
-    """A workspace from torch's caching allocator that the allocator knows is
-    in use on `stream` (the stream the kernels run on), so that the block is
-    not handed out again while those kernels may still touch it."""
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
-    if isinstance(stream, torch.cuda.Stream):
-        ws.record_stream(stream)
-    return ws
+    """A workspace for kernels on `stream`, from torch's caching allocator."""
+    return _memory.workspace(max(int(nbytes), 256), dev, stream)
 
 
 def _req(t: torch.Tensor, name: str, dtype, ndim=None, device=None):
@@ -97,7 +92,7 @@ def decode(q: torch.Tensor, unified_kv: torch.Tensor, kv_indices: torch.Tensor,
     if kv_indptr.numel() != N + 1 or attn_sink.numel() != H:
         raise ValueError("kv_indptr must have N+1 entries and attn_sink H entries")
     if out is None:
-        out = torch.empty_like(q)
+        out = _memory.empty(q.shape, q.dtype, dev, stream)
     else:
         _req(out, "out", torch.bfloat16, 3, dev)
         if out.shape != q.shape:
@@ -154,7 +149,7 @@ def decode_fp8(q: torch.Tensor, kv_fp8: torch.Tensor, kv_scale: torch.Tensor,
     if kv_indptr.numel() != N + 1 or attn_sink.numel() != H:
         raise ValueError("kv_indptr must have N+1 entries and attn_sink H entries")
     if out is None:
-        out = torch.empty_like(q)
+        out = _memory.empty(q.shape, q.dtype, dev, stream)
     else:
         _req(out, "out", torch.bfloat16, 3, dev)
         if out.shape != q.shape:
@@ -276,11 +271,11 @@ def build_indices(state_slot, swa_len, swa_head, comp_indptr, comp_block, comp_s
     if capacity is None:
         capacity = N * int(win) + comp_block.numel()
     if kv_indices is None:
-        kv_indices = torch.empty(max(int(capacity), 1), dtype=torch.int32, device=dev)
+        kv_indices = _memory.empty(max(int(capacity), 1), torch.int32, dev, stream)
     if kv_indptr is None:
-        kv_indptr = torch.empty(N + 1, dtype=torch.int32, device=dev)
+        kv_indptr = _memory.empty(N + 1, torch.int32, dev, stream)
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
+        status = _memory.empty(1, torch.int32, dev, stream)
     with torch.cuda.device(dev):
         rc = lib.sda_build_indices(
             state_slot.data_ptr(), swa_len.data_ptr(), swa_head.data_ptr(), comp_indptr.data_ptr(),
@@ -324,13 +319,13 @@ def build_decode(q, unified_kv, attn_sink, softmax_scale, state_slot, swa_len, s
     if capacity is None:
         capacity = N * int(win) + comp_block.numel()
     if kv_indices is None:
-        kv_indices = torch.empty(max(int(capacity), 1), dtype=torch.int32, device=dev)
+        kv_indices = _memory.empty(max(int(capacity), 1), torch.int32, dev, stream)
     if kv_indptr is None:
-        kv_indptr = torch.empty(N + 1, dtype=torch.int32, device=dev)
+        kv_indptr = _memory.empty(N + 1, torch.int32, dev, stream)
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
+        status = _memory.empty(1, torch.int32, dev, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _memory.empty(q.shape, q.dtype, dev, stream)
     if workspace is None:
         size = (workspace_size if kv_scale is None else workspace_size_fp8)(N, H, D, int(capacity))
         workspace = _workspace_for(size, dev, stream)
@@ -460,7 +455,7 @@ def validate_indices(kv_indices, kv_indptr, total_pages, status=None, stream=Non
     dev = kv_indptr.device
     _req(kv_indices, "kv_indices", torch.int32, 1, dev)
     if status is None:
-        status = torch.empty(2, dtype=torch.int32, device=dev)
+        status = _memory.empty(2, torch.int32, dev, stream)
     with torch.cuda.device(dev):
         rc = lib.sda_validate_indices(kv_indices.data_ptr() if kv_indices.numel() else None,
                                       kv_indices.numel(), kv_indptr.data_ptr(),
@@ -488,13 +483,13 @@ def topk_slots(scores, lengths, block_table, *, k, k_per_block, capacity=None, c
     if capacity is None:
         capacity = N * int(k)
     if comp_indptr is None:
-        comp_indptr = torch.empty(N + 1, dtype=torch.int32, device=dev)
+        comp_indptr = _memory.empty(N + 1, torch.int32, dev, stream)
     if comp_block is None:
-        comp_block = torch.empty(max(int(capacity), 1), dtype=torch.int32, device=dev)
+        comp_block = _memory.empty(max(int(capacity), 1), torch.int32, dev, stream)
     if comp_slot is None:
-        comp_slot = torch.empty(max(int(capacity), 1), dtype=torch.int32, device=dev)
+        comp_slot = _memory.empty(max(int(capacity), 1), torch.int32, dev, stream)
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
+        status = _memory.empty(1, torch.int32, dev, stream)
     with torch.cuda.device(dev):
         rc = lib.sda_topk_slots(scores.data_ptr() if scores.numel() else None, S,
                                 lengths.data_ptr() if N else None,
@@ -548,13 +543,13 @@ def qk_norm_rope_swa_store(q, kv, q_norm_w, kv_norm_w, cos_cache, sin_cache, pos
         if kv_fp8.shape[1] != D or kv_scale.numel() != total_pages:
             raise ValueError("kv_fp8 must be [total_pages, D] and kv_scale [total_pages]")
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _memory.empty(q.shape, q.dtype, dev, stream)
     else:
         _req(q_out, "q_out", torch.bfloat16, 3, dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
+        status = _memory.empty(1, torch.int32, dev, stream)
     common = (q.data_ptr(), kv.data_ptr(), q_norm_w.data_ptr(), kv_norm_w.data_ptr(),
               cos_cache.data_ptr() if cos_cache.numel() else None,
               sin_cache.data_ptr() if sin_cache.numel() else None, int(max_pos),

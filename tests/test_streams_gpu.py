@@ -3,7 +3,9 @@ current stream, where queued work still uses it, is not written by the call."""
 import pytest
 import torch
 
+import parity
 import sink_sda_decode_gb300 as sda
+from sink_sda_decode_gb300 import inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +89,38 @@ def test_two_calls_without_a_workspace_on_two_streams():
         torch.cuda.synchronize()
         for x in (a, b):
             assert torch.equal(x[0], want[0]) and torch.equal(x[1], want[1])
+
+
+def path(op):
+    """The calls of the decode path, with the part of each result that is defined whole."""
+    w = inputs.config(1, device="cuda")
+    if op == "decode":
+        idx, ptr = parity.to_dev(w)
+        return lambda s: (sda.decode(w.q, w.unified_kv, idx, ptr, w.attn_sink, w.softmax_scale, stream=s),)
+    if op == "fp8":
+        idx, ptr = parity.to_dev(w)
+        pool = inputs.fp8_pool(w)
+        return lambda s: (sda.decode_fp8(w.q, pool.codes, pool.scale, idx, ptr, w.attn_sink, w.softmax_scale,
+                                         stream=s),)
+    if op in ("build", "build_decode"):
+        bi = w.builder_inputs("cuda")
+        kw = dict(win=w.win, k_per_block=w.k_per_block, swa_pages=w.swa_pages)
+        if op == "build":
+            return lambda s: sda.build_indices(**bi, **kw, total_pages=w.total_pages, stream=s)[1:]
+        names = ("state_slot", "swa_len", "swa_head", "comp_indptr", "comp_block", "comp_slot")
+        return lambda s: sda.build_decode(w.q, w.unified_kv, w.attn_sink, w.softmax_scale, *(bi[x] for x in names),
+                                          **kw, stream=s)[::2]
+    if op == "topk":
+        ti = inputs.topk_inputs(w)
+        return lambda s: sda.topk_slots(ti.scores, ti.lengths, ti.block_table, k=ti.k, k_per_block=w.k_per_block,
+                                        stream=s)[::3]
+    si = inputs.store_inputs(w)
+    return lambda s: sda.qk_norm_rope_swa_store(w.q, si.kv_new, si.q_norm_w, si.kv_norm_w, si.cos_cache, si.sin_cache,
+                                                si.positions, si.state_slot, eps=si.eps, win=w.win,
+                                                swa_pages=w.swa_pages, unified_kv=w.unified_kv, stream=s)
+
+
+@pytest.mark.parametrize("op", ["decode", "fp8", "build", "build_decode", "topk", "store"])
+def test_decode_path(op):
+    check_untouched(path(op))
+    check_not_given_away(path(op))
