@@ -217,11 +217,16 @@ def decode_error_flag(workspace: torch.Tensor, stream=None) -> int:
     0 = fine; 1 = a pipeline wait timed out; 2 = kv_indptr was not a prefix
     sum inside [0, len(kv_indices)] (nothing was computed)."""
     lib = _lib.load()
-    flag = torch.zeros(1, dtype=torch.int32, device=workspace.device)
-    with torch.cuda.device(workspace.device):
+    dev = workspace.device
+    with torch.cuda.device(dev):
+        flag = torch.zeros(1, dtype=torch.int32, device=dev)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream(dev))
         _lib.check(lib.sda_decode_error_flag(workspace.data_ptr(), flag.data_ptr(),
                                              _stream_ptr(stream)), "sda_decode_error_flag")
-    return int(flag.item())
+        if stream is not None:
+            stream.synchronize()
+        return int(flag.item())
 
 
 def debug_wait_fault(withhold_arrive: bool, timeout_ns: int = 0) -> None:

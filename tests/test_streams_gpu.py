@@ -124,3 +124,18 @@ def path(op):
 def test_decode_path(op):
     check_untouched(path(op))
     check_not_given_away(path(op))
+
+
+def test_error_word_of_decode_on_another_stream():
+    """It is that of the call, also while the call still waits on its stream."""
+    w = inputs.random_small(seed=90, N=2, H=16, D=512, P=100, lengths=[3, 4], device="cuda")
+    idx, ptr = parity.to_dev(w)
+    ws = torch.empty(sda.workspace_size(w.N, w.H, w.D, idx.numel()), dtype=torch.uint8, device="cuda")
+    bad = torch.tensor([0, 5, 4], **I32)  # no prefix sums
+    side = torch.cuda.Stream()
+    for p, word in ((bad, 2), (ptr, 0)):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        sda.decode(w.q, w.unified_kv, idx, p, w.attn_sink, w.softmax_scale, workspace=ws, stream=side)
+        assert sda.decode_error_flag(ws, side) == word
