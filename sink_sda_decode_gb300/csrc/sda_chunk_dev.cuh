@@ -251,14 +251,21 @@ __device__ __forceinline__ int seen_row(const ChunkParams& p, int* error, const 
 // 16 positions lie in one block (tiles and blocks start at multiples of 16) and
 // so in 16 pool rows in a row.  A box that no row sees is read from behind the
 // pool, which fills it with zeros.
+// x: a position of the box that is seen, and whose row is r (-1: outside the pool);
+// last: the last one that is.  The pool may end in the middle of a box (it holds groups
+// of 8): what lies behind is filled with zeros, and raises the error word if it is seen.
+__device__ __forceinline__ int group_of_box(const ChunkGeom& g, int* error, int j, int x, int r, int last) {
+  if (r < 0) return (int)((g.total_pages - g.base) / 8);
+  if ((long long)r + (last - x) >= g.total_pages) atomicExch(error, 3);
+  return (int)((r - (x - j) - g.base) / 8);
+}
 template <typename C>
 __device__ __forceinline__ int box_group(const ChunkParams& p, int* error, const C& c, int j) {
-  const int behind = (int)((p.g.total_pages - p.g.base) / 8);
-  int x = j;  // the box's first position that is seen, if any, tells its block
+  int x = j, last = min(j + 15, c.hi - 1);  // the first and the last that are seen, if any
+  if (last < c.lo) last = min(last, p.g.first - 1);
   if (x < c.lo && x >= p.g.first) x = c.lo;
-  if (x >= j + 16) return behind;
-  const int r = seen_row(p, error, c, x);
-  return r < 0 ? behind : (int)((r - (x - j) - p.g.base) / 8);
+  const int r = x > last ? -1 : pool_row_of(p.g, error, c.b, x);
+  return group_of_box(p.g, error, j, x, r, last);
 }
 
 ChunkParams chunk_params(const void* kv, const ChunkGeom& g, const float* attn_sink, float scale,
