@@ -463,8 +463,9 @@ sda_status sda_qk_norm_rope_swa_store_fp8(const void* q, const void* kv, const v
  *               and lse outside [q_indptr[0], q_indptr[B]) are not written
  *   kv_len      [B] int32 in [0, max_blocks * k_per_block], at most 2^31 - 512
  *   attn_sink   [H] fp32 sink logits (-inf: no sink)
- *   out         [T, H, D] bf16, 16-byte aligned; lse [T, H] fp32; they overlap
- *               neither each other nor anything that is read
+ *   out         [T, H, D] bf16, 16-byte aligned; lse [T, H] fp32; they and the
+ *               workspace overlap neither each other nor anything that is read
+ *               (SDA_ERR_INVALID_ARG)
  * The device error word (sda_paged_error_flag on the workspace): 2 = q_indptr
  * or kv_len broke the contract, or more than 2^31 - 1 tiles of up to 64
  * positions by up to 128 rows (nothing computed); 3 = a table entry pointed
@@ -502,8 +503,8 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
  *   lse   [T, H] fp32
  *   prev  [B, S] fp32, S = max_blocks * k_per_block <= 2^31 - 512, or NULL for
  *         zeros
- *   out   [B, S] fp32; may be prev itself, must not otherwise overlap what is
- *         read
+ *   out   [B, S] fp32; may be prev itself; otherwise out and the workspace
+ *         overlap neither each other nor anything that is read
  * T may be 0 (q and lse may then be NULL): out = decay * prev.  Error word and
  * workspace as sda_chunk_attention (word 2: lengths outside the contract, out
  * without any weight added).  The timing hook brackets all of its launches.

@@ -974,6 +974,13 @@ static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
+// The small arrays that the CTAs of a paged-cache call read at any time.
+static bool overlaps_tables(const ChunkGeom& g, const void* p, size_t n) {
+  return overlaps(g.block_table, static_cast<size_t>(g.B) * g.max_blocks * 4, p, n) ||
+         overlaps(g.q_indptr, (static_cast<size_t>(g.B) + 1) * 4, p, n) ||
+         overlaps(g.kv_len, static_cast<size_t>(g.B) * 4, p, n);
+}
+
 sda_status sda_paged_error_flag(const void* workspace, int32_t* device_flag, void* stream) {
   if (!workspace || !device_flag || !aligned(workspace, 256) || !aligned(device_flag, 4))
     return SDA_ERR_INVALID_ARG;
@@ -1028,6 +1035,10 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
       overlaps(unified_kv, pn, lse, ln) || overlaps(out, on, lse, ln))
     return SDA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return SDA_ERR_WORKSPACE;
+  const size_t sn = static_cast<size_t>(H) * 4;
+  if (overlaps_tables(g, out, on) || overlaps_tables(g, lse, ln) || overlaps(attn_sink, sn, out, on) ||
+      overlaps(attn_sink, sn, lse, ln))
+    return SDA_ERR_INVALID_ARG;
   DeviceCaps caps;
   cudaError_t e = paged_caps(kOpAttention, &caps);
   if (e != cudaSuccess) {
@@ -1036,6 +1047,10 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
   }
   const ChunkLayout L = chunk_layout(g, caps.num_sms);
   if (workspace_bytes < L.total) return SDA_ERR_WORKSPACE;
+  if (overlaps(q, on, workspace, L.total) || overlaps(unified_kv, pn, workspace, L.total) ||
+      overlaps_tables(g, workspace, L.total) || overlaps(attn_sink, sn, workspace, L.total) ||
+      overlaps(out, on, workspace, L.total) || overlaps(lse, ln, workspace, L.total))
+    return SDA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   e = launch_chunk_plan(g, L, workspace, st);
   if (e == cudaSuccess && g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_before, st);
@@ -1099,9 +1114,9 @@ sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t tot
   // out is prev itself or apart from it, and apart from what all CTAs read
   const size_t nb = static_cast<size_t>(B) * S * 4, rows = static_cast<size_t>(T) * H;
   if (prev && prev != out && overlaps(prev, nb, out, nb)) return SDA_ERR_INVALID_ARG;
-  if (overlaps(q, rows * D * 2, out, nb) || overlaps(lse, rows * 4, out, nb) ||
-      overlaps(unified_kv, static_cast<size_t>(total_pages) * D * 2, out, nb) ||
-      overlaps(block_table, static_cast<size_t>(B) * max_blocks * 4, out, nb))
+  const size_t qn = rows * D * 2, pn = static_cast<size_t>(total_pages) * D * 2;
+  if (overlaps(q, qn, out, nb) || overlaps(lse, rows * 4, out, nb) || overlaps(unified_kv, pn, out, nb) ||
+      overlaps_tables(g, out, nb))
     return SDA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return SDA_ERR_WORKSPACE;
   DeviceCaps caps;
@@ -1112,6 +1127,10 @@ sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t tot
   }
   const MassLayout L = mass_layout(B, S, caps.num_sms);
   if (workspace_bytes < L.total) return SDA_ERR_WORKSPACE;
+  if (overlaps(q, qn, workspace, L.total) || overlaps(lse, rows * 4, workspace, L.total) ||
+      overlaps(unified_kv, pn, workspace, L.total) || overlaps_tables(g, workspace, L.total) ||
+      overlaps(prev, prev ? nb : 0, workspace, L.total) || overlaps(out, nb, workspace, L.total))
+    return SDA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (g_ev_before && g_ev_after) e = cudaEventRecord(g_ev_before, st);
   if (e == cudaSuccess)

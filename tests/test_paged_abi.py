@@ -143,3 +143,33 @@ def test_python_refuses_sizes_that_do_not_fit():
         sda.chunk_attention_workspace_size(2 ** 31, 1, 1, 64)
     with pytest.raises(ValueError):
         sda.attention_mass_workspace_size(1, 1, 0)
+
+
+# every array in a place of its own, 1 MB apart at least: (pointer, bytes)
+APART = dict(table=(1 << 26, 2 * 4 * 4), indptr=(1 << 27, 3 * 4), kv_len=(1 << 28, 2 * 4))
+
+
+@pytest.mark.parametrize("name,size", [(k, n) for k, (_, n) in APART.items()] + [("sink", 16 * 4)])
+@pytest.mark.parametrize("result", ["out", "lse"])
+def test_results_of_chunk_attention_are_apart_from_tables(lib, name, size, result):
+    at = {k: p for k, (p, _) in APART.items()}
+    at.update(sink=1 << 29, lse=1 << 30, out=1 << 31, ws=1 << 40)
+    long = {"out": 3 * 16 * 512 * 2, "lse": 3 * 16 * 4}[result]
+    for where in (at[name] - long + 16, at[name], at[name] + (size - 1) // 16 * 16):  # 16-byte aligned
+        assert attend(lib, **dict(at, **{result: where})) == INVALID
+    if lib.sda_chunk_attention_workspace_size(2, 3, 16, 512, ctypes.byref(ctypes.c_size_t(0))) != OK:
+        # (without a GPU nothing is enqueued: what is apart gets as far as the device)
+        for where in (at[name] - long, at[name] + (size + 15) // 16 * 16):
+            assert attend(lib, **dict(at, **{result: where})) not in (OK, INVALID)
+
+
+@pytest.mark.parametrize("name", list(APART))
+def test_out_of_attention_mass_is_apart_from_tables(lib, name):
+    at = {k: p for k, (p, _) in APART.items()}
+    at.update(lse=1 << 30, out=1 << 31, ws=1 << 40)
+    at_name, size = APART[name]
+    for where in (at_name - 2 * 64 * 4 + 4, at_name, at_name + size - 4):
+        assert mass(lib, **dict(at, out=where)) == INVALID
+    if lib.sda_attention_mass_workspace_size(2, 4, 16, ctypes.byref(ctypes.c_size_t(0))) != OK:
+        for where in (at_name - 2 * 64 * 4, at_name + size):
+            assert mass(lib, **dict(at, out=where)) not in (OK, INVALID)

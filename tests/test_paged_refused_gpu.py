@@ -54,3 +54,44 @@ def test_more_tiles_than_are_counted_after_a_call_that_cut_units():
                             k_per_block=2 ** 30, out=out, lse=lse, workspace=ws)
         assert sda.paged_error_flag(ws) == error
         assert bool((out == 7).all()) == bool(error) and bool((lse == 7).all()) == bool(error)
+
+
+@pytest.mark.parametrize("what", ["q", "pool", "table", "q_indptr", "kv_len", "sink", "out", "lse", "prev"])
+def test_workspace_is_apart(what):
+    """A workspace that begins, or ends, inside an array of the call is refused."""
+    c = Case(62, m=[2, 3], n=[100, 200], H=16, D=512, K=16)
+    lse = torch.zeros(5, 16, device="cuda")
+    S = c.table.shape[1] * 16
+    sizes = {"attend": sda.chunk_attention_workspace_size(2, 5, 16, 512),
+             "mass": sda.attention_mass_workspace_size(2, c.table.shape[1], 16)}
+
+    def call(op, a, ws):
+        t = (a.get("q", c.q), a.get("pool", c.pool), a.get("table", c.table), a.get("q_indptr", c.q_indptr),
+             a.get("kv_len", c.kv_len))
+        if op == "attend":
+            sda.chunk_attention(*t, a.get("sink", c.sink), c.scale, k_per_block=16, out=a.get("out"),
+                                lse=a.get("lse"), workspace=ws)
+        else:
+            sda.attention_mass(*t, a.get("lse", lse), c.scale, k_per_block=16, scores=a.get("prev"),
+                               out=a.get("out"), workspace=ws)
+
+    for op in ("attend", "mass"):
+        if what in {"attend": ("prev",), "mass": ("sink",)}[op]:
+            continue
+        like = {"out": c.q if op == "attend" else torch.zeros(2, S, device="cuda"), "lse": lse,
+                "prev": torch.zeros(2, S, device="cuda")}.get(what)
+        like = getattr(c, what) if like is None else like
+        n, size = like.numel() * like.element_size(), sizes[op]
+        room = (n + 255) // 256 * 256
+        buf = torch.zeros(2 * room + size, dtype=torch.uint8, device="cuda")
+        for at in (0, (room + size - n) // 256 * 256):  # the array's first byte; the workspace's is room's last 256
+            begin = room - 256 if at == 0 else room
+            t = buf[at:at + n].view(like.dtype).view(like.shape).copy_(like)
+            ws = buf[begin:begin + size]
+            overlap = at < begin + size and begin < at + n
+            assert overlap
+            with pytest.raises(sda._lib.SdaError):
+                call(op, {what: t}, ws)
+        t = buf[:n].view(like.dtype).view(like.shape).copy_(like)
+        call(op, {what: t}, buf[room:room + size])  # one behind the other
+        assert sda.paged_error_flag(buf[room:room + size]) == 0
