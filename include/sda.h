@@ -532,7 +532,8 @@ sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t tot
  *               sequence in increasing position; behind freed_indptr[B]: -1
  * Arguments (device pointers): scores [B, stride] fp32, slot_table [B, stride]
  * int32 (entries behind kv_len are not read), kv_len [B] int32 in [0, stride]
- * (outside: counts as 0, status bit 1); 0 <= first + recent <= budget;
+ * (outside: counts as 0, status bit 1); stride <= 2^31 - 2048, B <= 2^24;
+ * 0 <= first + recent <= budget;
  * out_stride >= min(stride, budget); freed_capacity >= B * max(stride -
  * budget, 0), at most 2^31 - 1.  out_scores / out_table / out_len may be
  * scores / slot_table / kv_len themselves (with out_stride = stride) and must

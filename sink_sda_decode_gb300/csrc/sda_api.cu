@@ -1148,8 +1148,8 @@ sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64
                            float* out_scores, int32_t* out_table, int64_t out_stride,
                            int32_t* out_len, int32_t* freed_slots, int64_t freed_capacity,
                            int32_t* freed_indptr, int32_t* status, void* stream) {
-  if (B < 0 || stride < 0 || stride > 0x7fffffffll || budget < 0 || first < 0 || recent < 0 ||
-      out_stride < 0 || out_stride > 0x7fffffffll || freed_capacity < 0)
+  if (B < 0 || B > (1 << 24) || stride < 0 || stride > kMaxEvictLen || budget < 0 || first < 0 ||
+      recent < 0 || out_stride < 0 || out_stride > 0x7fffffffll || freed_capacity < 0)
     return SDA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(first) + recent > budget) return SDA_ERR_INVALID_ARG;
   const int64_t most = stride > budget ? stride - budget : 0;  // slots a sequence can free

@@ -5,6 +5,10 @@
 
 namespace sda {
 
+// Most columns of a table: the kernels step over them by up to 1024, counted in 32 bits
+// (a step past the last of 2^31 - 1 would have wrapped round to negative positions).
+constexpr int64_t kMaxEvictLen = 0x7fffffff - 2047;
+
 struct EvictArgs {
   const float* scores;   // [B, S]
   const int32_t* slots;  // [B, S]

@@ -173,3 +173,16 @@ def test_out_of_attention_mass_is_apart_from_tables(lib, name):
     if lib.sda_attention_mass_workspace_size(2, 4, 16, ctypes.byref(ctypes.c_size_t(0))) != OK:
         for where in (at_name - 2 * 64 * 4, at_name + size):
             assert mass(lib, **dict(at, out=where)) not in (OK, INVALID)
+
+
+def test_evict_slots_counts_in_32_bits(lib):
+    """Rows of 2^31 - 2048 columns and 2^24 sequences are the most (every array in a place of its own)."""
+    at = dict(scores=1 << 44, table=1 << 45, kv_len=1 << 46, out_scores=1 << 47, out_table=1 << 48, out_len=1 << 49,
+              freed=1 << 50, indptr=1 << 51, status=1 << 52, budget=2 ** 31 - 4096, first=0, recent=0)
+    for B, stride, refused in ((1, 2 ** 31 - 2047, True), (1, 2 ** 31 - 1, True), (1, 2 ** 31 - 2048, False),
+                               (2 ** 24 + 1, 3, True), (2 ** 31 - 1, 0, True), (2 ** 24, 3, False)):
+        a = dict(at, B=B, stride=stride, out_stride=stride, capacity=4096)
+        if refused:
+            assert evict(lib, **a) == INVALID
+        elif lib.sda_chunk_attention_workspace_size(2, 3, 16, 512, ctypes.byref(ctypes.c_size_t(0))) != OK:
+            assert evict(lib, **a) not in (OK, INVALID)  # (without a GPU: as far as the device)
