@@ -408,7 +408,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const float sinkA = whole && vA ? __ldg(p.attn_sink + un.h0 + hA - tokA * H) : 0.f;
       const float sinkB = whole && vB ? __ldg(p.attn_sink + un.h0 + hB - tokB * H) : 0.f;
       const float scA = vA ? sc : 0.f, scB = vB ? sc : 0.f;
-      float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;  // l: this thread's share
+      float mA = kNoScore, mB = kNoScore, lA = 0.f, lB = 0.f;  // l: this thread's share
       for (int i = i0; i < i1; ++i, ++g) {
         const int s = g & 1;
         const int j0 = chunk_tile_start(i, un.nf, un.lo, kTile);
@@ -560,12 +560,12 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
             eB = fmaxf(eB, hm[(hc ^ 1) * 64 + hB]);
           }
           float alphaA = 1.f, alphaB = 1.f;
-          if (eA > mA + kHeadroom || (mA == -INFINITY && eA > mA)) {
-            alphaA = ex2_approx(mA - eA);  // 0 when m was -inf
+          if (eA > mA + kHeadroom) {
+            alphaA = ex2_approx(mA - eA);  // 0 when there was no score
             lA *= alphaA;
             mA = eA;
           }
-          if (eB > mB + kHeadroom || (mB == -INFINITY && eB > mB)) {
+          if (eB > mB + kHeadroom) {
             alphaB = ex2_approx(mB - eB);
             lB *= alphaB;
             mB = eB;
@@ -626,7 +626,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int w2 = 0; w2 < 2; ++w2) {
           const int r = w2 ? hB : hA;
           if (r >= R) continue;
-          const float m = w2 ? mB : mA;
+          const float mw = w2 ? mB : mA, m = mw == kNoScore ? -INFINITY : mw;
           const float l = s_lsum[r] + s_lsum[64 + r];  // read before fac[r] overwrites s_lsum[64 + r]
           float f = 0.f;
           if (whole) {

@@ -23,6 +23,11 @@ __device__ __forceinline__ uint32_t seen_bits(int pos, int j, int window, int fi
 
 constexpr float kHeadroom = 8.0f;  // log2: the running reference is raised when a score exceeds it by this
 
+// The running reference of a row that has no score yet, finite so that a score of -inf
+// (an overflow, say) has weight 2^-inf = 0 against it too, not 2^(-inf + inf) = NaN.  What
+// is stored of it, or goes into lse, is -inf.
+constexpr float kNoScore = -3.402823466e38f;
+
 struct ChunkParams {
   const __nv_bfloat16* kv;
   const float* attn_sink;

@@ -515,7 +515,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       int pos[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        m[i] = -INFINITY;
+        m[i] = kNoScore;
         l[i] = 0.f;
         // (rows past the unit's end have factor 0: their weights, never used, stay
         // finite and raise nothing)
@@ -635,8 +635,8 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const int r = row0 + 8 * i4;
             const float t = fmaxf(fmaxf(hm[r], hm[64 + r]), fmaxf(hm[128 + r], hm[192 + r]));
             float alpha = 1.f;
-            if (t > m[i4] + kHeadroom || (m[i4] == -INFINITY && t > m[i4])) {
-              alpha = ex2_approx(m[i4] - t);  // 0 when m was -inf
+            if (t > m[i4] + kHeadroom) {
+              alpha = ex2_approx(m[i4] - t);  // 0 when there was no score
               l[i4] *= alpha;
               m[i4] = t;
             }
@@ -681,7 +681,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
         t += __shfl_xor_sync(0xffffffffu, t, 2);
         if (tq == 0) {
           s_l[part * 64 + row0 + 8 * i4] = t;
-          if (part == 0) s_m[row0 + 8 * i4] = m[i4];
+          if (part == 0) s_m[row0 + 8 * i4] = m[i4] == kNoScore ? -INFINITY : m[i4];
         }
       }
       named_bar_sync(1, kSmThreads);
