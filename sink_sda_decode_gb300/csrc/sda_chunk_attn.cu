@@ -166,6 +166,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
   int* const error = reinterpret_cast<int*>(reinterpret_cast<char*>(p.hdr) + kErrorWords) + blockIdx.x;
   if (threadIdx.x == 0) {
     *error = 0;
+    if (bad && p.mode == kCut) p.recs[blockIdx.x] = ChunkUnit{-1};
     if (blockIdx.x == 0) {
       p.hdr->words = gridDim.x;
       if (p.mode != kPlanned) p.hdr->error = bad ? 2 : 0;
@@ -182,9 +183,10 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // prefetches of the tile two ahead into L2, kept this warp busier than the
     // tensor pipe: one TMA instruction costs about 90 cycles of issue.)
     const int behind = (int)((p.g.total_pages - p.g.base) / 8);
+    bool over = false;
     auto box_of = [&](const Walk& c) {
       return lane < C::kBoxes
-                 ? box_group(p, error, c, c.start() + lane * 16)
+                 ? box_group(p, error, c, c.start() + lane * 16, &over)
                  : behind;
     };
     Walk c;  // runs a tile ahead of the copies
@@ -213,6 +215,7 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
         c.next(p.g);
       }
     }
+    if (over) atomicExch(error, 3);
     // copies in flight land before the CTA's memory goes away (the last KS stages)
     for (int x = max(0, loads - KS * HV); x < loads; ++x)
       pipe_drain(kv_full((x / HV) % KS, x % HV), (x / HV / KS) & 1, wc);

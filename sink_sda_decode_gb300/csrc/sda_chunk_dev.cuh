@@ -119,11 +119,6 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long* sums = reinterpret_cast<long long*>(scratch);  // [kW]
   int* found = scratch + 2 * kW;                             // [5]
-  auto refuse = [&]() {
-    *bad = true;
-    if (p.mode == kCut && tid == 0) p.recs[worker] = ChunkUnit{-1};
-    return ChunkStart{0, 0, 0, 0};
-  };
   // exclusive prefix of one value per thread, and the total
   auto scan = [&](long long v, long long* total) {
     long long x = v;
@@ -154,7 +149,8 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
     else mine += units_of(g, R, b);
   }
   long long at = scan(mine, &U);
-  if (__syncthreads_or(wrong)) return refuse();
+  *bad = __syncthreads_or(wrong);
+  if (*bad) return st;
   for (int b = b0; b < b1; ++b) {
     s_seq[b] = (int)at;
     at += units_of(g, R, b);
@@ -193,7 +189,10 @@ __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker,
       }
     }
     const long long tiles = scan(nt, &tt);  // of the units before this stretch
-    if (tt > 0x7fffffffll) return refuse();
+    if (tt > 0x7fffffffll) {
+      *bad = true;
+      return st;
+    }
     const long long cost = tt + U * unit_cost(R);
     const long long per = cost > 0 ? (cost + p.workers - 1) / p.workers : 1;
     const long long mine0 = tiles + (long long)u0 * unit_cost(R);
@@ -256,21 +255,25 @@ __device__ __forceinline__ int seen_row(const ChunkParams& p, int* error, const 
 // 16 positions lie in one block (tiles and blocks start at multiples of 16) and
 // so in 16 pool rows in a row.  A box that no row sees is read from behind the
 // pool, which fills it with zeros.
-// x: a position of the box that is seen, and whose row is r (-1: outside the pool);
-// last: the last one that is.  The pool may end in the middle of a box (it holds groups
-// of 8): what lies behind is filled with zeros, and raises the error word if it is seen.
-__device__ __forceinline__ int group_of_box(const ChunkGeom& g, int* error, int j, int x, int r, int last) {
-  if (r < 0) return (int)((g.total_pages - g.base) / 8);
-  if ((long long)r + (last - x) >= g.total_pages) atomicExch(error, 3);
-  return (int)((r - (x - j) - g.base) / 8);
+// The pool may end in the middle of a box (it holds groups of 8): what lies behind is
+// filled with zeros too, and raises the error word if it is seen.  y: the box's group;
+// last: the last of its positions that is seen.  (Boxes begin at every other group, so
+// the last group is one's first only where its second half does not exist.)
+__device__ __forceinline__ bool ends_behind(const ChunkGeom& g, int y, int j, int last) {
+  return y == (int)((g.total_pages - g.base) / 8) - 1 && last >= j + 8;
 }
 template <typename C>
-__device__ __forceinline__ int box_group(const ChunkParams& p, int* error, const C& c, int j) {
-  int x = j, last = min(j + 15, c.hi - 1);  // the first and the last that are seen, if any
-  if (last < c.lo) last = min(last, p.g.first - 1);
+__device__ __forceinline__ int box_group(const ChunkParams& p, int* error, const C& c, int j, bool* over) {
+  const int behind = (int)((p.g.total_pages - p.g.base) / 8);
+  int x = j;  // the box's first position that is seen, if any, tells its block
   if (x < c.lo && x >= p.g.first) x = c.lo;
-  const int r = x > last ? -1 : pool_row_of(p.g, error, c.b, x);
-  return group_of_box(p.g, error, j, x, r, last);
+  if (x >= j + 16) return behind;
+  const int r = seen_row(p, error, c, x);
+  if (r < 0) return behind;
+  const int y = (int)((r - (x - j) - p.g.base) / 8);
+  const int last = min(j + 15, c.hi - 1);
+  *over |= ends_behind(p.g, y, j, last < c.lo ? min(last, p.g.first - 1) : last);
+  return y;
 }
 
 ChunkParams chunk_params(const void* kv, const ChunkGeom& g, const float* attn_sink, float scale,

@@ -176,6 +176,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
   int* const error = reinterpret_cast<int*>(reinterpret_cast<char*>(p.hdr) + kErrorWords) + blockIdx.x;
   if (threadIdx.x == 0) {
     *error = 0;
+    if (bad && p.mode == kCut) p.recs[worker] = ChunkUnit{-1};
     if (blockIdx.x == 0) {
       p.hdr->words = gridDim.x;
       if (p.mode != kPlanned) p.hdr->error = bad ? 2 : 0;
@@ -202,8 +203,9 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const uint32_t dst0 = keys ? sK + half * C::kKHalf + (lane & 1) * C::kBox : sV + lane * C::kBox;
       const uint32_t bytes = keys ? C::kKBytes : C::kVBytes;
       const int behind = (int)((p.g.total_pages - p.g.base) / 8);
+      bool over = false;
       auto box_of = [&](const Walk& c) {
-        return lane < 4 ? box_group(p, error, c, c.start() + off) : behind;
+        return lane < 4 ? box_group(p, error, c, c.start() + off, &over) : behind;
       };
       Walk c;  // runs a tile ahead of the copies
       c.init(p.g, begin);
@@ -227,6 +229,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
           c.next(p.g);
         }
       }
+      if (over) atomicExch(error, 3);
     } else {
       // ===================================================== passing on landed stages
       for (; g < nt; ++g) {

@@ -688,7 +688,10 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int j = tl.k0 + lane * 16;
       if (lane < 4 && j < tl.n) {
         const int r = pool_row_of(p.g, error, tl.b, j);
-        y = group_of_box(p.g, error, j, j, r, min(j + 15, tl.n - 1));
+        if (r >= 0) {
+          y = (int)((r - p.g.base) / 8);
+          if (ends_behind(p.g, y, j, tl.n - 1)) atomicExch(error, 3);
+        }
       }
       if (g >= KS && !warp_wait(bar(kSkFree0 + s), ((g / KS) - 1) & 1, wc)) return false;
       if (lane == 0) mbar_arrive_expect_tx(bar(kSkFull0 + s), C::kStage);
