@@ -526,7 +526,8 @@ enum StepBar : int {
   kSAccEmpty0 = kSAccFull0 + 2,
   kSkFull0 = kSAccEmpty0 + 2,
   kSkFree0 = kSkFull0 + 6,
-  kSBars = kSkFree0 + 6
+  kSDrain = kSkFree0 + 6,
+  kSBars
 };
 
 template <int R, int D>
@@ -600,6 +601,7 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
   if (tid == 0) {
     mbar_init(bar(kSqFull), 1);
     mbar_init(bar(kSqEmpty), 1);
+    mbar_init(bar(kSDrain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kSAccFull0 + i), 1);
       mbar_init(bar(kSAccEmpty0 + i), 8);
@@ -782,8 +784,14 @@ mass_step_kernel(const __grid_constant__ CUtensorMap tmap_q,
       ++g;
       return true;
     });
-    // this thread's MMAs are done before TMEM and shared memory go away
-    if (g > 0) pipe_drain(bar(kSkFree0 + (g - 1) % KS), ((g - 1) / KS) & 1, wc);
+    // MMAs are done and q has landed before TMEM and shared memory go away, also where a
+    // wait gave up in the middle of a tile
+    if (elect_one()) {
+      mma_commit(bar(kSDrain));
+      pipe_drain(bar(kSDrain), 0, wc);
+      if (q_loads > 0) pipe_drain(bar(kSqFull), (q_loads - 1) & 1, wc);
+    }
+    __syncwarp();
   } else if (warp < 8) {
     // ===================================================== weights and sums
     // 16x256b: thread t holds positions hA = 16 q4 + t / 4 and hB = hA + 8 at the rows
