@@ -193,9 +193,10 @@ sda_status sda_decode_error_flag(const void* workspace, int32_t* device_flag, vo
  * stream immediately before its attention kernel and `after` immediately
  * after it, and every later sda_qk_norm_rope_swa_store(_fp8) / sda_topk_slots
  * does the same around its kernel(s), so that the caller can time them alone
- * (cudaEventElapsedTime).  The events are
- * cudaEvent_t handles created and owned by the caller.  NULL, NULL turns the
- * hook off.  No effect on results.
+ * (cudaEventElapsedTime).  sda_chunk_attention records them around its attention
+ * kernel (not its plan and its merge), sda_attention_mass and sda_evict_slots
+ * around all of their launches.  The events are cudaEvent_t handles created and
+ * owned by the caller.  NULL, NULL turns the hook off.  No effect on results.
  */
 sda_status sda_set_timing_events(void* before, void* after);
 
@@ -451,7 +452,16 @@ sda_status sda_qk_norm_rope_swa_store_fp8(const void* q, const void* kv, const v
  *   out = sum_j e^(x_j - lse) kv_j
  * A row that sees nothing (n_b < m_b, or n_b = 0) gets out = +0 and lse =
  * attn_sink[h]; with attn_sink[h] = +inf out = +0 and lse = +inf.  Infinities
- * and NaN in positions that a row does not see leave the row as it is.
+ * and NaN in positions that a row does not see leave the row as it is.  A row that
+ * sees one gets NaN or, where its score is -inf, no weight from it (an infinite
+ * element may still make that of out NaN).  Scores are fp32: one below its range has
+ * weight 0, one above it makes the row NaN.
+ *
+ * Rows are loaded 16 at a time where k_per_block is a multiple of 16 and the pool
+ * holds, from base on, a multiple of 8 rows; else one by one, which is slower (a
+ * token of 64 heads over 8 caches of up to 65536 positions 120 us in place of 89, a
+ * prompt of 4 x 512 tokens over 4096 positions 1162 in place of 730): round the pool
+ * up to whole groups of 8 rows.
  *
  * Arguments (device pointers):
  *   q           [T, H, D] bf16, 16-byte aligned; D in {64, 128, 256, 512},
@@ -505,6 +515,9 @@ sda_status sda_chunk_attention(const void* q, const void* unified_kv, int64_t to
  *         zeros
  *   out   [B, S] fp32; may be prev itself; otherwise out and the workspace
  *         overlap neither each other nor anything that is read
+ * All S columns of out are written on every call: tables much wider than their
+ * sequences cost their width (one token of 64 sequences of 513 to 767 positions: 16 us
+ * with 768 columns, 55 with 131072).
  * T may be 0 (q and lse may then be NULL): out = decay * prev.  Error word and
  * workspace as sda_chunk_attention (word 2: lengths outside the contract, out
  * without any weight added).  The timing hook brackets all of its launches.
@@ -539,6 +552,9 @@ sda_status sda_attention_mass(const void* q, const void* unified_kv, int64_t tot
  * scores / slot_table / kv_len themselves (with out_stride = stride) and must
  * not otherwise overlap what is read; no two outputs overlap.  *status (device int32, overwritten):
  * bits 1 (bad length), 8 (a NaN competed).  Graph-capturable, no workspace.
+ * All of out_scores, out_table and freed_slots is written: a table much wider than
+ * its sequences costs its width (64 sequences of 513 to 767 positions cut to 512: 11
+ * us with 768 columns, 39 with 131072).
  */
 sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64_t stride,
                            const int32_t* kv_len, int B, int budget, int first, int recent,

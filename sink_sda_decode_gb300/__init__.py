@@ -241,9 +241,9 @@ def debug_wait_fault(withhold_arrive: bool, timeout_ns: int = 0) -> None:
 
 def set_timing_events(before: torch.cuda.Event | None, after: torch.cuda.Event | None) -> None:
     """Record `before` / `after` around the attention kernel of every later
-    decode() / decode_fp8() and around the kernel of every later
-    qk_norm_rope_swa_store() / topk_slots() on this thread (None, None turns
-    it off).
+    decode() / decode_fp8() / chunk_attention() and around the kernels of every
+    later qk_norm_rope_swa_store() / topk_slots() / attention_mass() /
+    evict_slots() on this thread (None, None turns it off).
     Events must be created with enable_timing=True."""
     lib = _lib.load()
     handles = []

@@ -459,7 +459,8 @@ chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
           // A cached row with an infinity or NaN that some row of this tile
           // does not see: its weight there is 0, but 0 x inf = NaN in the MMA.
           // Such rows are cleared in shared memory (the rows that do see it
-          // have a NaN weight already), after the QK MMAs have read them.
+          // have a NaN weight already, or 0 where the score is -inf), after the QK MMAs
+          // have read them.
           if (named_bar_or(1, kSmThreads, poison)) {
             uint8_t* stage = smem + C::kOffKV + (g % KS) * C::kStage;
             const int r = st >> 2, part = st & 3;  // 4 threads per cached row

@@ -13,7 +13,7 @@
 // key (32 rows, all of D) and as value (64 rows, half of D); the two rings are freed
 // by different MMAs, so that the keys of the next tile land while the weights of
 // this one are computed.  2048 tokens of 64 heads over 8192 positions, D = 512 (1.92
-// TFLOP): 1.32 to 1.37 ms between runs, about 1400 TFLOP/s, against 2.09 ms with
+// TFLOP): 1.32 to 1.39 ms between runs, about 1400 TFLOP/s, against 2.09 ms with
 // one CTA a tile and tiles multicast to two CTAs.  A tile takes about 1600 cycles, 1365
 // of them MMAs.
 //
@@ -479,7 +479,7 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (cmd & kPoison) {
         // Values with an infinity or NaN, which some row does not see: its weight
         // there is 0, but 0 x inf = NaN in the MMA.  They are cleared; the rows that
-        // do see them have a NaN weight already.
+        // do see them have a NaN weight already, or 0 where the score is -inf.
         const int r = st >> 2, part4 = st & 3;  // 4 threads per row
         auto chunk = [&](int ch) {
           return reinterpret_cast<uint4*>(smem + C::kOffV + (x % KS) * C::kVBytes + (r >> 3) * C::kGroup +
@@ -693,7 +693,8 @@ chunk_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // the factors of the piece before have been read in both CTAs
       if (pieces > 0) warp_wait(bar(kODone), (pieces - 1) & 1, wc);
       if (st < kR) {
-        const float ml = s_m[st], mr = ml == kNoScore ? -INFINITY : ml, lr = (s_l[st] + s_l[64 + st]) + (s_l[128 + st] + s_l[192 + st]);
+        const float mp = s_m[st], mr = mp == kNoScore ? -INFINITY : mp;
+        const float lr = (s_l[st] + s_l[64 + st]) + (s_l[128 + st] + s_l[192 + st]);
         float f = 0.f;
         if (whole) {
           if (st < nrows) {

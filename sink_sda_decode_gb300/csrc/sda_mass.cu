@@ -25,7 +25,7 @@
 // mass_step_kernel, for steps of few rows: see there.
 //
 // Measured, 2 sequences of 500 to 600 tokens over 6000 to 8192 positions, 64 heads,
-// D = 512 (542 GFLOP): 287 to 325 us, 1890 to 1670 TFLOP/s between runs, the tensor
+// D = 512 (542 GFLOP): 285 to 328 us, 1900 to 1650 TFLOP/s between runs, the tensor
 // pipe active 94 % of the cycles.  One CTA to 128 positions took 744 us; pairs
 // with 8 epilogue warps 488 (the weights set the pace), with 16 warps 396, and with a
 // range of rows per position in place of masks tested per weight 287.
@@ -999,7 +999,11 @@ cudaError_t launch_mass(const void* q, const void* kv, const ChunkGeom& g, const
   float* part = reinterpret_cast<float*>(base + L.part_off);
   const int64_t S = (int64_t)g.max_blocks * g.k_per_block;
   // Up to 64 rows a sequence on average: their scores with a tile of positions are one
-  // MMA tile, and the time is that of reading the cache once.
+  // MMA tile, and the time is that of reading the cache once.  (q_indptr lies on the
+  // device, so the rule goes by the average.  A batch whose rows are all in one sequence
+  // reloads them, 64 at a time, for every tile of its positions: 64 sequences of 4096
+  // positions, 64 heads, 64 tokens in one and none in the others, D = 512, 96 us, where
+  // 65 tokens, by the kernel for chunks, take 27; one token in each takes 49.)
   if (g.T > 0 && (int64_t)g.T * g.H <= (int64_t)64 * g.B && g.B <= kStepSeqs)
     return launch_mass_step(q, kv, g, lse, scale, prev, decay, out, 2 * L.grid, ws, st);
   const int64_t fill = (g.B * S + kPlanThreads - 1) / kPlanThreads;

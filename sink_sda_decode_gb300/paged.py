@@ -115,7 +115,9 @@ def chunk_attention(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torc
     [H] fp32 sink logits.  Returns (out [T, H, D] bf16, lse [T, H] fp32, the log
     of the softmax denominator, sink included).  A row that sees nothing gets
     out = 0 and lse = the sink; rows outside [q_indptr[0], q_indptr[B]) are not
-    written.  H up to 256, D in {64, 128, 256, 512}.
+    written.  H up to 256, D in {64, 128, 256, 512}.  Fast where k_per_block is a
+    multiple of 16 and unified_kv holds, from `base` on, a multiple of 8 rows; else
+    cached rows are loaded one by one.
 
     Asynchronous on `stream`.  With out, lse and `workspace` (uint8, at least
     chunk_attention_workspace_size(...) bytes) given the call allocates nothing
@@ -209,6 +211,7 @@ def attention_mass(q: torch.Tensor, unified_kv: torch.Tensor, block_table: torch
     for j < kv_len[b] and 0 behind it.  `scores` [B, S] fp32 (None: zeros) may be
     given as `out` too.  To rank positions by the last few tokens only, pass
     those tokens (and their lse): they still stand at the end of the cache.
+    All of `out` is written, so a table much wider than its sequences costs its width.
     Deterministic.  Asynchronous on `stream`; with `out` and `workspace` (uint8,
     attention_mass_workspace_size(...) bytes) given, the call can be captured.
     """
@@ -267,7 +270,8 @@ def evict_slots(scores: torch.Tensor, slot_table: torch.Tensor, kv_len: torch.Te
     first.  Returns an Evicted with tables of min(S, budget) columns.  `out`
     (an Evicted of preallocated tensors) keeps the call free of allocations; its
     scores, slot_table and kv_len may be the inputs themselves, which is the
-    update in place.  Asynchronous on `stream`.
+    update in place.  All of them is written, so a table much wider than its
+    sequences costs its width.  Asynchronous on `stream`.
     """
     lib = _lib.load()
     _need(scores, "scores", torch.float32, 2)
