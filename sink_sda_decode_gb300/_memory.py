@@ -29,8 +29,12 @@ def empties(dev, stream, *specs, results: bool = True) -> list[torch.Tensor]:
 
 def empty(shape, dtype, dev, stream) -> torch.Tensor:
     """One result."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
     return empties(dev, stream, (shape, dtype))[0]
 
 
 def workspace(nbytes: int, dev, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return empties(dev, stream, (nbytes, torch.uint8), results=False)[0]
