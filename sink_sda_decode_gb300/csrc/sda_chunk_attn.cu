@@ -26,7 +26,7 @@
 //
 // What bounds it at D = 512 and R = 64: with three stages of 48 positions, the way of a
 // stage from its load over scores, softmax and PV to its release; neither the tensor
-// pipe (active 38 %) nor DRAM (56 %) is full.  One token of 64 heads over 8 caches of
+// pipe (active 40 %) nor DRAM (60 %) is full.  One token of 64 heads over 8 caches of
 // 16384 to 65536 positions (365 MB): 86 us, where a copy of as many bytes takes 55;
 // about 12 of them are the merge of cut units.
 #include <cuda_bf16.h>

@@ -13,7 +13,7 @@
 // key (32 rows, all of D) and as value (64 rows, half of D); the two rings are freed
 // by different MMAs, so that the keys of the next tile land while the weights of
 // this one are computed.  2048 tokens of 64 heads over 8192 positions, D = 512 (1.92
-// TFLOP): 1.32 to 1.39 ms between runs, about 1400 TFLOP/s, against 2.09 ms with
+// TFLOP): 1.32 to 1.40 ms between runs, about 1400 TFLOP/s, against 2.09 ms with
 // one CTA a tile and tiles multicast to two CTAs.  A tile takes about 1600 cycles, 1365
 // of them MMAs.
 //
