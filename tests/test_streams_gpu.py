@@ -139,3 +139,25 @@ def test_error_word_of_decode_on_another_stream():
             torch.cuda._sleep(200_000_000)
         sda.decode(w.q, w.unified_kv, idx, p, w.attn_sink, w.softmax_scale, workspace=ws, stream=side)
         assert sda.decode_error_flag(ws, side) == word
+
+
+@pytest.mark.parametrize("op", ["attend", "mass", "evict", "decode"])
+def test_captured_on_a_forked_stream(op):
+    """A call without memory of its own on a stream that a capture has forked."""
+    call = path(op) if op == "decode" else paged()[op]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    call(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.fill_(3)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
