@@ -102,9 +102,10 @@ struct Cursor {
 
 // Where worker `worker` begins; called by all THREADS threads of the CTA, which
 // then are past a barrier.  `s_seq` (kFusedSeqs + 1 words) and `scratch` (64 words)
-// are shared memory that is free until then.  *bad: the lengths broke the contract;
-// the merge is launched all the same and goes by the records, so every worker says
-// that it begins in no unit (the workspace may hold an earlier call's, or anything).
+// are shared memory that is free until then.  *bad: the lengths broke the contract.
+// The merge is launched all the same and goes by the records, so the caller then
+// (kCut) records that the worker begins in no unit: the workspace may hold an earlier
+// call's record, or anything.
 template <int THREADS, int R, int TILE>
 __device__ __noinline__ ChunkStart chunk_begin(const ChunkParams& p, int worker, int* s_seq,
                                                   int* scratch, bool* bad) {
