@@ -1341,9 +1341,11 @@ static sda_status append_common(AppendParams p, void* stream, const char* who) {
                            {p.status, 4}};
     for (const Span& w : writes) {
       if (overlaps_tables(g, w.p, w.n)) return SDA_ERR_INVALID_ARG;
-      for (const Span& r : reads)
-        if (!(w.p == p.q_out && r.p == p.q && w.p == r.p) && overlaps(w.p, w.n, r.p, r.n))
-          return SDA_ERR_INVALID_ARG;
+      for (const Span& r : reads) {
+        // (q_out and q themselves: another array at q's address is read by other warps)
+        const bool in_place = &w == &writes[0] && &r == &reads[0] && p.q_out == p.q;
+        if (!in_place && overlaps(w.p, w.n, r.p, r.n)) return SDA_ERR_INVALID_ARG;
+      }
       for (const Span& o : writes)
         if (&o != &w && overlaps(w.p, w.n, o.p, o.n)) return SDA_ERR_INVALID_ARG;
     }

@@ -147,3 +147,15 @@ def test_python_refuses(lib):
     for bad in ((2 ** 31, 1, 1, 64), (1, 1, 1, 64, 2 ** 31), (1, 1, 1, 64, 1, 0), (1, 1, 1, 64, 1, 2 ** 31)):
         with pytest.raises(ValueError):
             sda.chunk_attention_fp8_workspace_size(*bad)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H", [1, 16])
+@pytest.mark.parametrize("name", ["kv", "q_w", "kv_w", "cos", "sin"])
+def test_in_place_is_for_queries_alone(lib, no_gpu, name, H, fp8):
+    """q_out = q is taken, but not with another array that is read at the same address: rows of
+    it are read by other warps while q's are overwritten."""
+    q = APPEND["q"]
+    assert append(lib, fp8, H=H, q_out=q) not in (OK, INVALID)
+    assert append(lib, fp8, H=H, q_out=q, **{name: q}) == INVALID
+    assert append(lib, fp8, H=H, **{name: q}) not in (OK, INVALID)  # read alone: any address
