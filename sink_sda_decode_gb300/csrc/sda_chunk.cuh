@@ -224,6 +224,14 @@ __device__ inline long long scan_exclusive(long long v, long long* warp_sums, lo
   return r;
 }
 
+// l 2^d, d <= 0.  2^d alone is 0 below 2^-126, and a sum l of weights far larger than that
+// small where their reference counts scales (sda_chunk_fp8.cuh).
+__device__ __forceinline__ float times_exp2(float l, float d) {
+  if (d >= -126.f) return l * ex2_approx(d);
+  const float h = ex2_approx(0.5f * d);
+  return l * h * h;
+}
+
 // Last index i in [0, n) with a[i] <= x; a non-decreasing, a[0] <= x.
 __device__ __forceinline__ int last_le(const int* a, int n, int x) {
   int lo = 0, hi = n;

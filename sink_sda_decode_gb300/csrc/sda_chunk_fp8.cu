@@ -585,12 +585,12 @@ chunk_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q, const ChunkFp8Param
           float alphaA = 1.f, alphaB = 1.f;
           if (eA > mA + kHeadroom) {
             alphaA = ex2_approx(mA - eA);  // 0 when there was no score
-            lA *= alphaA;
+            lA = times_exp2(lA, mA - eA);
             mA = eA;
           }
           if (eB > mB + kHeadroom) {
             alphaB = ex2_approx(mB - eB);
-            lB *= alphaB;
+            lB = times_exp2(lB, mB - eB);
             mB = eB;
           }
           weights(std::true_type{});
@@ -659,7 +659,7 @@ chunk_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q, const ChunkFp8Param
               float lse = M * kLn2;
               if (M != -INFINITY && ms != INFINITY) {
                 const float a = m == -INFINITY ? 0.f : ex2_approx(m - M);
-                const float den = fmaf(l, a, ex2_approx(ms - M));
+                const float den = denominator(l, m - M, ex2_approx(ms - M));
                 f = a / den / kWeightUnit;
                 lse = (M + log2f(den)) * kLn2;
               }

@@ -70,6 +70,11 @@ __device__ __forceinline__ float scale_log(float su) {
   return fmaxf(y - 3.f, kLeastLog);
 }
 
+// l 2^d + sink, d <= 0 (-inf: the row has no score, and l is 0).
+__device__ __forceinline__ float denominator(float l, float d, float sink) {
+  return d >= -126.f ? fmaf(l, ex2_approx(d), sink) : times_exp2(l, d) + sink;
+}
+
 // warp_wait in less code: these kernels wait at some forty places, and the instructions of
 // all roles have to stay in the instruction cache (a pair kernel of 205 KB had 30 % of its
 // warps waiting for instructions).  The first try has no time to sleep: 26 cycles where the

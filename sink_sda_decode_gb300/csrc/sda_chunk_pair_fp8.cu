@@ -822,7 +822,7 @@ chunk_pair_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,
               float alpha = 1.f;
               if (t > m[i4] + kHeadroom) {
                 alpha = ex2_approx(m[i4] - t);  // 0 when there was no score
-                l[i4] *= alpha;
+                l[i4] = times_exp2(l[i4], m[i4] - t);
                 m[i4] = t;
               }
               if (i > i0 && tq == 0 && part == 0) {  // both CTAs hold O^T of this row
@@ -908,7 +908,7 @@ chunk_pair_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,
             float lse = M * kLn2;
             if (M != -INFINITY && ms != INFINITY) {
               const float a = mr == -INFINITY ? 0.f : ex2_approx(mr - M);
-              const float den = fmaf(lr, a, ex2_approx(ms - M));
+              const float den = denominator(lr, mr - M, ex2_approx(ms - M));
               f = a / den / kWeightUnit;
               lse = (M + log2f(den)) * kLn2;
             }

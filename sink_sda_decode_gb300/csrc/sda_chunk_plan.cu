@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) chunk_combine_kernel(
     const float2 ml = i0 == 0 ? ml0 : ml_of(i0 + lane);
     // (a piece whose rows are all masked has m = -inf, l = 0 and weight 0)
     const float w = i0 + lane < np ? ex2_approx(ml.x - M) : 0.f;
-    den += ml.x == -INFINITY ? ml.y : ml.y * w;
+    den += ml.x == -INFINITY ? ml.y : times_exp2(ml.y, ml.x - M);
     const int n = min(32, np - i0);
     for (int j0 = 0; j0 < n; j0 += P) {
       float v[P][C::kPer];
