@@ -768,6 +768,10 @@ chunk_pair_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,
               const uint64_t pr = f2_pack(a0, a1);
               both[i4] = f2_add(both[i4], pr);
               f2_unpack(f2_mul(pr, sj[rep]), a0, a1);
+              if constexpr (decltype(masked)::value) {  // (0 x a scale that is no number)
+                a0 = (see >> (8 * i4 + 2 * rep)) & 1u ? a0 : 0.f;
+                a1 = (see >> (8 * i4 + 2 * rep + 1)) & 1u ? a1 : 0.f;
+              }
               pk[i4][rep] = pack_f16(a0, a1);
               top = f16_top(top, pk[i4][rep]);
             });
