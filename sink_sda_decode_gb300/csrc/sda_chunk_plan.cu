@@ -230,9 +230,9 @@ ChunkLayout chunk_layout(const ChunkGeom& g, int num_sms, bool fp8) {
     L.grid /= 2;
   }
   L.tile = fp8 ? (L.pair ? 128 : 64) : chunk_tile(L.R, g.D);
-  // Where no unit can have more than kWholeTiles tiles (short tables, or a window)
-  // units are not cut: a merge takes as long as about four tiles.
-  constexpr int64_t kWholeTiles = 8;
+  // Where no unit can have more than `whole` tiles (short tables, or a window) units are not
+  // cut: a merge takes as long as about four tiles of up to 64 positions.  (Four of 128.)
+  const int64_t whole = L.tile == 128 ? 4 : 8;
   const int64_t S = (int64_t)g.max_blocks * g.k_per_block;
   int64_t most = (S + L.tile - 1) / L.tile;
   if (g.window > 0) {
@@ -242,7 +242,7 @@ ChunkLayout chunk_layout(const ChunkGeom& g, int num_sms, bool fp8) {
   }
   L.mode = kPlanned;
   if (g.B <= kFusedSeqs) {
-    if (most * L.tile <= kWholeTiles * 64) L.mode = kWhole;
+    if (most <= whole) L.mode = kWhole;
     else if (rows / L.R + g.B <= kFusedUnits) L.mode = kCut;
   }
   size_t off = kErrorWords + kErrorBytes;

@@ -263,3 +263,17 @@ def test_lengths_near_two_billion_are_refused(H, B):
                         workspace=ws)
     assert sda.paged_error_flag(ws) == 2
     assert bool((out == 3.0).all())
+
+
+@pytest.mark.parametrize("columns", [385, 430, 432, 433, 480])
+def test_tables_of_more_than_eight_tiles_share_the_work_alike(columns):
+    """64 rows at D = 512 take tiles of 48: from 385 positions on units are cut as in wide
+    tables, to the bit."""
+    n = [columns - 3, 200]
+    c = Case(80, m=[1, 1], n=n, H=64, D=512, K=1, columns=columns)
+    out, lse = check(c)
+    wide = torch.full((2, 4000), -7, dtype=torch.int32, device="cuda")
+    wide[:, :columns] = c.table
+    c.table = wide
+    again, l2 = c.attend(sda)
+    assert torch.equal(out, again) and torch.equal(lse, l2)
