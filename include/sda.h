@@ -580,7 +580,7 @@ sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64
  *   positions not bounded by max_pos); T * (H + 1) < 2^31; eps >= 0 finite (on the host)
  *   q_out       [T, H, D] bf16; may be q itself
  * Every row x of a token at 0 <= p < max_pos becomes, in fp32, y as
- * sda_qk_norm_rope_swa_store has it; q_out = y and the KV row's y goes to its pool row,
+ * sda_qk_norm_rope_swa_store has it, to the bit; q_out = y and the KV row's y goes to its pool row,
  * rounded to nearest even bf16.  A token at another position (more tokens than positions
  * among them) gets q_out = 0 and stores nothing.  Rows of q_out outside [q_indptr[0],
  * q_indptr[B]), and of sequences whose lengths break the contract, are not written.

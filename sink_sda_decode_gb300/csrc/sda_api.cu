@@ -1382,7 +1382,7 @@ static AppendParams append_params(const void* q, const void* kv, const void* q_n
   p.R = rope_dim;
   p.max_pos = max_pos;
   p.eps = eps;
-  p.inv_d = 1.f / static_cast<float>(D);
+  p.inv_d = (D & (D - 1)) == 0 ? 1.f / static_cast<float>(D) : 0.f;
   p.q_out = static_cast<uint16_t*>(H > 0 ? q_out : nullptr);
   p.status = status;
   return p;

@@ -18,9 +18,10 @@
 // loads in flight.  8-bit blocks are CTAs of their own, ahead of the others in the grid:
 // the CTA that holds a block's first new token finds its scale over all new rows of it,
 // then writes them.
-// What bounds it: DRAM (4 bytes an element of q), and close to it the instructions, some 270 a
-// row of 512.  2048 tokens of 64 heads, D = 512, bf16 cache (273 MB): 51 us, 5.4 TB/s; with 370
-// instructions a row (weights unpacked anew, registers spilled) it took 65.  24 thousand rows without
+// What bounds it: DRAM (4 bytes an element of q), and close to it the instructions, some 250 a
+// row of 512.  2048 tokens of 64 heads, D = 512, bf16 cache (273 MB): 51 us, 5.3 TB/s; with 370
+// instructions a row (weights unpacked anew, registers spilled) it took 65, with places found
+// anew for every row 54.  24 thousand rows without
 // queries into codes: 19 us, two passes over each block's rows, 3 to 4 blocks a CTA.  Calls of few rows:
 // the chain of a launch, the search for the sequence, a row's load and its store (6 us).
 #include "sda_append.cuh"
@@ -116,8 +117,9 @@ __device__ __forceinline__ void load_weights(const uint16_t* w, int chunks, int 
   }
 }
 
-// A row's values in place; cos_row and sin_row are its position's.  1 / sqrt is rsqrtf,
-// within 2 units of the last place.
+// A row's values in place; cos_row and sin_row are its position's.  Every operation is rounded
+// as in sda_store.cu, so that a row has the same bits in both stores: the mean is a division
+// (inv_d: exact) and the inverse root an IEEE root and division.
 template <int CPL>
 __device__ __forceinline__ void row_values(const AppendParams& p, const uint4 (&w)[CPL], bool norm,
                                            const float* cos_row, const float* sin_row, int lane,
@@ -138,7 +140,8 @@ __device__ __forceinline__ void row_values(const AppendParams& p, const uint4 (&
     float ss = even + odd;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+    const float mean = p.inv_d != 0.f ? ss * p.inv_d : ss / (float)p.g.D;
+    const float inv = 1.f / sqrtf(__fadd_rn(mean, p.eps));
     const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
@@ -183,40 +186,41 @@ __device__ __forceinline__ int64_t pool_row(const AppendParams& p, int b, int po
 // Rows of q, and of kv into a bf16 pool: `rpt` rows a token.
 template <int CPL, bool FP8>
 __device__ __forceinline__ void plain_rows(const AppendParams& p, int64_t worker, int64_t workers) {
-  const int lane = threadIdx.x & 31, chunks = p.g.D >> 3;
+  const int lane = threadIdx.x & 31, D = p.g.D, chunks = D >> 3;
   const int H = p.g.H, rpt = H + (FP8 ? 0 : 1);
   const int64_t rows = (int64_t)p.g.T * rpt, each = (rows + workers - 1) / workers;
-  int64_t r = worker * each;
-  const int64_t r1 = min(r + each, rows);
-  if (r >= r1) return;
-  int t = (int)(r / rpt), h = (int)(r - (int64_t)t * rpt);
-  auto src_of = [&](int tt, int hh) {
-    return hh < H ? p.q + ((size_t)tt * H + hh) * p.g.D : p.kv + (size_t)tt * p.g.D;
-  };
+  const int64_t r0 = worker * each;
+  if (r0 >= rows) return;
+  int left = (int)min(each, rows - r0), t = (int)(r0 / rpt), h = (int)(r0 - (int64_t)t * rpt);
+  size_t at_q = ((size_t)t * H + h) * D;  // of the row, or of the next of q behind a row of kv
   uint4 x[CPL], wq[CPL];
-  load_row<CPL>(src_of(t, h), chunks, lane, x);
+  load_row<CPL>(h < H ? p.q + at_q : p.kv + (size_t)t * D, chunks, lane, x);
   load_weights<CPL>(p.q_w, chunks, lane, wq);
   const int half = p.R >> 1;
   Place at;
   at.init(p, t);
   bool live = at.live(p);
   int pos = live ? at.pos() : 0;
+  bool ok = position_ok(p, pos);
   const float *cos_row = p.cos_cache + (size_t)pos * half, *sin_row = p.sin_cache + (size_t)pos * half;
-  for (; r < r1; ++r) {
-    int nt = t, nh = h + 1;
-    if (nh == rpt) nh = 0, ++nt;
+  for (;; --left) {
+    const bool is_kv = !FP8 && h == H;
+    uint16_t* dst = p.q_out + at_q;
+    if (!is_kv) at_q += D;
+    int nh = h + 1;
+    if (nh == rpt) nh = 0;
     float f[CPL][8];
 #pragma unroll
     for (int j = 0; j < CPL; ++j) unpack8(x[j], f[j]);
-    if (r + 1 < r1) load_row<CPL>(src_of(nt, nh), chunks, lane, x);
+    if (left > 1)
+      load_row<CPL>(FP8 || nh < H ? p.q + at_q : p.kv + (size_t)(t + (nh == 0)) * D, chunks, lane, x);
     // (rows of tokens outside every sequence, or in one whose lengths make no sense, stay as they are)
     if (live) {
-      const bool ok = position_ok(p, pos), is_kv = h == H;
-      uint16_t* dst = is_kv ? nullptr : p.q_out + ((size_t)t * H + h) * p.g.D;
-      if (!FP8 && is_kv) {
+      if (is_kv) {
+        dst = nullptr;
         if (ok) {
           const int64_t row = pool_row(p, at.b, pos);
-          if (row >= 0) dst = p.pool + row * p.g.D;
+          if (row >= 0) dst = p.pool + row * D;
           else if (lane == 0) report(p, 2);
         } else if (lane == 0) {
           report(p, 1);
@@ -237,14 +241,16 @@ __device__ __forceinline__ void plain_rows(const AppendParams& p, int64_t worker
         }
       }
     }
-    if (nt != t && r + 1 < r1) {
-      at.to(p, nt);
+    if (left == 1) return;
+    h = nh;
+    if (h == 0) {
+      at.to(p, ++t);
       live = at.live(p);
       pos = live ? at.pos() : 0;
+      ok = position_ok(p, pos);
       cos_row = p.cos_cache + (size_t)pos * half;
       sin_row = p.sin_cache + (size_t)pos * half;
     }
-    t = nt, h = nh;
   }
 }
 

@@ -16,7 +16,7 @@ struct AppendParams {
   const float* sin_cache;
   ChunkGeom g;                // (window, first and the division by H are not used)
   int R, max_pos;
-  float eps, inv_d;           // inv_d = 1 / D
+  float eps, inv_d;           // inv_d = 1 / D, 0 where that is not exact
   uint16_t* q_out;            // [T, H, D] bf16 (may be q itself)
   uint16_t* pool;             // [total_pages, D] bf16, or null
   uint8_t* codes;             // [total_pages, D] E4M3, or null

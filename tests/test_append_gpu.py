@@ -398,3 +398,24 @@ def test_step_by_step_is_the_cache_that_attention_reads():
         c.of = scales.cpu().double()[torch.arange(codes.shape[0]) // K]
         c.worth()
         check8(sda, c)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,rope", [(16, 16), (64, 32), (128, 64), (192, 8), (256, 256), (512, 64), (528, 64), (1024, 1024)])
+def test_same_bits_as_the_ring_store(D, rope, fp8):
+    """A row is the same in both stores (a block of one row has the ring's scale)."""
+    T = 300
+    a = Append(70 + D, m=[T], n=[T], H=5, D=D, K=1, rope=rope, fp8=fp8).cuda()
+    q, _ = a.call()
+    d = a.d
+    ring = torch.zeros(T, D, dtype=d["pool"].dtype, device="cuda")
+    scale = torch.zeros(T, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    q2, _ = sda.qk_norm_rope_swa_store(d["q"], d["kv"], d["q_w"], d["kv_w"], d["cos"], d["sin"], pos,
+                                       torch.zeros_like(pos), eps=1e-6, win=T, swa_pages=T,
+                                       **(dict(kv_fp8=ring, kv_scale=scale) if fp8 else dict(unified_kv=ring)))
+    rows = d["table"][0, :T].long()
+    assert torch.equal(q.view(torch.int16), q2.view(torch.int16))
+    assert torch.equal(d["pool"][rows], ring)
+    if fp8:
+        assert torch.equal(d["scale"][rows], scale)
