@@ -419,3 +419,59 @@ def test_same_bits_as_the_ring_store(D, rope, fp8):
     assert torch.equal(d["pool"][rows], ring)
     if fp8:
         assert torch.equal(d["scale"][rows], scale)
+
+
+def same_cache(a, b):
+    return torch.equal(a["pool"], b["pool"]) and torch.equal(a["scale"], b["scale"])
+
+
+def test_scales_of_a_captured_call():
+    """A replay with other rows, lengths and scales writes the scales, too."""
+    a = Append(24, m=[1, 4, 40], n=[32, 48, 96], H=2, D=512).cuda()
+    out, st = torch.empty_like(a.d["q"]), torch.empty(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        a.call(q_out=out, status=st)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.call(q_out=out, status=st)
+    for seed, n, size in ((25, [18, 37, 81], 0.01), (26, [17, 40, 90], 50.0)):
+        b = Append(seed, m=[1, 4, 40], n=n, H=2, D=512, size=size, norm=False)
+        b.kv_w, b.q_w = a.kv_w, a.q_w
+        for k in ("kv", "q", "pool", "scale"):
+            a.d[k].copy_(getattr(b, k))
+        a.d["table"].fill_(-7)
+        a.d["table"][:, :b.table.shape[1]] = b.table.cuda()
+        a.d["n"].copy_(torch.tensor(n, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        b.cuda()
+        b.d["cos"], b.d["sin"] = a.d["cos"], a.d["sin"]
+        want, ws = b.call()
+        assert torch.equal(out, want) and int(st.item()) == int(ws.item()) == 0
+        assert same_cache(a.d, b.d) and not torch.equal(b.d["scale"].cpu(), b.scale)
+
+
+def test_scales_on_another_stream_and_at_a_large_base():
+    a, b, c = (Append(27, m=[3, 40], n=[20, 70], H=1, D=512).cuda() for _ in range(3))
+    a.call()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    b.call(stream=s)
+    s.synchronize()
+    assert same_cache(a.d, b.d)
+    base = (1 << 32) // 512 + 1000
+    pool = torch.zeros(base + c.pool.shape[0], 512, dtype=torch.uint8, device="cuda")
+    pool[base:] = c.d["pool"]
+    c.d["pool"], c.base = pool, base
+    c.call()
+    assert torch.equal(pool[base:], a.d["pool"]) and torch.equal(c.d["scale"], a.d["scale"])
+    assert not torch.equal(a.d["scale"].cpu(), a.scale)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_without_queries_of_many_tokens(fp8):
+    """A warp's rows are then of one token each."""
+    check(Append(28, m=[5000, 0, 3, 4100], n=[5000, 9, 300, 4500], H=0, D=64, K=16, rope=32, fp8=fp8, trail=7))
+    check(Append(29, m=[1000, 1000], n=[1500, 1000], H=3, D=64, K=16, rope=32, fp8=fp8, lead=5))
