@@ -393,6 +393,7 @@ chunk_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q, const ChunkFp8Param
     // tile's positions: thread t holds rows hA = 16 q4 + t / 4 and hB = hA + 8 at
     // the positions kPos hc + 8 rep + 2 (t % 4) + {0, 1}.
     constexpr int kPos = kTile / 2, kReps = kPos / 8, kE = 4 * kReps;
+    static_assert(kReps == 4, "loads and stores of 32 positions");
     const int q4 = warp & 3, hc = warp >> 2, st = threadIdx.x, tq = lane & 3;
     const int hA = q4 * 16 + (lane >> 2), hB = hA + 8;
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
@@ -454,18 +455,8 @@ chunk_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q, const ChunkFp8Param
         {
           const uint32_t ta = tmem + lane_base + s * 64 + kPos * hc;
           uint32_t v[kE];
-          if constexpr (kReps == 4) {
-            tmem_ld_16x256b_x4(ta, v);
-            tmem_wait_ld();
-          } else {
-            static_assert(kReps == 3, "24 positions");
-            uint32_t v2[8], v1[4];
-            tmem_ld_16x256b_x2(ta, v2);
-            tmem_ld_16x256b_x1(ta + 16, v1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < kE; ++e) v[e] = e < 8 ? v2[e] : v1[e - 8];
-          }
+          tmem_ld_16x256b_x4(ta, v);
+          tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < kE; ++e) x[e] = __uint_as_float(v[e]) * sj[2 * (e >> 2) + (e & 1)];
         }
@@ -496,7 +487,7 @@ chunk_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q, const ChunkFp8Param
                                               (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4));
             };
             uint32_t bad = 0;
-            for (int ch = part; ch < D / 8 && r < kTile; ch += 4) {
+            for (int ch = part; ch < D / 8; ch += 4) {
               const uint4 w = *chunk(ch);
               bad |= f16_bad(w.x) || f16_bad(w.y) || f16_bad(w.z) || f16_bad(w.w);
             }
@@ -537,15 +528,8 @@ chunk_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q, const ChunkFp8Param
             pb[rep] = pack_f16(w[2], w[3]);
           }
           if (held) {
-            if constexpr (kReps == 4) {
-              stmatrix_x4(pchunk(lane >> 3), pa[0], pa[1], pa[2], pa[3]);
-              stmatrix_x4(pchunk(lane >> 3) + 1024, pb[0], pb[1], pb[2], pb[3]);
-            } else {
-              stmatrix_x2(pchunk((lane >> 3) & 1), pa[0], pa[1]);
-              stmatrix_x1(pchunk(2), pa[2]);
-              stmatrix_x2(pchunk((lane >> 3) & 1) + 1024, pb[0], pb[1]);
-              stmatrix_x1(pchunk(2) + 1024, pb[2]);
-            }
+            stmatrix_x4(pchunk(lane >> 3), pa[0], pa[1], pa[2], pa[3]);
+            stmatrix_x4(pchunk(lane >> 3) + 1024, pb[0], pb[1], pb[2], pb[3]);
           }
           return top > kWeightTop || fmaxf(sumA, sumB) > kSumTop;
         };

@@ -35,8 +35,8 @@ struct SpreadParams {
 };
 
 // Tiles are read whole, so what lies between the last row and the end of its tile is zeros.
-// A warp takes 8 rows.  What bounds it: a read and two writes of L2 a code, 11 MB for the
-// prompt above.
+// A warp takes 8 rows.  What bounds it: a read and two writes of L2 a code, 12.6 MB for
+// the prompt above.
 template <int D>
 __global__ void __launch_bounds__(256) spread_kernel(const SpreadParams p) {
   constexpr int kL = D / 16, kPer = 32 / kL;  // lanes a row, rows a load
