@@ -586,7 +586,8 @@ sda_status sda_evict_slots(const float* scores, const int32_t* slot_table, int64
  * q_indptr[B]), and of sequences whose lengths break the contract, are not written.
  * *status (device int32, overwritten): bits 1 (a token without a position in [0,
  * max_pos)), 2 (a row's table entry points outside the pool: not stored), 4 (a sequence
- * whose q_indptr or kv_len breaks chunk attention's contract: left out).
+ * whose q_indptr or kv_len breaks chunk attention's contract: left out; where q_indptr
+ * descends anywhere, tokens of other sequences may be left out, too).
  * The rows written are the only ones touched; two sequences may share blocks that
  * neither writes.  What is written overlaps neither what is read (q_out = q apart) nor
  * what else is written (SDA_ERR_INVALID_ARG).  One launch, and a clear of *status with

@@ -51,9 +51,11 @@ def append_rows(kv: torch.Tensor, cos_cache: torch.Tensor, sin_cache: torch.Tens
     scale is the least power of two that its rows need; where new rows need a larger one
     the codes that are there are rounded to it.  Returns (q_out or None, status [1]
     int32: bits 1 a token without a position in the caches, 2 a table entry outside the
-    pool, 4 lengths outside the contract).
+    pool, 4 lengths outside the contract: such a sequence is left out, and where q_indptr
+    descends others may be, too).
 
-    D a multiple of 16 up to 1024.  A block that is written belongs to one sequence.
+    D a multiple of 16 up to 1024, half one of 4 up to D / 2.  A block that is written
+    belongs to one sequence.
     Asynchronous on `stream`; with q_out and status given the call allocates nothing and
     can be captured into a CUDA graph.
     """
@@ -74,6 +76,8 @@ def append_rows(kv: torch.Tensor, cos_cache: torch.Tensor, sin_cache: torch.Tens
     if angles != sin_cache.shape:
         raise ValueError("cos_cache and sin_cache must have the same shape")
     max_pos, half = angles
+    if half % 4 or 2 * half > D:
+        raise ValueError("cos_cache must have a multiple of 4 columns, at most D / 2")
     if (unified_kv is None) == (kv_fp8 is None):
         raise ValueError("pass exactly one of unified_kv (bf16 pool) or kv_fp8 + block_scale")
     K, base = _int32(k_per_block, "k_per_block", 1), int(base)

@@ -475,3 +475,31 @@ def test_rows_without_queries_of_many_tokens(fp8):
     """A warp's rows are then of one token each."""
     check(Append(28, m=[5000, 0, 3, 4100], n=[5000, 9, 300, 4500], H=0, D=64, K=16, rope=32, fp8=fp8, trail=7))
     check(Append(29, m=[1000, 1000], n=[1500, 1000], H=3, D=64, K=16, rope=32, fp8=fp8, lead=5))
+
+
+def test_refusals_say_what_is_wrong():
+    for rope, D in ((4, 64), (20, 64), (72, 64)):
+        a = Append(30, m=[2], n=[9], H=0, D=D, rope=rope).cuda()
+        before = a.d["pool"].clone()
+        with pytest.raises(ValueError, match="multiple of 4 columns"):
+            a.call()
+        assert torch.equal(a.d["pool"], before)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ptr", [[0, 100, 3, 5], [0, 4, 3, 3], [0, 3, 2, 5]])
+def test_descending_bounds_touch_nothing_else(ptr, fp8):
+    """Sequences beside a bad one are stored or left out; the rest of the pool stays."""
+    a = Append(31, m=[3, 1, 1], n=[20, 30, 40], H=2, fp8=fp8).cuda()
+    a.d["ptr"] = torch.tensor(ptr, dtype=torch.int32, device="cuda")
+    _, st = a.call()
+    assert int(st.item()) == 4
+    may = torch.zeros(a.pool.shape[0], dtype=torch.bool)
+    for b in range(3):
+        if 0 <= ptr[b] <= ptr[b + 1] <= 5:
+            n = a.n[b]
+            blocks = range((n - (ptr[b + 1] - ptr[b])) // a.K, -(-n // a.K))  # (codes of a block may be rounded again)
+            for j in blocks:
+                first = int(a.table[b, j]) * a.K
+                may[first:first + a.K] = True
+    assert torch.equal(a.d["pool"].cpu()[~may], a.pool[~may])
