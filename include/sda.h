@@ -632,7 +632,7 @@ sda_status sda_append_rows_fp8(const void* q, const void* kv, const void* q_norm
  * tables, if these are 2 GB at most.  That is the size that the query gives with the
  * tables' width; with max_blocks = 0 it gives the least that a call takes, and a call with
  * less than the whole does without (a prompt chunk of 2048 tokens of 64 heads over 8192
- * positions then takes 1.60 ms in place of 1.31).
+ * positions then takes 1.60 ms in place of 1.31, with weights of f16 in place of bf16).
  * Numerics: codes and q enter the MMAs exactly (q's rows times a power of two;
  * elements of q below 2^-13 of their row's largest may be off by 2^-21 of that), scales
  * multiply scores and weights in fp32, weights are rounded to f16 (2^-11 of themselves,
