@@ -638,8 +638,10 @@ sda_status sda_append_rows_fp8(const void* q, const void* kv, const void* q_norm
  * multiply scores and weights in fp32, weights are rounded to f16 (2^-11 of themselves,
  * or 2^-28 of the row's largest weight times scale), with rows side by side to bf16 (2^-8
  * of themselves; a row whose weights all lie below 2^-86 of its sink's may be 0); lse and
- * the denominator are fp32 (exponents up to log2 of the smallest scale round: lse is off
- * by up to 2^-20, by 2^-18 where every scale that a row sees is 0 or near 2^-90).
+ * the denominator are fp32: lse is off by up to 2^-20 (1 + |lse|), beside its scores' own
+ * rounding, and where the reference counts a small scale s (not with rows side by side)
+ * exponents as large as log2 s round, too: by up to 2^-22 |log2 s| more, s the largest that
+ * the row sees, 2^-90 if that is smaller or 0.
  */
 sda_status sda_chunk_attention_fp8_workspace_size(int B, int T, int H, int D, int max_blocks,
                                                   int k_per_block, size_t* bytes);
