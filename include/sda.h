@@ -610,7 +610,9 @@ sda_status sda_append_rows(const void* q, const void* kv, const void* q_norm_w, 
  * of its sequence keeps its scale, or takes 2^e where that is larger: its codes then
  * become code * old / new; one that held none takes 2^e whatever block_scale says.  Codes
  * are rounded to nearest even; an infinity or NaN becomes the NaN code.  A block that is
- * written belongs to one sequence.
+ * written belongs to one sequence, and one CTA writes its new rows: blocks of some hundred
+ * rows at most are meant (8192 rows of 512: 10 us in blocks of 16, 18 of 64, 52 of 256, 194
+ * of 1024, 1505 in one of 8192; 41 in blocks of one).
  */
 sda_status sda_append_rows_fp8(const void* q, const void* kv, const void* q_norm_w, const void* kv_norm_w,
                                const float* cos_cache, const float* sin_cache, int max_pos,
@@ -639,9 +641,9 @@ sda_status sda_append_rows_fp8(const void* q, const void* kv, const void* q_norm
  * or 2^-28 of the row's largest weight times scale), with rows side by side to bf16 (2^-8
  * of themselves; a row whose weights all lie below 2^-86 of its sink's may be 0); lse and
  * the denominator are fp32: lse is off by up to 2^-20 (1 + |lse|), beside its scores' own
- * rounding, and where the reference counts a small scale s (not with rows side by side)
- * exponents as large as log2 s round, too: by up to 2^-22 |log2 s| more, s the largest that
- * the row sees, 2^-90 if that is smaller or 0.
+ * rounding.  Where the reference counts scales (not with rows side by side) exponents as
+ * large as log2 of a scale round, too: by up to 2^-22 |log2 s| more, for the scale s that
+ * the row sees whose |log2| is largest (2^-90 if that is smaller or 0).
  */
 sda_status sda_chunk_attention_fp8_workspace_size(int B, int T, int H, int D, int max_blocks,
                                                   int k_per_block, size_t* bytes);

@@ -22,7 +22,7 @@
 // row of 512.  2048 tokens of 64 heads, D = 512, bf16 cache (273 MB): 51 us, 5.3 TB/s; with 370
 // instructions a row (weights unpacked anew, registers spilled) it took 65, with places found
 // anew for every row 54.  24 thousand rows without
-// queries into codes: 19 us, two passes over each block's rows, 3 to 4 blocks a CTA.  Calls of few rows:
+// queries into codes: 20 us, two passes over each block's rows, 3 to 4 blocks a CTA.  Calls of few rows:
 // the chain of a launch, the search for the sequence, a row's load and its store (6 us).
 #include "sda_append.cuh"
 #include "sda_rows.cuh"

@@ -222,8 +222,8 @@ ChunkLayout chunk_layout(const ChunkGeom& g, int num_sms, bool fp8) {
   L.grid = num_sms < kMaxPlanGrid ? num_sms : kMaxPlanGrid;
   // With more than 128 rows a sequence on average (64 over an 8-bit cache: one token of 128
   // heads over 32 caches of 4600 positions 74.6 us against 88.1 with one CTA a tile, of 96
-  // heads 66.7 against 86.1; in single slots two tokens of 64 heads 75.7 against 69.7), pairs of CTAs
-  // take units of 128 rows.
+  // heads 66.7 against 86.1), pairs of CTAs take units of 128 rows.  (In single slots two tokens of
+  // 64 heads take 75.7 against 69.7 so; the layout's sizes do not go by the size of blocks.)
   L.pair = g.D >= 256 && rows > (int64_t)(fp8 ? 64 : 128) * g.B;
   if (L.pair) {
     L.R = 128;
@@ -231,7 +231,9 @@ ChunkLayout chunk_layout(const ChunkGeom& g, int num_sms, bool fp8) {
   }
   L.tile = fp8 ? (L.pair ? 128 : 64) : chunk_tile(L.R, g.D);
   // Where no unit can have more than `whole` tiles (short tables, or a window) units are not
-  // cut: a merge takes as long as about four tiles of up to 64 positions.  (Four of 128.)
+  // cut: a merge takes as long as about four tiles of up to 64 positions.  (Four of 128: over
+  // 8-bit caches of 500 positions 64 sequences of 128 heads take 29.9 us whole and 36.0 cut, 4 take
+  // 25.2 and 24.7; of 64 heads, tiles of 64, 26.7 and 39.6, 24.8 and 21.1.)
   const int64_t whole = L.tile == 128 ? 4 : 8;
   const int64_t S = (int64_t)g.max_blocks * g.k_per_block;
   int64_t most = (S + L.tile - 1) / L.tile;
