@@ -79,13 +79,22 @@ struct Place {
     b = sequence_of(p.g.q_indptr, p.g.B, t);
     if (b >= 0) load(p);
   }
+  // On to the next sequence, or, where that has no token behind t either, behind all that have
+  // none (a padded batch may hold thousands: one by one they took 770 us); B behind the last.
+  __device__ __forceinline__ void next(const AppendParams& p) {
+    const int after = ++b;
+    if (b >= p.g.B) return;
+    load(p);
+    if (t < q1) return;
+    b = sequence_of(p.g.q_indptr, p.g.B, t);
+    if (b <= after) b = after;
+    else load(p);
+  }
   // token t' > t; b = -1 before the first sequence, B behind the last
   __device__ __forceinline__ void to(const AppendParams& p, int t_) {
     t = t_;
     if (b < 0) return init(p, t_);
-    while (b < p.g.B && t >= __ldg(p.g.q_indptr + b + 1)) {
-      if (++b < p.g.B) load(p);
-    }
+    while (b < p.g.B && t >= q1) next(p);
   }
   // Whether the token is one of a sequence whose lengths make sense.
   __device__ __forceinline__ bool live(const AppendParams& p) const {
@@ -398,10 +407,8 @@ __device__ __forceinline__ void code_blocks(const AppendParams& p, int t, int t1
   }
   while (at.t < t1 && at.b < p.g.B) {
     if (at.bad || at.t >= at.q1) {
-      if (++at.b < p.g.B) {
-        at.load(p);
-        at.t = max(at.t, at.q0);
-      }
+      at.next(p);
+      if (at.b < p.g.B) at.t = max(at.t, at.q0);
       continue;
     }
     int pos = at.pos();
