@@ -429,6 +429,7 @@ def test_scales_of_a_captured_call():
     """A replay with other rows, lengths and scales writes the scales, too."""
     a = Append(24, m=[1, 4, 40], n=[32, 48, 96], H=2, D=512).cuda()
     out, st = torch.empty_like(a.d["q"]), torch.empty(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
         a.call(q_out=out, status=st)
@@ -506,6 +507,7 @@ def test_descending_bounds_touch_nothing_else(ptr, fp8):
 
 
 def replayed(f, n=10):
+    torch.cuda.synchronize()  # (the other stream comes after this one's work)
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
         f()
